@@ -25,6 +25,15 @@
  *              D_row = prob * 2 * C * relu(G), dprob = sum_n C relu(G)^2,
  *              plus the per-expert Amax of section "Shapes".
  *
+ * and, defined here, what stands before and after them in a training step:
+ *
+ *   gg_route, gg_route_bwd   the router: top-k choice, weights, tokens per
+ *              expert, balance loss; the gradient of its logits.
+ *   gg_plan, gg_permute, gg_combine, gg_combine_bwd   tokens to the rows of
+ *              the grouped GEMMs, and back.
+ *   gg_grad_norm, gg_grad_clip   the 2-norm over many gradients, and
+ *              clipping by it.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Pointers are device pointers unless marked [host].  Every buffer is
@@ -93,6 +102,9 @@ typedef enum {
 /* GG_DSITUGLU is defined for the block-scaled contract only (gg_dglu_mx). */
 typedef enum { GG_DSWIGLU = 0, GG_DGEGLU = 1, GG_DSITUGLU = 2 } gg_act;
 
+/* What gg_route makes of a logit. */
+typedef enum { GG_SOFTMAX = 0, GG_SIGMOID = 1 } gg_score;
+
 enum {
     /* dGLU: in each 64-column pair of C and D the gate block comes first.
      * Default (flag clear): the input block comes first, as the dGLU page's
@@ -129,7 +141,10 @@ enum {
      * ("Additional Type Constraints").  The dgrad entries take it with an
      * FP8 d_dtype only (the same section pairs FP8 operands with FP8
      * outputs), else GG_ERR_UNSUPPORTED; gg_wgrad_mx with any wgrad_dtype. */
-    GG_FLAG_AB_E5M2 = 32u
+    GG_FLAG_AB_E5M2 = 32u,
+    /* gg_route, gg_route_bwd: the chosen experts' weights are divided by
+     * their sum. */
+    GG_FLAG_NORMALIZE = 64u
 };
 
 /*
@@ -165,7 +180,9 @@ enum {
     GG_DEVERR_DECREASING = 1,   /* an offset is smaller than its predecessor   */
     GG_DEVERR_GRANULE = 2,      /* a group size is not a multiple of 256       */
     GG_DEVERR_LAST = 4,         /* last offset != tokens_sum / > m_rows        */
-    GG_DEVERR_SKIPPED = 8       /* a group was too malformed to compute        */
+    GG_DEVERR_SKIPPED = 8,      /* a group was too malformed to compute        */
+    GG_DEVERR_IDS = 16          /* gg_plan: an id outside -1 .. E-1, or twice
+                                   in its token                                */
 };
 
 /* ABI version of the loaded library (GG_ABI_VERSION of its build). */
@@ -484,6 +501,209 @@ gg_status gg_dsrelu(const void* a_fp8, const uint8_t* sfa, int64_t m_rows, int32
                     void* d_row, gg_dtype d_dtype, float* dprob, float* amax,
                     const gg_fp8_out* fp8_out, uint32_t flags,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The router                                                                */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace gg_route needs. */
+size_t gg_route_workspace_size(int64_t tokens, int32_t num_experts);
+
+/*
+ * The choice of experts, their weights, tokens per expert and the balance
+ * loss.  Per token t, with x its logits:
+ *   key_e   = x_e + bias_e                     (one fp32 addition)
+ *   ids     = the top_k experts of the largest keys, largest first, ties to
+ *             the lower index.  -0 and +0 are equal, NaN is above +inf.  A
+ *             logit or key of -inf is never chosen: where fewer than top_k
+ *             are above it, the rest of ids is -1 and of prob 0.
+ *   scores  = softmax(x) over all experts (GG_SOFTMAX) or sigmoid(x)
+ *             (GG_SIGMOID), without the bias
+ *   prob    = scale * score of the chosen; with GG_FLAG_NORMALIZE
+ *             scale * softmax over the chosen experts' logits (GG_SOFTMAX),
+ *             scale * s / (sum of the chosen s + 1e-20) (GG_SIGMOID)
+ *   counts_e = tokens that chose e;  N = routed = tokens with a choice
+ *   balance = num_experts * sum_e (counts_e / (top_k N)) (1/N) sum_t p_te,
+ *             p the softmax, or s / (sum over all experts of s + 1e-20); a
+ *             token whose logits are all -inf adds nothing; 0 if N is 0
+ * A NaN or +inf logit makes NaN of what the formulas say it enters.
+ * fp32 arithmetic; the loss is summed in an order that depends on the sizes
+ * alone, so equal calls give equal bits.
+ *
+ * logits     (tokens, num_experts), dtype GG_BF16, GG_F16 or GG_F32, element
+ *            (t, e) at logits[t*ld + e], ld >= num_experts; aligned to its
+ *            element.
+ * tokens     0 .. 2^23.  num_experts 1..1024.
+ * bias       float[num_experts], or NULL for none.
+ * top_k      1 .. min(32, num_experts).  scale: finite.
+ * ids, prob  (tokens, top_k) int32 / float outputs.
+ * counts     int32[num_experts], routed int32[1]: outputs.
+ * balance    float[1] output, or NULL: the loss is not computed.
+ * flags      0 or GG_FLAG_NORMALIZE.
+ * workspace  >= gg_route_workspace_size(tokens, num_experts), 256-B aligned.
+ */
+gg_status gg_route(const void* logits, gg_dtype dtype, int64_t ld, int64_t tokens,
+                   int32_t num_experts, const float* bias, int32_t top_k, gg_score score,
+                   float scale, uint32_t flags, int32_t* ids, float* prob, int32_t* counts,
+                   int32_t* routed, float* balance,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient of gg_route's logits:
+ *   dlogits = d/dlogits (sum_tj dprob_tj prob_tj + dbalance balance)
+ * at the choice `ids` (the choice and the counts have no gradient).  Rows of
+ * a token without a choice are 0.
+ *
+ * logits, dtype, ld, tokens, num_experts, top_k, score, scale, flags, ids,
+ * counts, routed   as given to and made by gg_route.  An id outside
+ *            0 .. num_experts-1 is no choice; the ids of a token differ.
+ * dprob      float (tokens, top_k) if row_of is NULL; otherwise float[m_rows],
+ *            the gradient by expert row that gg_dglu and gg_dsrelu write, and
+ *            choice (t, j) takes dprob[row_of[t*top_k + j]]: 0 where row_of
+ *            is outside 0 .. m_rows-1 (a dropped choice).
+ * dbalance   float[1] in device memory, or NULL for no balance loss.
+ * dlogits    output (tokens, num_experts), dtype, contiguous, not
+ *            overlapping logits; aligned to its element; rounded once.
+ */
+gg_status gg_route_bwd(const void* logits, gg_dtype dtype, int64_t ld, int64_t tokens,
+                       int32_t num_experts, int32_t top_k, gg_score score, float scale,
+                       uint32_t flags, const int32_t* ids, const int32_t* counts,
+                       const int32_t* routed, const float* dprob, const int32_t* row_of,
+                       int64_t m_rows, const float* dbalance, void* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Dispatch to the expert-sorted rows, and back                              */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace gg_plan needs. */
+size_t gg_plan_workspace_size(int64_t tokens, int32_t num_experts);
+
+/* The most rows that gg_plan can need, whatever the ids are: with n = tokens
+ * * top_k, n + (granule-1) * min(num_experts, n) down to a multiple of
+ * granule.  0 for arguments out of gg_plan's ranges. */
+int64_t gg_plan_max_rows(int64_t tokens, int32_t top_k, int32_t num_experts, int32_t granule);
+
+/*
+ * The rows of every token's choices in the layout the grouped GEMMs take:
+ * expert after expert, tokens in order within an expert, every group padded
+ * to a multiple of `granule` rows (256 for this library's GEMMs).
+ *   counts_e  = tokens that chose e
+ *   padded_offsets_e = sum of the padded counts of experts 0 .. e
+ *   row_of[t, j] = padded_offsets_{e-1} + number of tokens t' < t that chose
+ *                  e = ids[t, j]; -1 where there is no row
+ *   prob_rows[row_of[t, j]] = prob[t, j], 0 in the padding
+ * An id of -1 has no row; nor has one outside -1 .. num_experts-1 or a
+ * second use of an expert by a token, which set GG_DEVERR_IDS.  Groups are
+ * cut off at m_rows (down to a multiple of granule): choices past it have
+ * no row, counts and padded_offsets hold what is left, GG_DEVERR_LAST is set.
+ *
+ * ids        (tokens, top_k) int32; tokens 0 .. 2^23, top_k 1..32,
+ *            num_experts 1..1024, granule a power of two in 1..256.
+ * m_rows     rows there is room for, 0 .. 2^31-1; gg_plan_max_rows suffices.
+ * prob       (tokens, top_k) float and prob_rows float[m_rows], or both NULL.
+ *            Rows at or past padded_offsets[E-1] are not written.
+ * counts, padded_offsets  int32[num_experts], row_of (tokens, top_k) int32:
+ *            outputs.
+ * workspace  >= gg_plan_workspace_size(tokens, num_experts), 256-B aligned;
+ *            its error word is read with gg_device_error.
+ */
+gg_status gg_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t num_experts,
+                  int32_t granule, int64_t m_rows, const float* prob, int32_t* counts,
+                  int32_t* padded_offsets, int32_t* row_of, float* prob_rows,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * x_rows[row_of[t, j], :] = x[t, :] for every choice with a row (row_of
+ * within 0 .. m_rows-1), and zeros in every group's padding rows,
+ * padded_offsets[e-1] + counts[e] .. padded_offsets[e]-1.  Copies: any value
+ * keeps its bits.
+ *
+ * x          (tokens, width), element (t, c) at x[t*ldx + c], ldx >= width;
+ *            GG_BF16, GG_F16, GG_F32, GG_F8E4M3 or GG_F8E5M2 (rows of bytes:
+ *            the E8M0 scales of MXFP8 rows too), aligned to its element.
+ * width      1 .. 2^20.
+ * row_of, counts, padded_offsets  as made by gg_plan.
+ * x_rows     output (m_rows, width), contiguous; other rows are not written.
+ * The gradient of x is gg_combine of x_rows' gradient with no weights.
+ */
+gg_status gg_permute(const void* x, gg_dtype dtype, int64_t ldx, int64_t tokens, int32_t width,
+                     const int32_t* row_of, int32_t top_k, const int32_t* counts,
+                     const int32_t* padded_offsets, int32_t num_experts, int64_t m_rows,
+                     void* x_rows, void* stream);
+
+/*
+ * out[t, :] = sum_j weights[t, j] * y_rows[row_of[t, j], :] over the choices
+ * with a row, in fp32 in the order of j, rounded once; 0 for a token with
+ * none.
+ *
+ * y_rows     (m_rows, width) contiguous, GG_BF16, GG_F16 or GG_F32.
+ * weights    (tokens, top_k) float, or NULL for 1.
+ * out        (tokens, width), y_rows' dtype, element (t, c) at out[t*ldo + c].
+ */
+gg_status gg_combine(const void* y_rows, gg_dtype dtype, int64_t m_rows, int32_t width,
+                     const int32_t* row_of, int64_t tokens, int32_t top_k, const float* weights,
+                     void* out, int64_t ldo, void* stream);
+
+/*
+ * The gradients of gg_combine:
+ *   dy_rows[row_of[t, j], :] = weights[t, j] * dout[t, :]  (rounded once;
+ *                              zeros in the padding rows, as gg_permute)
+ *   dweights[t, j] = sum_c dout[t, c] * y_rows[row_of[t, j], c]   (fp32; 0
+ *                              for a choice without a row)
+ * dout (tokens, width) with row pitch ldd; y_rows, dy_rows (m_rows, width)
+ * contiguous, not overlapping; all of one dtype.  weights, dweights
+ * (tokens, top_k) float.
+ */
+gg_status gg_combine_bwd(const void* dout, gg_dtype dtype, int64_t ldd, int64_t tokens,
+                         int32_t width, const void* y_rows, int64_t m_rows, const float* weights,
+                         const int32_t* row_of, int32_t top_k, const int32_t* counts,
+                         const int32_t* padded_offsets, int32_t num_experts, void* dy_rows,
+                         float* dweights, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gradient norm and clipping                                                */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace gg_grad_norm needs. */
+size_t gg_grad_workspace_size(void);
+
+/*
+ * sumsq = (accumulate ? sumsq : 0) + sum of the squares of every element of
+ * n tensors, in fp64, in an order that depends on the sizes alone.
+ *
+ * ptrs       int64[n] device array: the tensors' addresses, aligned to their
+ *            elements; not read for an empty tensor.
+ * ends       int64[n] device array: cumulative element counts (tensor i has
+ *            ends[i] - ends[i-1] elements), non-decreasing.
+ * dtypes     int32[n] device array: GG_BF16, GG_F16 or GG_F32 each (a tensor
+ *            of any other value is left out).
+ * n          0 .. 2^24.  total: elements of all tensors, ends[n-1] [host],
+ *            up to 2^40; elements past it are left out.
+ * sumsq      double[1], device memory, 8-byte aligned: ranks that share the
+ *            parameters add theirs up before gg_grad_clip.
+ * workspace  >= gg_grad_workspace_size() bytes, 256-B aligned.
+ */
+gg_status gg_grad_norm(const int64_t* ptrs, const int64_t* ends, const int32_t* dtypes, int32_t n,
+                       int64_t total, double* sumsq, int32_t accumulate,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * norm   = sqrt(sumsq)
+ * factor = min(1, max_norm / (norm + eps))    (NaN if norm is NaN)
+ * every element g becomes g * factor (one fp32 product, rounded once to its
+ * type).
+ *
+ * ptrs, ends, dtypes, n, total  as for gg_grad_norm.
+ * sumsq      double[1], device memory.
+ * max_norm   >= 0 and not NaN; eps >= 0 and finite.
+ * norm       float[2] output: norm and factor.
+ * out_ptrs   int64[n] device array of the results' addresses, in ptrs' types,
+ *            or NULL: in place, and where the factor is exactly 1 nothing is
+ *            written.  A result is its own tensor or does not overlap any.
+ */
+gg_status gg_grad_clip(const int64_t* ptrs, const int64_t* ends, const int32_t* dtypes, int32_t n,
+                       int64_t total, const double* sumsq, float max_norm, float eps, float* norm,
+                       const int64_t* out_ptrs, void* stream);
 
 #ifdef __cplusplus
 }

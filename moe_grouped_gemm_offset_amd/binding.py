@@ -21,12 +21,17 @@ GG_DSWIGLU, GG_DGEGLU, GG_DSITUGLU = 0, 1, 2
 GG_FLAG_GATE_FIRST, GG_FLAG_GEGLU_MASK_FILTER, GG_FLAG_VALIDATE_OFFSETS = 1, 2, 4
 GG_FLAG_TENSOR_RAGGED, GG_FLAG_STATIC_SCHED, GG_FLAG_AB_E5M2 = 8, 16, 32
 GG_DEVERR_DECREASING, GG_DEVERR_GRANULE, GG_DEVERR_LAST, GG_DEVERR_SKIPPED = 1, 2, 4, 8
+GG_DEVERR_IDS = 16
+GG_FLAG_NORMALIZE = 64
+GG_SOFTMAX, GG_SIGMOID = 0, 1
 STATUS_NAMES = ["GG_OK", "GG_ERR_NULL", "GG_ERR_SHAPE", "GG_ERR_DTYPE", "GG_ERR_LAYOUT",
                 "GG_ERR_ALIGN", "GG_ERR_MODE", "GG_ERR_WORKSPACE", "GG_ERR_UNSUPPORTED",
                 "GG_ERR_DEVICE", "GG_ERR_HIP", "GG_ERR_OFFSETS", "GG_ERR_VALUE"]
 EXPORTS = ["gg_abi_version", "gg_last_error", "gg_device_error", "gg_wgrad_workspace_size",
            "gg_wgrad", "gg_wgrad_noalloc", "gg_wgrad_mx", "gg_dglu_workspace_size", "gg_dglu", "gg_dglu_mx",
-           "gg_dsrelu_workspace_size", "gg_dsrelu"]
+           "gg_dsrelu_workspace_size", "gg_dsrelu", "gg_route_workspace_size", "gg_route",
+           "gg_route_bwd", "gg_plan_workspace_size", "gg_plan_max_rows", "gg_plan", "gg_permute",
+           "gg_combine", "gg_combine_bwd", "gg_grad_workspace_size", "gg_grad_norm", "gg_grad_clip"]
 
 _TORCH_DTYPE = {torch.bfloat16: GG_BF16, torch.float16: GG_F16, torch.float32: GG_F32,
                 torch.float8_e4m3fn: GG_F8E4M3, torch.float8_e5m2: GG_F8E5M2}
@@ -80,6 +85,30 @@ def load_library(path=LIB_PATH):
     L.gg_dsrelu.restype = ctypes.c_int
     L.gg_dsrelu.argtypes = [P, P, I64, I32, P, P, P, P, I32, I32, P, I32, P, I32, P, P, P, I32, P, P,
                             P, U32, P, SZ, P]
+    L.gg_route_workspace_size.restype = SZ
+    L.gg_route_workspace_size.argtypes = [I64, I32]
+    L.gg_route.restype = ctypes.c_int
+    L.gg_route.argtypes = [P, I32, I64, I64, I32, P, I32, I32, F, U32, P, P, P, P, P, P, SZ, P]
+    L.gg_route_bwd.restype = ctypes.c_int
+    L.gg_route_bwd.argtypes = [P, I32, I64, I64, I32, I32, I32, F, U32, P, P, P, P, P, I64, P, P, P]
+    L.gg_plan_workspace_size.restype = SZ
+    L.gg_plan_workspace_size.argtypes = [I64, I32]
+    L.gg_plan_max_rows.restype = I64
+    L.gg_plan_max_rows.argtypes = [I64, I32, I32, I32]
+    L.gg_plan.restype = ctypes.c_int
+    L.gg_plan.argtypes = [P, I64, I32, I32, I32, I64, P, P, P, P, P, P, SZ, P]
+    L.gg_permute.restype = ctypes.c_int
+    L.gg_permute.argtypes = [P, I32, I64, I64, I32, P, I32, P, P, I32, I64, P, P]
+    L.gg_combine.restype = ctypes.c_int
+    L.gg_combine.argtypes = [P, I32, I64, I32, P, I64, I32, P, P, I64, P]
+    L.gg_combine_bwd.restype = ctypes.c_int
+    L.gg_combine_bwd.argtypes = [P, I32, I64, I64, I32, P, I64, P, P, I32, P, P, I32, P, P, P]
+    L.gg_grad_workspace_size.restype = SZ
+    L.gg_grad_workspace_size.argtypes = []
+    L.gg_grad_norm.restype = ctypes.c_int
+    L.gg_grad_norm.argtypes = [P, P, P, I32, I64, P, I32, P, SZ, P]
+    L.gg_grad_clip.restype = ctypes.c_int
+    L.gg_grad_clip.argtypes = [P, P, P, I32, I64, P, F, F, P, P, P]
     _lib = L
     return L
 
@@ -287,3 +316,237 @@ def gg_dsrelu(a, sfa, b, sfb, b_ptrs, sfb_ptrs, n, c, padded_offsets, alpha, pro
                        _TORCH_DTYPE[d_row.dtype], _ptr(dprob), _ptr(amax), _ref(q), _ab(a, flags), _ptr(ws),
                        nbytes, _stream(stream)))
     return ws
+
+
+# --------------------------------------------------------------------------
+# around the grouped GEMMs: router, dispatch and combine, gradient clipping
+# --------------------------------------------------------------------------
+
+def _need(t, what, shape, dtypes, like=None, rows=False):
+    """Checks a tensor argument: type, shape (None: any extent), device, and
+    that it is contiguous (rows: that each row is, at any pitch)."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if t.dtype not in dtypes:
+        raise GGError(3, f"{what} has dtype {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise GGError(2, f"{what} has shape {tuple(t.shape)}, not "
+                         f"{tuple('any' if n is None else n for n in shape)}")
+    if like is not None and t.device != like.device:
+        raise GGError(9, f"{what} is on {t.device}, not {like.device}")
+    if rows:
+        if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or
+                          (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
+            raise GGError(4, f"{what} needs contiguous rows that do not overlap")
+    elif not t.is_contiguous():
+        raise GGError(4, f"{what} must be contiguous")
+    return t
+
+
+def _pitch(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+_BYTES = (torch.float8_e4m3fn, torch.float8_e5m2, torch.uint8)
+
+
+def gg_route_workspace_size(tokens, num_experts):
+    return load_library().gg_route_workspace_size(tokens, num_experts)
+
+
+def gg_plan_workspace_size(tokens, num_experts):
+    return load_library().gg_plan_workspace_size(tokens, num_experts)
+
+
+def gg_plan_max_rows(tokens, top_k, num_experts, granule=256):
+    return load_library().gg_plan_max_rows(tokens, top_k, num_experts, granule)
+
+
+def gg_grad_workspace_size():
+    return load_library().gg_grad_workspace_size()
+
+
+def gg_route(logits, ids, prob, counts, routed, balance=None, bias=None, score=GG_SOFTMAX, scale=1.0,
+             flags=0, workspace=None, stream=None):
+    """The router (gg_route of gg_moe.h): logits (T, E) at any row pitch; ids
+    int32 and prob float32 (T, top_k), counts int32 (E,), routed int32 (1,)
+    and balance float32 (1,) are written.  Returns the workspace used."""
+    L = load_library()
+    _need(logits, "logits", (None, None), _FLOATS, rows=True)
+    T, E = logits.shape
+    k = ids.shape[-1]
+    _need(ids, "ids", (T, k), torch.int32, logits)
+    _need(prob, "prob", (T, k), torch.float32, logits)
+    _need(counts, "counts", (E,), torch.int32, logits)
+    _need(routed, "routed", (1,), torch.int32, logits)
+    if balance is not None:
+        _need(balance, "balance", (1,), torch.float32, logits)
+    if bias is not None:
+        _need(bias, "bias", (E,), torch.float32, logits)
+    ws, nbytes = _workspace(workspace, L.gg_route_workspace_size(T, E), logits, stream)
+    _check(L.gg_route(_ptr(logits), _TORCH_DTYPE[logits.dtype], _pitch(logits), T, E, _ptr(bias), k,
+                      score, scale, flags, _ptr(ids), _ptr(prob), _ptr(counts), _ptr(routed),
+                      _ptr(balance), _ptr(ws), nbytes, _stream(stream)))
+    return ws
+
+
+def gg_route_bwd(logits, ids, counts, routed, dprob, dlogits, row_of=None, dbalance=None,
+                 score=GG_SOFTMAX, scale=1.0, flags=0, stream=None):
+    """The gradient of gg_route's logits (gg_route_bwd of gg_moe.h).  dprob is
+    float32: (T, top_k), or with row_of (T, top_k) one value per expert row,
+    (m_rows,), as gg_dglu and gg_dsrelu write it."""
+    L = load_library()
+    _need(logits, "logits", (None, None), _FLOATS, rows=True)
+    T, E = logits.shape
+    k = ids.shape[-1]
+    _need(ids, "ids", (T, k), torch.int32, logits)
+    _need(counts, "counts", (E,), torch.int32, logits)
+    _need(routed, "routed", (1,), torch.int32, logits)
+    m = 0
+    if row_of is None:
+        _need(dprob, "dprob", (T, k), torch.float32, logits)
+    else:
+        _need(row_of, "row_of", (T, k), torch.int32, logits)
+        _need(dprob, "dprob", (None,), torch.float32, logits)
+        m = dprob.shape[0]
+    if dbalance is not None:
+        _need(dbalance, "dbalance", (1,), torch.float32, logits)
+    _need(dlogits, "dlogits", (T, E), logits.dtype, logits)
+    _check(L.gg_route_bwd(_ptr(logits), _TORCH_DTYPE[logits.dtype], _pitch(logits), T, E, k, score,
+                          scale, flags, _ptr(ids), _ptr(counts), _ptr(routed), _ptr(dprob),
+                          _ptr(row_of), m, _ptr(dbalance), _ptr(dlogits), _stream(stream)))
+
+
+def gg_plan(ids, counts, padded_offsets, row_of, m_rows, granule=256, prob=None, prob_rows=None,
+            workspace=None, stream=None):
+    """Rows of every token's choices in the expert-sorted layout (gg_plan of
+    gg_moe.h): ids int32 (T, top_k); counts and padded_offsets int32 (E,),
+    row_of int32 (T, top_k) and prob_rows float32 (m_rows,) are written.
+    Returns the workspace used (gg_device_error reads its error word)."""
+    L = load_library()
+    _need(ids, "ids", (None, None), torch.int32)
+    T, k = ids.shape
+    _need(counts, "counts", (None,), torch.int32, ids)
+    E = counts.shape[0]
+    _need(padded_offsets, "padded_offsets", (E,), torch.int32, ids)
+    _need(row_of, "row_of", (T, k), torch.int32, ids)
+    if prob is not None:
+        _need(prob, "prob", (T, k), torch.float32, ids)
+    if prob_rows is not None:
+        _need(prob_rows, "prob_rows", (m_rows,), torch.float32, ids)
+    ws, nbytes = _workspace(workspace, L.gg_plan_workspace_size(T, E), ids, stream)
+    _check(L.gg_plan(_ptr(ids), T, k, E, granule, m_rows, _ptr(prob), _ptr(counts),
+                     _ptr(padded_offsets), _ptr(row_of), _ptr(prob_rows), _ptr(ws), nbytes,
+                     _stream(stream)))
+    return ws
+
+
+def gg_permute(x, row_of, counts, padded_offsets, x_rows, stream=None):
+    """x_rows[row_of[t, j]] = x[t], zeros in the padding (gg_permute of
+    gg_moe.h): x (T, width) at any row pitch, x_rows (m_rows, width); one- to
+    four-byte types."""
+    L = load_library()
+    _need(x, "x", (None, None), _FLOATS + _BYTES, rows=True)
+    T, width = x.shape
+    k = row_of.shape[-1]
+    _need(row_of, "row_of", (T, k), torch.int32, x)
+    _need(counts, "counts", (None,), torch.int32, x)
+    E = counts.shape[0]
+    _need(padded_offsets, "padded_offsets", (E,), torch.int32, x)
+    _need(x_rows, "x_rows", (None, width), x.dtype, x)
+    _check(L.gg_permute(_ptr(x), _TORCH_DTYPE.get(x.dtype, GG_F8E4M3), _pitch(x), T, width,
+                        _ptr(row_of), k, _ptr(counts), _ptr(padded_offsets), E, x_rows.shape[0],
+                        _ptr(x_rows), _stream(stream)))
+
+
+def gg_combine(y_rows, row_of, out, weights=None, stream=None):
+    """out[t] = sum_j weights[t, j] y_rows[row_of[t, j]] (gg_combine of
+    gg_moe.h); weights None: 1.  out (T, width) at any row pitch."""
+    L = load_library()
+    _need(out, "out", (None, None), _FLOATS, rows=True)
+    T, width = out.shape
+    k = row_of.shape[-1]
+    _need(y_rows, "y_rows", (None, width), out.dtype, out)
+    _need(row_of, "row_of", (T, k), torch.int32, out)
+    if weights is not None:
+        _need(weights, "weights", (T, k), torch.float32, out)
+    _check(L.gg_combine(_ptr(y_rows), _TORCH_DTYPE[out.dtype], y_rows.shape[0], width, _ptr(row_of), T,
+                        k, _ptr(weights), _ptr(out), _pitch(out), _stream(stream)))
+
+
+def gg_combine_bwd(dout, y_rows, row_of, weights, counts, padded_offsets, dy_rows, dweights,
+                   stream=None):
+    """The gradients of gg_combine (gg_combine_bwd of gg_moe.h): dy_rows
+    (m_rows, width), zeros in the padding, and dweights float32 (T, top_k)."""
+    L = load_library()
+    _need(dout, "dout", (None, None), _FLOATS, rows=True)
+    T, width = dout.shape
+    k = row_of.shape[-1]
+    _need(y_rows, "y_rows", (None, width), dout.dtype, dout)
+    m = y_rows.shape[0]
+    _need(row_of, "row_of", (T, k), torch.int32, dout)
+    _need(weights, "weights", (T, k), torch.float32, dout)
+    _need(counts, "counts", (None,), torch.int32, dout)
+    E = counts.shape[0]
+    _need(padded_offsets, "padded_offsets", (E,), torch.int32, dout)
+    _need(dy_rows, "dy_rows", (m, width), dout.dtype, dout)
+    _need(dweights, "dweights", (T, k), torch.float32, dout)
+    _check(L.gg_combine_bwd(_ptr(dout), _TORCH_DTYPE[dout.dtype], _pitch(dout), T, width, _ptr(y_rows),
+                            m, _ptr(weights), _ptr(row_of), k, _ptr(counts), _ptr(padded_offsets), E,
+                            _ptr(dy_rows), _ptr(dweights), _stream(stream)))
+
+
+def grad_table(tensors):
+    """What gg_grad_norm and gg_grad_clip take of a list of tensors on one
+    GPU, built once and kept while the tensors keep their memory:
+    (ptrs, ends, dtypes, total)."""
+    for i, t in enumerate(tensors):
+        if t.dtype not in _FLOATS:
+            raise GGError(3, f"tensor {i} has dtype {t.dtype}")
+        if not t.is_contiguous():
+            raise GGError(4, f"tensor {i} must be contiguous")
+        if t.device != tensors[0].device:
+            raise GGError(9, f"tensor {i} is on {t.device}, not {tensors[0].device}")
+    dev = tensors[0].device if tensors else torch.device("cuda")
+    ends, total = [], 0
+    for t in tensors:
+        total += t.numel()
+        ends.append(total)
+    return (torch.tensor([t.data_ptr() for t in tensors], dtype=torch.int64, device=dev),
+            torch.tensor(ends, dtype=torch.int64, device=dev),
+            torch.tensor([_TORCH_DTYPE[t.dtype] for t in tensors], dtype=torch.int32, device=dev), total)
+
+
+def _need_table(ptrs, ends, dtypes, sumsq):
+    _need(ptrs, "ptrs", (None,), torch.int64)
+    n = ptrs.shape[0]
+    _need(ends, "ends", (n,), torch.int64, ptrs)
+    _need(dtypes, "dtypes", (n,), torch.int32, ptrs)
+    _need(sumsq, "sumsq", (1,), torch.float64, ptrs)
+    return n
+
+
+def gg_grad_norm(ptrs, ends, dtypes, total, sumsq, accumulate=False, workspace=None, stream=None):
+    """sumsq (float64, (1,)) = the sum of squares over many tensors
+    (gg_grad_norm of gg_moe.h; grad_table makes the first four arguments).
+    Returns the workspace used."""
+    L = load_library()
+    n = _need_table(ptrs, ends, dtypes, sumsq)
+    ws, nbytes = _workspace(workspace, L.gg_grad_workspace_size(), ptrs, stream)
+    _check(L.gg_grad_norm(_ptr(ptrs), _ptr(ends), _ptr(dtypes), n, total, _ptr(sumsq),
+                          int(bool(accumulate)), _ptr(ws), nbytes, _stream(stream)))
+    return ws
+
+
+def gg_grad_clip(ptrs, ends, dtypes, total, sumsq, max_norm, norm, eps=1e-6, out_ptrs=None,
+                 stream=None):
+    """Scales every tensor by min(1, max_norm / (sqrt(sumsq) + eps)), in place
+    or into out_ptrs' tensors; norm (float32, (2,)) = the norm and the factor
+    (gg_grad_clip of gg_moe.h)."""
+    L = load_library()
+    n = _need_table(ptrs, ends, dtypes, sumsq)
+    _need(norm, "norm", (2,), torch.float32, ptrs)
+    if out_ptrs is not None:
+        _need(out_ptrs, "out_ptrs", (n,), torch.int64, ptrs)
+    _check(L.gg_grad_clip(_ptr(ptrs), _ptr(ends), _ptr(dtypes), n, total, _ptr(sumsq), max_norm, eps,
+                          _ptr(norm), _ptr(out_ptrs), _stream(stream)))

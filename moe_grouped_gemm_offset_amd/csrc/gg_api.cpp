@@ -15,14 +15,13 @@
 #include <cstring>
 #include <mutex>
 
-#include "gg_moe.h"
-#include "gg_internal.hpp"
+#include "gg_host.hpp"
 
-namespace {
+namespace gg {
 
 // The last error message of this thread (a fixed buffer: no entry point
 // allocates memory, on any path).
-thread_local char g_err[512];
+static thread_local char g_err[512];
 
 gg_status fail(gg_status s, const char* fmt, ...) {
     va_list ap;
@@ -37,8 +36,6 @@ gg_status ok() {
     return GG_OK;
 }
 
-// GG_LOG set (to anything but "0"): every launch reports the kernel variant
-// it chose, the workgroup tile and the grid on stderr, one line per call.
 // Read at every call (a getenv, no allocation).
 bool log_enabled() {
     const char* v = getenv("GG_LOG");
@@ -49,14 +46,6 @@ void log_launch(const char* op, const gg::LaunchInfo& i, const char* shape) {
     fprintf(stderr, "[gg] %s %s: %s, tile %dx%d, %d waves, grid %lld\n", op, shape, i.kernel,
             i.tm, i.tn, i.waves, (long long)i.grid);
 }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-bool is_out_dtype(gg_dtype d) { return d == GG_BF16 || d == GG_F16 || d == GG_F32; }
-
-bool is_fp8(gg_dtype d) { return d == GG_F8E4M3 || d == GG_F8E5M2; }
 
 // Current device must be a gfx950; the answer is cached per device ordinal.
 gg_status check_device() {
@@ -85,6 +74,12 @@ gg_status check_device() {
 gg_status hip_fail(hipError_t e, const char* what) {
     return fail(GG_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace gg
+
+using namespace gg;
+
+namespace {
 
 // GG_FLAG_VALIDATE_OFFSETS: read the offsets on the host and apply the
 // pages' rules.  dgrad: last <= total; wgrad: last == total.
@@ -153,7 +148,7 @@ extern "C" {
 
 int gg_abi_version(void) { return GG_ABI_VERSION; }
 
-const char* gg_last_error(void) { return g_err; }
+const char* gg_last_error(void) { return gg::g_err; }
 
 gg_status gg_device_error(const void* workspace, void* stream, int32_t* code) {
     if (!workspace || !code)

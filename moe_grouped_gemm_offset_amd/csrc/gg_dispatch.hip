@@ -1,0 +1,493 @@
+// gg_dispatch.hip -- tokens to the expert-sorted rows the grouped GEMMs take,
+// and back: the row of every (token, choice), the copies, the weighted sum
+// of a token's rows and that sum's gradients.
+#include "gg_internal.hpp"
+#include "gg_lane.hpp"
+
+namespace gg {
+
+namespace {
+
+// ---- the plan --------------------------------------------------------------
+//
+// A row's place in its expert's group is the number of earlier tokens that
+// chose the expert.  Tokens go in chunks of 256: per chunk an LDS bitmap,
+// one bit per (expert, token), is set with integer ORs (their order does not
+// matter), and a token's rank is the population count of the bits below its
+// own.  A block takes a run of chunks.  plan_count_kernel writes each
+// block's counts, plan_assign_kernel sums those of the blocks before it and
+// numbers the rows.  With one block there is nothing to join and
+// plan_assign_kernel counts for itself.
+//
+// An id outside 0 .. E-1, or one that its token has already used, has no row.
+
+constexpr int kPlanThreads = 1024;
+constexpr int kChunk = 256;                          // tokens of a bitmap
+constexpr int kWords = kChunk / 32;
+constexpr int kMaxExperts = 1024;
+
+// Whether slot i (token t, choice j) of the ids has a row; f |= a flag if the
+// id is neither a valid one nor -1.
+__device__ __forceinline__ bool plan_slot(const PlanArgs& p, int64_t i, int64_t t, int& e, int& f) {
+    e = p.ids[i];
+    if (e < 0 || e >= p.E) {
+        if (e != -1)
+            f |= GG_DEVERR_IDS;
+        return false;
+    }
+    for (int64_t q = t * p.k; q < i; q++)
+        if (p.ids[q] == e) {
+            f |= GG_DEVERR_IDS;
+            return false;
+        }
+    return true;
+}
+
+// Sets the chunk's bits; every thread of the block calls it.
+__device__ void plan_bits(const PlanArgs& p, int64_t t0, uint32_t* bits, int& f) {
+    for (int i = threadIdx.x; i < p.E * kWords; i += kPlanThreads)
+        bits[i] = 0;
+    __syncthreads();
+    const int64_t t1 = min(p.T, t0 + kChunk);
+    for (int64_t i = t0 * p.k + threadIdx.x; i < t1 * p.k; i += kPlanThreads) {
+        const int64_t t = i / p.k;
+        int e;
+        if (plan_slot(p, i, t, e, f)) {
+            const int b = (int)(t - t0);
+            atomicOr(&bits[e * kWords + (b >> 5)], 1u << (b & 31));
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int plan_ones(const uint32_t* bits, int e) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; w++)
+        c += __popc(bits[e * kWords + w]);
+    return c;
+}
+
+// Workspace: header (int32 0: the error word), then [blocks][E + 1] int32:
+// each block's counts and its flags.
+__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(PlanArgs p, int64_t run) {
+    __shared__ uint32_t bits[kMaxExperts * kWords];
+    __shared__ int32_t flags;
+    const int e = threadIdx.x;
+    if (e == 0)
+        flags = 0;
+    int count = 0, f = 0;
+    const int64_t t1 = min(p.T, (int64_t)(blockIdx.x + 1) * run);
+    for (int64_t t = blockIdx.x * run; t < t1; t += kChunk) {
+        plan_bits(p, t, bits, f);
+        if (e < p.E)
+            count += plan_ones(bits, e);
+        __syncthreads();
+    }
+    if (f)
+        atomicOr(&flags, f);
+    __syncthreads();
+    int32_t* part = p.ws + kWsHeader / 4 + (int64_t)blockIdx.x * (p.E + 1);
+    if (e < p.E)
+        part[e] = count;
+    if (e == 0)
+        part[p.E] = flags;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_assign_kernel(PlanArgs p, int64_t run, int blocks) {
+    __shared__ uint32_t bits[kMaxExperts * kWords];
+    __shared__ int32_t base[kMaxExperts];            // row of the block's next token of an expert
+    __shared__ int32_t stop[kMaxExperts];            // end of the group, within m_rows
+    __shared__ int32_t fill[kMaxExperts];            // first padding row
+    __shared__ int64_t scan[kPlanThreads];
+    __shared__ int32_t flags;
+    const int e = threadIdx.x, E = p.E;
+    if (e == 0)
+        flags = 0;
+    int f = 0;
+    // counts of the blocks before this one, and of all
+    int before = 0, all = 0;
+    if (blocks > 1) {
+        if (e < E) {
+            for (int b = 0; b < blocks; b++) {
+                const int c = p.ws[kWsHeader / 4 + (int64_t)b * (E + 1) + e];
+                before += b < (int)blockIdx.x ? c : 0;
+                all += c;
+            }
+        }
+        if (blockIdx.x == 0 && e < blocks)
+            f |= p.ws[kWsHeader / 4 + (int64_t)e * (E + 1) + E];
+    } else {
+        for (int64_t t = 0; t < p.T; t += kChunk) {
+            plan_bits(p, t, bits, f);
+            if (e < E)
+                all += plan_ones(bits, e);
+            __syncthreads();
+        }
+    }
+    // the padded groups' ends: a scan over the experts
+    const int64_t padded = e < E ? ((int64_t)all + p.granule - 1) / p.granule * p.granule : 0;
+    scan[e] = padded;
+    __syncthreads();
+    for (int h = 1; h < kPlanThreads; h <<= 1) {
+        const int64_t v = e >= h ? scan[e - h] : 0;
+        __syncthreads();
+        scan[e] += v;
+        __syncthreads();
+    }
+    // groups are cut off where the rows end
+    const int64_t limit = p.m_rows / p.granule * p.granule;
+    const int64_t b0 = min(scan[e] - padded, limit), b1 = min(scan[e], limit);
+    const int kept = (int)min((int64_t)all, b1 - b0);
+    if (e < E) {
+        base[e] = (int)(b0 + min((int64_t)before, b1 - b0));
+        stop[e] = (int)b1;
+        fill[e] = (int)(b0 + kept);
+        if (blockIdx.x == 0) {
+            p.counts[e] = kept;
+            p.ends[e] = (int)b1;
+            if (kept < all)
+                f |= GG_DEVERR_LAST;
+        }
+    }
+    __syncthreads();
+    const int64_t t1 = min(p.T, (int64_t)(blockIdx.x + 1) * run);
+    int seen = 0;
+    for (int64_t t0 = blockIdx.x * run; t0 < t1; t0 += kChunk) {
+        plan_bits(p, t0, bits, seen);
+        const int64_t i1 = min(t1, t0 + kChunk) * p.k;
+        for (int64_t i = t0 * p.k + threadIdx.x; i < i1; i += kPlanThreads) {
+            const int64_t t = i / p.k;
+            int x;
+            int32_t row = -1;
+            if (plan_slot(p, i, t, x, seen)) {
+                const int b = (int)(t - t0);
+                int rank = __popc(bits[x * kWords + (b >> 5)] & ((1u << (b & 31)) - 1u));
+                for (int w = 0; w < (b >> 5); w++)
+                    rank += __popc(bits[x * kWords + w]);
+                const int64_t r = (int64_t)base[x] + rank;
+                if (r < stop[x])
+                    row = (int32_t)r;
+            }
+            p.row_of[i] = row;
+            if (p.prob_rows && row >= 0)
+                p.prob_rows[row] = p.prob[i];
+        }
+        __syncthreads();
+        if (e < E)
+            base[e] = min(base[e] + plan_ones(bits, e), stop[e]);
+        __syncthreads();
+    }
+    // padding rows, the experts dealt to the blocks
+    if (p.prob_rows)
+        for (int x = blockIdx.x; x < E; x += gridDim.x)
+            for (int r = fill[x] + threadIdx.x; r < stop[x]; r += kPlanThreads)
+                p.prob_rows[r] = 0.0f;
+    if (f)
+        atomicOr(&flags, f);
+    __syncthreads();
+    if (blockIdx.x == 0 && e == 0)
+        p.ws[0] = flags;
+}
+
+// ---- rows ------------------------------------------------------------------
+//
+// Token rows and expert rows are walked in 16-byte vectors at element
+// alignment; a row's last, shorter one goes element by element.  A block is
+// tx vectors of a row by 256 / tx tokens.
+
+constexpr int kRowThreads = 256;
+constexpr int kPadParts = 8;                         // blocks that share an expert's padding rows
+
+template <int DT>
+struct RowElem {
+    typedef typename Elem<DT>::T T;
+    static constexpr int N = 16 / (int)sizeof(T);
+};
+
+// x_rows[row_of[t, j]] = x[t], zeros in the padding.  SIZE: bytes of an
+// element; the values are copied as they are.
+template <int SIZE>
+__global__ void __launch_bounds__(kRowThreads) permute_kernel(RowsArgs p, int tx, int pads) {
+    typedef typename Raw<16>::T V;
+    const int col = threadIdx.x % tx + (int)blockIdx.y * tx;
+    const int64_t bytes = (int64_t)p.width * SIZE;
+    const int64_t at = (int64_t)col * 16;
+    if (at >= bytes)
+        return;
+    const bool whole = at + 16 <= bytes;
+    char* out = (char*)p.rows_out;
+    if ((int)blockIdx.x < pads) {
+        const int e = blockIdx.x / kPadParts, part = blockIdx.x % kPadParts;
+        const int ty = kRowThreads / tx;
+        const int begin = e ? p.ends[e - 1] : 0;
+        const int64_t r1 = min((int64_t)p.ends[e], p.m_rows);
+        for (int64_t r = (int64_t)max(begin, 0) + max(p.counts[e], 0) + part * ty + threadIdx.x / tx; r < r1;
+             r += kPadParts * ty) {
+            if (whole)
+                *(V*)(out + r * bytes + at) = V{0, 0, 0, 0};
+            else
+                for (int64_t b = at; b < bytes; b++)
+                    out[r * bytes + b] = 0;
+        }
+        return;
+    }
+    const int64_t t = (int64_t)(blockIdx.x - pads) * (kRowThreads / tx) + threadIdx.x / tx;
+    if (t >= p.T)
+        return;
+    const char* in = (const char*)p.tokens + t * p.ld * SIZE;
+    if (whole) {
+        const V v = *(const V*)(in + at);
+        for (int j = 0; j < p.k; j++) {
+            const int64_t r = p.row_of[t * p.k + j];
+            if (r >= 0 && r < p.m_rows)
+                *(V*)(out + r * bytes + at) = v;
+        }
+    } else {
+        for (int j = 0; j < p.k; j++) {
+            const int64_t r = p.row_of[t * p.k + j];
+            if (r >= 0 && r < p.m_rows)
+                for (int64_t b = at; b < bytes; b++)
+                    out[r * bytes + b] = in[b];
+        }
+    }
+}
+
+// out[t] = sum_j w[t, j] y[row_of[t, j]], in fp32 in the order of j, rounded
+// once.
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(RowsArgs p, int tx) {
+    typedef typename Elem<DT>::T T;
+    constexpr int N = RowElem<DT>::N;
+    const int c = (threadIdx.x % tx + (int)blockIdx.y * tx) * N;
+    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / tx) + threadIdx.x / tx;
+    if (t >= p.T || c >= p.width)
+        return;
+    const T* y = (const T*)p.rows_in;
+    T* out = (T*)p.out + t * p.ld;
+    const int32_t* row_of = p.row_of + t * p.k;
+    const float* w = p.weights ? p.weights + t * p.k : nullptr;
+    if (c + N <= p.width) {
+        float acc[N];
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            acc[i] = 0.0f;
+        for (int j = 0; j < p.k; j++) {
+            const int64_t r = row_of[j];
+            if (r < 0 || r >= p.m_rows)
+                continue;
+            Vec<DT, N> v;
+            v.load(y + r * p.width + c);
+            const float wj = w ? w[j] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                acc[i] = fmaf(wj, v.get(i), acc[i]);
+        }
+        Vec<DT, N> v;
+        v.set(acc);
+        v.store(out + c);
+    } else {
+        for (int i = c; i < p.width; i++) {
+            float acc = 0.0f;
+            for (int j = 0; j < p.k; j++) {
+                const int64_t r = row_of[j];
+                if (r >= 0 && r < p.m_rows)
+                    acc = fmaf(w ? w[j] : 1.0f, to_f32<DT>(y[r * p.width + i]), acc);
+            }
+            out[i] = from_f32<DT>(acc);
+        }
+    }
+}
+
+// dy[row_of[t, j]] = w[t, j] dout[t] (rounded once; zeros in the padding),
+// dw[t, j] = <dout[t], y[row_of[t, j]]> in fp32.  A block a token; the first
+// `pads` blocks clear the padding.
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(RowsArgs p, int pads) {
+    typedef typename Elem<DT>::T T;
+    constexpr int N = RowElem<DT>::N, KB = 8;
+    __shared__ float part[kRowThreads / 64][KB];
+    T* dy = (T*)p.rows_out;
+    const int tid = threadIdx.x;
+    if ((int)blockIdx.x < pads) {
+        const int e = blockIdx.x / kPadParts, sub = blockIdx.x % kPadParts;
+        const int begin = e ? p.ends[e - 1] : 0;
+        const int64_t r1 = min((int64_t)p.ends[e], p.m_rows);
+        for (int64_t r = (int64_t)max(begin, 0) + max(p.counts[e], 0) + sub; r < r1; r += kPadParts)
+            for (int c = tid * N; c < p.width; c += kRowThreads * N) {
+                if (c + N <= p.width) {
+                    Vec<DT, N> z;
+                    z.raw = 0;
+                    z.store(dy + r * p.width + c);
+                } else {
+                    for (int i = c; i < p.width; i++)
+                        dy[r * p.width + i] = 0;
+                }
+            }
+        return;
+    }
+    const int64_t t = blockIdx.x - pads;
+    const T* dout = (const T*)p.tokens + t * p.ld;
+    const T* y = (const T*)p.rows_in;
+    for (int j0 = 0; j0 < p.k; j0 += KB) {
+        const int kb = min(KB, p.k - j0);
+        int64_t row[KB];
+        float w[KB], dot[KB];
+#pragma unroll
+        for (int j = 0; j < KB; j++) {
+            const int64_t r = j < kb ? p.row_of[t * p.k + j0 + j] : -1;
+            row[j] = r >= 0 && r < p.m_rows ? r : -1;
+            w[j] = j < kb ? p.weights[t * p.k + j0 + j] : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int c = tid * N; c < p.width; c += kRowThreads * N) {
+            if (c + N <= p.width) {
+                Vec<DT, N> d;
+                d.load(dout + c);
+#pragma unroll
+                for (int j = 0; j < KB; j++) {
+                    if (row[j] < 0)
+                        continue;
+                    Vec<DT, N> v;
+                    float f[N];
+                    v.load(y + row[j] * p.width + c);
+#pragma unroll
+                    for (int i = 0; i < N; i++) {
+                        dot[j] = fmaf(d.get(i), v.get(i), dot[j]);
+                        f[i] = w[j] * d.get(i);
+                    }
+                    v.set(f);
+                    v.store(dy + row[j] * p.width + c);
+                }
+            } else {
+                for (int i = c; i < p.width; i++) {
+                    const float d = to_f32<DT>(dout[i]);
+#pragma unroll
+                    for (int j = 0; j < KB; j++)
+                        if (row[j] >= 0) {
+                            dot[j] = fmaf(d, to_f32<DT>(y[row[j] * p.width + i]), dot[j]);
+                            dy[row[j] * p.width + i] = from_f32<DT>(w[j] * d);
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < KB; j++) {
+            const float s = group_all<64>(dot[j], OpAddF());
+            if ((tid & 63) == 0)
+                part[tid >> 6][j] = s;
+        }
+        __syncthreads();
+        if (tid < kb)
+            p.dweights[t * p.k + j0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        __syncthreads();
+    }
+}
+
+// Threads of a block along a row of `vecs` vectors: a power of two up to 256.
+int row_threads(int64_t vecs) {
+    int tx = 1;
+    while (tx < vecs && tx < kRowThreads)
+        tx *= 2;
+    return tx;
+}
+
+}  // namespace
+
+// ---- launches --------------------------------------------------------------
+
+static int64_t plan_blocks(int64_t T) {
+    const int64_t chunks = (T + kChunk - 1) / kChunk;
+    return chunks <= 2 ? 1 : chunks > 256 ? 256 : chunks;
+}
+
+size_t plan_workspace(int64_t T, int E) {
+    return kWsHeader + (size_t)plan_blocks(T) * (E + 1) * 4;
+}
+
+hipError_t launch_plan(const PlanArgs& p, hipStream_t s, LaunchInfo* info) {
+    int64_t blocks = plan_blocks(p.T);
+    const int64_t chunks = (p.T + kChunk - 1) / kChunk;
+    const int64_t run = (chunks + blocks - 1) / blocks * kChunk;     // tokens of a block
+    if (blocks > 1)
+        blocks = (p.T + run - 1) / run;
+    hipError_t e = hipSuccess;
+    if (blocks > 1) {
+        hipLaunchKernelGGL(plan_count_kernel, dim3((unsigned)blocks), dim3(kPlanThreads), 0, s, p, run);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess) {
+        hipLaunchKernelGGL(plan_assign_kernel, dim3((unsigned)blocks), dim3(kPlanThreads), 0, s, p, run,
+                           (int)blocks);
+        e = hipGetLastError();
+    }
+    if (info) {
+        snprintf(info->kernel, sizeof info->kernel, "%splan_assign_kernel",
+                 blocks > 1 ? "plan_count_kernel + " : "");
+        info->tm = (int)run;
+        info->tn = p.E;
+        info->waves = kPlanThreads / 64;
+        info->grid = blocks;
+    }
+    return e;
+}
+
+static void rows_info(LaunchInfo* info, const char* name, int dtype, int tokens, int cols, int64_t grid) {
+    if (!info)
+        return;
+    snprintf(info->kernel, sizeof info->kernel, "%s<%s>", name, dtype_name(dtype));
+    info->tm = tokens;
+    info->tn = cols;
+    info->waves = kRowThreads / 64;
+    info->grid = grid;
+}
+
+static int elem_bytes(int dtype) { return dtype == GG_F32 ? 4 : dtype == GG_BF16 || dtype == GG_F16 ? 2 : 1; }
+
+hipError_t launch_permute(const RowsArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
+    const int size = elem_bytes(dtype);
+    const int64_t vecs = ((int64_t)p.width * size + 15) / 16;
+    const int tx = row_threads(vecs), ty = kRowThreads / tx;
+    const int pads = p.E * kPadParts;
+    const dim3 grid((unsigned)(pads + (p.T + ty - 1) / ty), (unsigned)((vecs + tx - 1) / tx));
+    if (size == 1)
+        hipLaunchKernelGGL((permute_kernel<1>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
+    else if (size == 2)
+        hipLaunchKernelGGL((permute_kernel<2>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
+    else
+        hipLaunchKernelGGL((permute_kernel<4>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
+    rows_info(info, "permute_kernel", dtype, ty, tx * 16 / size, (int64_t)grid.x * grid.y);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine(const RowsArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
+    if (p.T == 0)
+        return hipSuccess;
+    const int size = elem_bytes(dtype);
+    const int64_t vecs = ((int64_t)p.width * size + 15) / 16;
+    const int tx = row_threads(vecs), ty = kRowThreads / tx;
+    const dim3 grid((unsigned)((p.T + ty - 1) / ty), (unsigned)((vecs + tx - 1) / tx));
+    if (dtype == GG_BF16)
+        hipLaunchKernelGGL((combine_kernel<GG_BF16>), grid, dim3(kRowThreads), 0, s, p, tx);
+    else if (dtype == GG_F16)
+        hipLaunchKernelGGL((combine_kernel<GG_F16>), grid, dim3(kRowThreads), 0, s, p, tx);
+    else
+        hipLaunchKernelGGL((combine_kernel<GG_F32>), grid, dim3(kRowThreads), 0, s, p, tx);
+    rows_info(info, "combine_kernel", dtype, ty, tx * 16 / size, (int64_t)grid.x * grid.y);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const RowsArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
+    const int pads = p.E * kPadParts;
+    const dim3 grid((unsigned)(pads + p.T));
+    if (dtype == GG_BF16)
+        hipLaunchKernelGGL((combine_bwd_kernel<GG_BF16>), grid, dim3(kRowThreads), 0, s, p, pads);
+    else if (dtype == GG_F16)
+        hipLaunchKernelGGL((combine_bwd_kernel<GG_F16>), grid, dim3(kRowThreads), 0, s, p, pads);
+    else
+        hipLaunchKernelGGL((combine_bwd_kernel<GG_F32>), grid, dim3(kRowThreads), 0, s, p, pads);
+    rows_info(info, "combine_bwd_kernel", dtype, 1, p.width, grid.x);
+    return hipGetLastError();
+}
+
+}  // namespace gg

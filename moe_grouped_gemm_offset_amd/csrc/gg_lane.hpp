@@ -1,0 +1,149 @@
+// gg_lane.hpp -- device helpers of the row-wise kernels (routing, dispatch,
+// clipping): element conversions, vector access at element alignment, and
+// reductions over groups of lanes of a wave.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gg_moe.h"
+
+namespace gg {
+
+// ---- elements ------------------------------------------------------------
+
+template <int DT>
+struct Elem {                                        // GG_BF16 and GG_F16
+    typedef uint16_t T;
+};
+template <>
+struct Elem<GG_F32> {
+    typedef uint32_t T;
+};
+
+template <int DT>
+__device__ __forceinline__ float to_f32(typename Elem<DT>::T u) {
+    if constexpr (DT == GG_BF16)
+        return __builtin_bit_cast(float, (uint32_t)u << 16);
+    else if constexpr (DT == GG_F16)
+        return (float)__builtin_bit_cast(_Float16, u);
+    else
+        return __builtin_bit_cast(float, u);
+}
+
+// fp32 to the element, to nearest even (the only rounding these kernels make)
+template <int DT>
+__device__ __forceinline__ typename Elem<DT>::T from_f32(float f) {
+    if constexpr (DT == GG_BF16)
+        return __builtin_bit_cast(uint16_t, (__bf16)f);
+    else if constexpr (DT == GG_F16)
+        return __builtin_bit_cast(uint16_t, (_Float16)f);
+    else
+        return __builtin_bit_cast(uint32_t, f);
+}
+
+// ---- vectors ---------------------------------------------------------------
+// N elements in one access of up to 16 bytes that needs no more than the
+// element's own alignment: rows of an odd width start anywhere, and global
+// memory takes unaligned vectors.
+
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> {
+    typedef uint32_t T __attribute__((ext_vector_type(4), aligned(1)));
+};
+template <>
+struct Raw<8> {
+    typedef uint32_t T __attribute__((ext_vector_type(2), aligned(1)));
+};
+
+template <int DT, int N>
+struct Vec {
+    static constexpr int kBytes = N * (int)sizeof(typename Elem<DT>::T);
+    typedef typename Raw<kBytes>::T T;
+    T raw;
+
+    __device__ __forceinline__ void load(const typename Elem<DT>::T* p) { raw = *(const T*)p; }
+    __device__ __forceinline__ void store(typename Elem<DT>::T* p) const { *(T*)p = raw; }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (DT == GG_F32)
+            return __builtin_bit_cast(float, (uint32_t)raw[i]);
+        else
+            return to_f32<DT>((uint16_t)(raw[i >> 1] >> (16 * (i & 1))));
+    }
+    __device__ __forceinline__ void set(const float (&f)[N]) {
+        if constexpr (DT == GG_F32) {
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                raw[i] = __builtin_bit_cast(uint32_t, f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 2)
+                raw[i >> 1] = (uint32_t)from_f32<DT>(f[i]) | (uint32_t)from_f32<DT>(f[i + 1]) << 16;
+        }
+    }
+};
+
+// ---- lanes -----------------------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+
+// Combines v over each aligned group of W lanes (4 <= W <= 64, a power of
+// two) with a commutative op; every lane gets the result, the same bits in
+// each.  Whole waves only: every lane must be active.
+template <int W, class T, class Op>
+__device__ __forceinline__ T group_all(T v, Op op) {
+    static_assert(sizeof(T) == 4 && W >= 4 && W <= 64, "32-bit values, groups of 4 to 64 lanes");
+    auto u = [](T x) { return __builtin_bit_cast(uint32_t, x); };
+    auto t = [](uint32_t x) { return __builtin_bit_cast(T, x); };
+    v = op(v, t(lane_dpp<0xB1>(u(v))));              // lane ^ 1
+    v = op(v, t(lane_dpp<0x4E>(u(v))));              // lane ^ 2
+    if constexpr (W >= 8)
+        v = op(v, t(lane_dpp<0x141>(u(v))));         // 7 - lane within eight
+    if constexpr (W >= 16)
+        v = op(v, t(lane_dpp<0x140>(u(v))));         // 15 - lane within sixteen
+    if constexpr (W >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
+        v = op(t(r[0]), t(r[1]));
+    }
+    if constexpr (W >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
+        v = op(t(r[0]), t(r[1]));
+    }
+    return v;
+}
+
+// Orders the LDS accesses of a wave's lanes around it (the hardware keeps a
+// wave's LDS accesses in order; this keeps the compiler from forwarding a
+// lane's own value past another lane's write).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+struct OpMaxU {
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
+};
+struct OpMaxF {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct OpAddF {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// Lowest lane of this lane's group of W for which the predicate holds, as an
+// index within the group (undefined if there is none).
+template <int W>
+__device__ __forceinline__ int group_first(bool pred, int lane) {
+    const uint64_t m = __ballot(pred);
+    if constexpr (W == 64)
+        return __ffsll((unsigned long long)m) - 1;
+    else
+        return __ffs((int)((uint32_t)(m >> (lane & ~(W - 1))) & (W == 32 ? ~0u : (1u << W) - 1u))) - 1;
+}
+
+}  // namespace gg
