@@ -1,0 +1,413 @@
+"""gg_route and gg_route_bwd against a plain implementation in 64 bits (GPU),
+and their refusals (CPU).
+
+Tolerances, from the arithmetic.  The kernels work in fp32 (unit roundoff
+u = 2^-24).  A score is an exp of an argument |a| <= 40 here, scaled by log2(e)
+in fp32 (relative error of the result: |a| log2(e) u + 2 u, under 64 u for the
+scores that matter), divided by a sum of up to 1024 of them (added pairwise
+over lanes, 16 in a row: 32 u): 128 u = 7.6e-6 relative to the row's largest
+weight.  The loss is a sum of such terms: the same bound, relative.  A
+gradient is a difference of products of at most four such factors: 512 u =
+3.1e-5 times the largest magnitude its terms can reach; 16-bit outputs add
+half an ulp (2^-8 bf16, 2^-11 fp16) of the value, fp16 also half of its
+smallest subnormal, 2^-25.
+"""
+import math
+
+import pytest
+import torch
+
+from moe_grouped_gemm_offset_amd import binding as B
+from tests.parity_util import say
+
+INF = float("inf")
+U = 2.0 ** -24
+TINY = 1e-20
+HALF_ULP = {torch.float32: U, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+FLOOR = {torch.float32: 0.0, torch.bfloat16: 0.0, torch.float16: 2.0 ** -25}
+
+
+# --------------------------------------------------------------------------
+# the definition, in 64 bits on the CPU
+# --------------------------------------------------------------------------
+
+def ref_scores(x, softmax):
+    """(scores, balance probabilities), 0 in rows without a finite logit."""
+    if softmax:
+        top = x.max(1, keepdim=True).values
+        e = torch.exp(x - torch.where(top == -INF, torch.zeros_like(top), top))
+        s = e.sum(1, keepdim=True)
+        p = torch.where(s == 0, torch.zeros_like(e), e / torch.where(s == 0, torch.ones_like(s), s))
+        return p, p
+    a = torch.sigmoid(x)
+    return a, a / (a.sum(1, keepdim=True) + TINY)
+
+
+def ref_route(logits, bias, k, softmax, normalize, scale, ids=None):
+    """A dict of the outputs; with ids given, differentiable in `logits`
+    (float64) at that choice."""
+    T, E = logits.shape
+    x = logits
+    if ids is None:
+        key = x.float() + (0.0 if bias is None else bias)
+        ids = torch.full((T, k), -1, dtype=torch.int64)
+        for t in range(T):
+            # NaN first, then by value; ties and equal zeros to the lower index
+            order = sorted((e for e in range(E) if not (x[t, e] == -INF or key[t, e] == -INF)),
+                           key=lambda e: (0, 0.0, e) if math.isnan(key[t, e]) else (1, -float(key[t, e]), e))
+            for j, e in enumerate(order[:k]):
+                ids[t, j] = e
+    there = ids >= 0
+    a, p = ref_scores(x, softmax)
+    at = ids.clamp_min(0)
+    if softmax and normalize:
+        v = torch.where(there, x.gather(1, at), torch.full_like(x[:, :1], -INF))
+        w = ref_scores(v, True)[0]
+    else:
+        w = torch.where(there, a.gather(1, at), torch.zeros_like(x[:, :1]))
+        if normalize:
+            w = w / (w.sum(1, keepdim=True) + TINY)
+    counts = torch.zeros(E, dtype=torch.int64)
+    counts.index_add_(0, at.flatten(), there.flatten().long())
+    n = int(there[:, 0].sum()) if T else 0
+    loss = E / (k * max(n, 1) ** 2) * (counts.double() * p.sum(0)).sum()
+    return dict(ids=ids, prob=scale * w, counts=counts, routed=n, balance=loss)
+
+
+def make_logits(T, E, dtype, seed, masked=0.0, spread=2.0):
+    g = torch.Generator().manual_seed(seed)
+    x = spread * torch.randn(T, E, generator=g)
+    if masked:
+        x[torch.rand(T, E, generator=g) < masked] = -INF
+        x[torch.rand(T, generator=g) < masked] = -INF
+    return x.to(dtype)
+
+
+def run_route(x, k, bias=None, score=B.GG_SOFTMAX, normalize=False, scale=1.0, balance=True, **kw):
+    T, E = x.shape
+    dev = x.device
+    o = dict(ids=torch.full((T, k), -7, dtype=torch.int32, device=dev),
+             prob=torch.full((T, k), float("nan"), device=dev),
+             counts=torch.full((E,), -7, dtype=torch.int32, device=dev),
+             routed=torch.full((1,), -7, dtype=torch.int32, device=dev),
+             balance=torch.full((1,), float("nan"), device=dev) if balance else None)
+    B.gg_route(x, o["ids"], o["prob"], o["counts"], o["routed"], o["balance"], bias=bias, score=score,
+               scale=scale, flags=B.GG_FLAG_NORMALIZE if normalize else 0, **kw)
+    torch.cuda.synchronize()
+    return o
+
+
+def check_route(x, k, bias, score, normalize, scale):
+    o = run_route(x.cuda(), k, None if bias is None else bias.cuda(), score, normalize, scale)
+    r = ref_route(x.double(), bias, k, score == B.GG_SOFTMAX, normalize, scale)
+    assert torch.equal(o["ids"].cpu().long(), r["ids"])
+    assert torch.equal(o["counts"].cpu().long(), r["counts"])
+    assert int(o["routed"]) == r["routed"]
+    err = (o["prob"].cpu().double() - r["prob"]).abs()
+    tol = 128 * U * abs(scale) * torch.ones_like(err)
+    say(f"  prob: worst {float(err.max()) if err.numel() else 0:.2e} of {128 * U * abs(scale):.2e}")
+    assert bool((err <= tol).all())
+    loss = float(r["balance"])
+    say(f"  balance {float(o['balance']):.6f} ref {loss:.6f}")
+    assert abs(float(o["balance"]) - loss) <= 128 * U * abs(loss)
+
+
+SHAPES = [(1, 1, 1), (1, 8, 8), (3, 7, 2), (5, 64, 6), (33, 65, 3), (64, 61, 32), (70, 128, 8),
+          (17, 129, 5), (130, 256, 8), (9, 257, 32), (40, 512, 10), (21, 513, 4), (12, 1000, 16),
+          (6, 1024, 32)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [B.GG_SOFTMAX, B.GG_SIGMOID])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_route(dtype, normalize, score):
+    for i, (T, E, k) in enumerate(SHAPES):
+        say("route", T, E, k, dtype, normalize, score)
+        bias = 0.3 * torch.randn(E, generator=torch.Generator().manual_seed(i)) if i % 2 else None
+        check_route(make_logits(T, E, dtype, 10 + i, masked=0.3 if i % 3 else 0.0), k, bias, score,
+                    normalize, 2.5 if i % 2 else 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [0, 1, 31, 32, 33, 63, 64, 65, 257, 2100])
+def test_route_lengths(T):
+    """Block and wave boundaries, and several blocks joined."""
+    say("route lengths", T)
+    check_route(make_logits(T, 96, torch.float32, T, masked=0.1), 4, None, B.GG_SIGMOID, True, 1.0)
+
+
+@pytest.mark.gpu
+def test_route_ties_zeros_and_masks():
+    """Equal logits go by index; -0 equals +0; rows with fewer live experts
+    than top_k, with none, and of the type's lowest values."""
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        low = torch.finfo(dtype).min
+        E, k = 70, 5
+        x = torch.zeros(8, E, dtype=dtype)
+        x[0, ::2] = -0.0
+        x[1] = 1.0
+        x[1, 69] = 2.0
+        x[2] = -INF
+        x[3] = -INF
+        x[3, 68], x[3, 3] = low, low
+        x[4] = low
+        x[5] = -INF
+        x[5, 66] = 0.5
+        x[6] = low
+        x[6, 40:43] = torch.tensor([3.0, 3.0, -3.0])
+        x[7] = torch.arange(E).flip(0).to(dtype) / 64 - 90
+        for score in (B.GG_SOFTMAX, B.GG_SIGMOID):
+            for normalize in (False, True):
+                say("route ties", dtype, score, normalize)
+                check_route(x, k, None, score, normalize, 1.0)
+
+
+@pytest.mark.gpu
+def test_route_bias_only_chooses():
+    """A bias moves the choice, not the weights; -inf takes an expert out; the
+    weights over a choice far below the row's top stay finite."""
+    x = torch.tensor([[200.0, 1.0, 0.5, -1.0], [0.0, 0.0, 0.0, 0.0]])
+    bias = torch.tensor([-INF, 0.0, 0.0, 5.0])
+    for score in (B.GG_SOFTMAX, B.GG_SIGMOID):
+        for normalize in (False, True):
+            say("route bias", score, normalize)
+            check_route(x, 3, bias, score, normalize, 1.0)
+
+
+@pytest.mark.gpu
+def test_route_nan_and_inf():
+    """NaN and +inf logits: valid, distinct ids (NaN above +inf), NaN where
+    the formulas give it, other tokens untouched."""
+    x = torch.randn(4, 64, generator=torch.Generator().manual_seed(3))
+    x[1, 10], x[1, 5], x[2, 7] = float("nan"), INF, INF
+    o = run_route(x.cuda(), 4)
+    r = ref_route(x.double(), None, 4, True, False, 1.0)
+    assert torch.equal(o["ids"].cpu().long(), r["ids"])
+    assert o["ids"][1, :2].tolist() == [10, 5] and int(o["ids"][2, 0]) == 7
+    prob = o["prob"].cpu().double()
+    assert bool(torch.isnan(prob[1]).all()) and bool(torch.isnan(o["balance"]).all())
+    keep = [0, 3]
+    assert float((prob[keep] - r["prob"][keep]).abs().max()) <= 128 * U
+    s = run_route(x.cuda(), 4, score=B.GG_SIGMOID)
+    assert math.isnan(float(s["prob"][1, 0])) and float(s["prob"][1, 1]) == 1.0
+
+
+@pytest.mark.gpu
+def test_route_pitch_and_no_balance():
+    """Rows at a pitch and an odd start; without the loss the rest is the
+    same, bit for bit."""
+    for dtype in (torch.bfloat16, torch.float32):
+        wide = make_logits(50, 301, dtype, 5).cuda()
+        x = wide[:, 3:3 + 133]
+        a = run_route(x, 6, score=B.GG_SIGMOID, normalize=True)
+        b = run_route(x.contiguous(), 6, score=B.GG_SIGMOID, normalize=True, balance=False)
+        for n in ("ids", "prob", "counts", "routed"):
+            assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.gpu
+def test_route_repeats_bit_for_bit():
+    x = make_logits(5000, 160, torch.bfloat16, 8).cuda()
+    a = run_route(x, 8)
+    for _ in range(3):
+        b = run_route(x, 8)
+        for n in a:
+            assert torch.equal(a[n], b[n]), n
+
+
+# --------------------------------------------------------------------------
+# the gradient
+# --------------------------------------------------------------------------
+
+def run_bwd(x, ids, counts, routed, dprob, score, normalize, scale, row_of=None, dbalance=None):
+    d = torch.full(x.shape, float("nan"), dtype=x.dtype, device=x.device)
+    B.gg_route_bwd(x, ids, counts, routed, dprob, d, row_of=row_of, dbalance=dbalance, score=score,
+                   scale=scale, flags=B.GG_FLAG_NORMALIZE if normalize else 0)
+    torch.cuda.synchronize()
+    return d
+
+
+def ref_bwd(x, ids, k, softmax, normalize, scale, g, db):
+    """The formula's gradient by automatic differentiation in 64 bits."""
+    live = (x > -INF)
+    v = torch.where(live, x.double(), torch.zeros_like(x.double())).requires_grad_(True)
+    # a masked logit takes part as -inf and has no gradient
+    z = torch.where(live, v, torch.full_like(v, -INF))
+    some = live.any(1)
+    z = torch.where(some[:, None], z, torch.zeros_like(z))
+    r = ref_route(z, None, k, softmax, normalize, scale, ids=torch.where(some[:, None], ids, -1))
+    a, p = ref_scores(z, softmax)
+    n = max(int((ids[:, 0] >= 0).sum()), 1)
+    counts = r["counts"].double()
+    loss = x.shape[1] / (k * n * n) * (counts * (p * some[:, None]).sum(0)).sum()
+    total = (torch.where(ids >= 0, r["prob"] * g, torch.zeros_like(g))).sum() + db * loss
+    (d,) = torch.autograd.grad(total, v)
+    d = torch.where(live & some[:, None], torch.nan_to_num(d, nan=0.0), torch.zeros_like(d))
+    return torch.where((ids[:, :1] >= 0), d, torch.zeros_like(d))
+
+
+def check_bwd(T, E, k, dtype, score, normalize, scale, masked, seed, rows=False):
+    softmax = score == B.GG_SOFTMAX
+    x = make_logits(T, E, dtype, seed, masked)
+    f = ref_route(x.double(), None, k, softmax, normalize, scale)
+    gen = torch.Generator().manual_seed(seed + 1)
+    g = torch.randn(T, k, generator=gen)
+    db = 0.7
+    ids = f["ids"].to(torch.int32).cuda()
+    counts = f["counts"].to(torch.int32).cuda()
+    routed = torch.tensor([f["routed"]], dtype=torch.int32).cuda()
+    row_of, dprob = None, g
+    if rows:
+        m = T * k + 5
+        row_of = torch.randperm(m, generator=gen)[: T * k].reshape(T, k).to(torch.int32)
+        row_of[torch.rand(T, k, generator=gen) < 0.2] = -1
+        dprob = torch.full((m,), 1e30)
+        dprob[row_of[row_of >= 0].long()] = g[row_of >= 0]
+        g = torch.where(row_of >= 0, g, torch.zeros_like(g))
+        row_of = row_of.cuda()
+    d = run_bwd(x.cuda(), ids, counts, routed, dprob.cuda(), score, normalize, scale, row_of,
+                torch.tensor([db]).cuda())
+    want = ref_bwd(x, f["ids"], k, softmax, normalize, scale, g.double(), db)
+    # the largest magnitude of a term: scale |g| through weights of at most 1
+    # (k of them in the mean), or the balance loss's E max(counts) / (k n^2)
+    n = max(f["routed"], 1)
+    size = abs(scale) * float(g.abs().max() if g.numel() else 0) * 2 + \
+        db * E * float(f["counts"].max() if E else 0) / (k * n * n) * 2
+    tol = 512 * U * size + (HALF_ULP[dtype] + U) * want.abs() + FLOOR[dtype]
+    err = (d.cpu().double() - want).abs()
+    say(f"  dlogits: worst {float((err / tol).max()) if err.numel() else 0:.3f} of the tolerance")
+    assert not bool(torch.isnan(d).any())
+    assert bool((err <= tol).all())
+    none = f["ids"][:, 0] < 0
+    assert bool((d.cpu()[none] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [B.GG_SOFTMAX, B.GG_SIGMOID])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_route_bwd(dtype, normalize, score):
+    for i, (T, E, k) in enumerate(SHAPES):
+        say("route_bwd", T, E, k, dtype, normalize, score)
+        check_bwd(T, E, k, dtype, score, normalize, 2.5 if i % 2 else 1.0, 0.3 if i % 3 else 0.0, 40 + i,
+                  rows=bool(i % 2))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("score", [B.GG_SOFTMAX, B.GG_SIGMOID])
+def test_route_bwd_differences(score, normalize):
+    """Against central differences of the 64-bit forward at the kernel's own
+    choice; a difference of step h = 1e-4 is off by h^2 / 6 times the third
+    derivative (under 100 here): 2e-7, besides the gradient's tolerance."""
+    T, E, k, scale, db = 3, 12, 4, 1.5, 0.4
+    softmax = score == B.GG_SOFTMAX
+    x = make_logits(T, E, torch.float32, 77, spread=1.0)
+    f = ref_route(x.double(), None, k, softmax, normalize, scale)
+    g = torch.randn(T, k, generator=torch.Generator().manual_seed(78))
+    d = run_bwd(x.cuda(), f["ids"].to(torch.int32).cuda(), f["counts"].to(torch.int32).cuda(),
+                torch.tensor([f["routed"]], dtype=torch.int32).cuda(), g.cuda(), score, normalize, scale,
+                None, torch.tensor([db]).cuda()).cpu().double()
+
+    def total(z):
+        r = ref_route(z, None, k, softmax, normalize, scale, ids=f["ids"])
+        return float((r["prob"] * g.double()).sum() + db * r["balance"])
+
+    h = 1e-4
+    for t in range(T):
+        for e in range(E):
+            z = x.double().clone()
+            z[t, e] += h
+            up = total(z)
+            z[t, e] -= 2 * h
+            slope = (up - total(z)) / (2 * h)
+            assert abs(slope - float(d[t, e])) <= 2e-7 + 512 * U * 20, (t, e)
+
+
+@pytest.mark.gpu
+def test_route_bwd_without_balance_and_extremes():
+    """No balance gradient; logits that underflow every sigmoid; an id past the
+    experts is no choice."""
+    x = torch.full((2, 40), -200.0)
+    x[1] = torch.linspace(-3, 3, 40)
+    ids = torch.tensor([[0, 1], [39, 1000]], dtype=torch.int32)
+    counts = torch.ones(40, dtype=torch.int32)
+    routed = torch.tensor([2], dtype=torch.int32)
+    g = torch.ones(2, 2)
+    for score in (B.GG_SOFTMAX, B.GG_SIGMOID):
+        for normalize in (False, True):
+            d = run_bwd(x.cuda(), ids.cuda(), counts.cuda(), routed.cuda(), g.cuda(), score, normalize, 1.0)
+            want = ref_bwd(x, torch.where(ids < 40, ids, -1).long(), 2, score == B.GG_SOFTMAX, normalize,
+                           1.0, g.double(), 0.0)
+            assert float((d.cpu().double() - want).abs().max()) <= 512 * U * 2
+
+
+# --------------------------------------------------------------------------
+# refusals, on the host (no GPU)
+# --------------------------------------------------------------------------
+
+P, WS = 1 << 20, 1 << 24
+NULL, SHAPE, DTYPE, LAYOUT, ALIGN, MODE, WORKSPACE, UNSUPPORTED, VALUE = 1, 2, 3, 4, 5, 6, 7, 8, 12
+
+
+def c_route(**kw):
+    a = dict(logits=P, dtype=0, ld=64, T=16, E=64, bias=None, k=4, score=0, scale=1.0, flags=0, ids=P,
+             prob=P, counts=P, routed=P, balance=P, ws=WS, wsb=1 << 20)
+    a.update(kw)
+    return B.load_library().gg_route(a["logits"], a["dtype"], a["ld"], a["T"], a["E"], a["bias"], a["k"],
+                                     a["score"], a["scale"], a["flags"], a["ids"], a["prob"], a["counts"],
+                                     a["routed"], a["balance"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(logits=None), NULL), (dict(ids=None), NULL), (dict(prob=None), NULL),
+    (dict(counts=None), NULL), (dict(routed=None), NULL), (dict(ws=None), NULL),
+    (dict(dtype=3), DTYPE), (dict(E=0), SHAPE), (dict(E=1025, ld=2000), SHAPE), (dict(T=-1), SHAPE),
+    (dict(T=(1 << 23) + 1), UNSUPPORTED), (dict(k=0), SHAPE), (dict(k=33), UNSUPPORTED),
+    (dict(E=3, k=4), SHAPE), (dict(ld=63), LAYOUT), (dict(score=2), MODE), (dict(flags=4), MODE),
+    (dict(scale=float("inf")), VALUE), (dict(scale=float("nan")), VALUE), (dict(logits=P + 1), ALIGN),
+    (dict(ids=P + 2), ALIGN), (dict(balance=P + 1), ALIGN), (dict(ws=WS + 8), ALIGN),
+    (dict(wsb=16), WORKSPACE),
+])
+def test_route_rejects(kw, status):
+    assert c_route(**kw) == status
+    assert B.gg_last_error() != ""
+
+
+def c_bwd(**kw):
+    a = dict(logits=P, dtype=0, ld=64, T=16, E=64, k=4, score=0, scale=1.0, flags=0, ids=P, counts=P,
+             routed=P, dprob=P, row_of=None, m=0, db=None, dl=P)
+    a.update(kw)
+    return B.load_library().gg_route_bwd(a["logits"], a["dtype"], a["ld"], a["T"], a["E"], a["k"],
+                                         a["score"], a["scale"], a["flags"], a["ids"], a["counts"],
+                                         a["routed"], a["dprob"], a["row_of"], a["m"], a["db"], a["dl"],
+                                         None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(ids=None), NULL), (dict(counts=None), NULL), (dict(routed=None), NULL), (dict(dprob=None), NULL),
+    (dict(dl=None), NULL), (dict(dl=P + 1), ALIGN), (dict(dprob=P + 2), ALIGN), (dict(db=P + 2), ALIGN),
+    (dict(row_of=P, m=-1), SHAPE), (dict(row_of=P, m=1 << 31), SHAPE), (dict(dtype=4), DTYPE),
+    (dict(flags=64 + 1), MODE), (dict(k=65), UNSUPPORTED), (dict(ld=1), LAYOUT),
+])
+def test_route_bwd_rejects(kw, status):
+    assert c_bwd(**kw) == status
+
+
+def test_binding_rejects():
+    """The binding checks types, shapes and layouts before the call."""
+    x = torch.zeros(4, 8)
+    i32, f32 = torch.int32, torch.float32
+    good = dict(ids=torch.zeros(4, 2, dtype=i32), prob=torch.zeros(4, 2), counts=torch.zeros(8, dtype=i32),
+                routed=torch.zeros(1, dtype=i32))
+    bad = [dict(ids=torch.zeros(4, 2, dtype=torch.int64)), dict(prob=torch.zeros(4, 3)),
+           dict(counts=torch.zeros(7, dtype=i32)), dict(routed=torch.zeros(1, dtype=f32)),
+           dict(prob=torch.zeros(2, 4).t()), dict(balance=torch.zeros(2)), dict(bias=torch.zeros(9))]
+    for b in bad:
+        with pytest.raises(B.GGError):
+            B.gg_route(x, workspace=torch.zeros(1 << 16, dtype=torch.uint8), **{**good, **b})
+    with pytest.raises(B.GGError):
+        B.gg_route(torch.zeros(8, 4).t(), workspace=torch.zeros(1 << 16, dtype=torch.uint8), **good)
+    with pytest.raises(B.GGError):
+        B.gg_route(x.double(), workspace=torch.zeros(1 << 16, dtype=torch.uint8), **good)
