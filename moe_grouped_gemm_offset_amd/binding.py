@@ -322,32 +322,61 @@ def gg_dsrelu(a, sfa, b, sfb, b_ptrs, sfb_ptrs, n, c, padded_offsets, alpha, pro
 # around the grouped GEMMs: router, dispatch and combine, gradient clipping
 # --------------------------------------------------------------------------
 
-def _need(t, what, shape, dtypes, like=None, rows=False):
-    """Checks a tensor argument: type, shape (None: any extent), device, and
-    that it is contiguous (rows: that each row is, at any pitch)."""
-    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+def _refuse(t, what, shape, dtype, dev, rows):
+    """Raises what _need or _need_rows found wrong with a tensor argument."""
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+        raise GGError(3, f"{what} has dtype {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise GGError(2, f"{what} has shape {tuple(t.shape)}, not {shape}")
+    if t.get_device() != dev:
+        raise GGError(9, f"{what} is on {t.device}, not on the device of the other arguments")
+    raise GGError(4, f"{what} needs contiguous rows that do not overlap" if rows
+                  else f"{what} must be contiguous")
+
+
+def _need(t, what, shape, dtype, dev):
+    """The address of a tensor argument of this shape, type and device index,
+    contiguous; raises otherwise.  (Written for few steps: a call's host time
+    is what a small call costs.)"""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse(t, what, shape, dtype, dev, False)
+
+
+def _need_rows(t, what, dtypes):
+    """(address, rows, columns, row pitch, device index) of a matrix of one of
+    the types whose rows are contiguous, at any pitch."""
     if t.dtype not in dtypes:
-        raise GGError(3, f"{what} has dtype {t.dtype}, not {' or '.join(map(str, dtypes))}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise GGError(2, f"{what} has shape {tuple(t.shape)}, not "
-                         f"{tuple('any' if n is None else n for n in shape)}")
-    if like is not None and t.device != like.device:
-        raise GGError(9, f"{what} is on {t.device}, not {like.device}")
-    if rows:
-        if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or
-                          (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
-            raise GGError(4, f"{what} needs contiguous rows that do not overlap")
-    elif not t.is_contiguous():
-        raise GGError(4, f"{what} must be contiguous")
-    return t
+        _refuse(t, what, t.shape, dtypes, t.get_device(), True)
+    if t.dim() != 2:
+        raise GGError(2, f"{what} has shape {tuple(t.shape)}, not two dimensions")
+    n, width = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), n, width, width, t.get_device()
+    pitch, step = t.stride()
+    if n * width and ((width > 1 and step != 1) or (n > 1 and pitch < width)):
+        _refuse(t, what, t.shape, t.dtype, t.get_device(), True)
+    return t.data_ptr(), n, width, pitch if n > 1 else width, t.get_device()
 
 
-def _pitch(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _extent(t, what):
+    """The length of a one-dimensional tensor argument."""
+    if t.dim() != 1:
+        raise GGError(2, f"{what} has shape {tuple(t.shape)}, not one dimension")
+    return t.shape[0]
+
+
+def _raw_stream(stream, dev):
+    """The hipStream_t of a call's stream argument (None: the current stream of
+    the arguments' device)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 _BYTES = (torch.float8_e4m3fn, torch.float8_e5m2, torch.uint8)
+_I32, _F32 = torch.int32, torch.float32
 
 
 def gg_route_workspace_size(tokens, num_experts):
@@ -372,21 +401,18 @@ def gg_route(logits, ids, prob, counts, routed, balance=None, bias=None, score=G
     int32 and prob float32 (T, top_k), counts int32 (E,), routed int32 (1,)
     and balance float32 (1,) are written.  Returns the workspace used."""
     L = load_library()
-    _need(logits, "logits", (None, None), _FLOATS, rows=True)
-    T, E = logits.shape
+    px, T, E, ld, dev = _need_rows(logits, "logits", _FLOATS)
     k = ids.shape[-1]
-    _need(ids, "ids", (T, k), torch.int32, logits)
-    _need(prob, "prob", (T, k), torch.float32, logits)
-    _need(counts, "counts", (E,), torch.int32, logits)
-    _need(routed, "routed", (1,), torch.int32, logits)
-    if balance is not None:
-        _need(balance, "balance", (1,), torch.float32, logits)
-    if bias is not None:
-        _need(bias, "bias", (E,), torch.float32, logits)
-    ws, nbytes = _workspace(workspace, L.gg_route_workspace_size(T, E), logits, stream)
-    _check(L.gg_route(_ptr(logits), _TORCH_DTYPE[logits.dtype], _pitch(logits), T, E, _ptr(bias), k,
-                      score, scale, flags, _ptr(ids), _ptr(prob), _ptr(counts), _ptr(routed),
-                      _ptr(balance), _ptr(ws), nbytes, _stream(stream)))
+    p_ids = _need(ids, "ids", (T, k), _I32, dev)
+    p_prob = _need(prob, "prob", (T, k), _F32, dev)
+    p_counts = _need(counts, "counts", (E,), _I32, dev)
+    p_routed = _need(routed, "routed", (1,), _I32, dev)
+    p_bal = None if balance is None else _need(balance, "balance", (1,), _F32, dev)
+    p_bias = None if bias is None else _need(bias, "bias", (E,), _F32, dev)
+    ws, nbytes = _workspace(workspace, L.gg_route_workspace_size(T, E) if workspace is None else 0,
+                            logits, stream)
+    _check(L.gg_route(px, _TORCH_DTYPE[logits.dtype], ld, T, E, p_bias, k, score, scale, flags, p_ids,
+                      p_prob, p_counts, p_routed, p_bal, ws.data_ptr(), nbytes, _raw_stream(stream, dev)))
     return ws
 
 
@@ -396,25 +422,20 @@ def gg_route_bwd(logits, ids, counts, routed, dprob, dlogits, row_of=None, dbala
     float32: (T, top_k), or with row_of (T, top_k) one value per expert row,
     (m_rows,), as gg_dglu and gg_dsrelu write it."""
     L = load_library()
-    _need(logits, "logits", (None, None), _FLOATS, rows=True)
-    T, E = logits.shape
+    px, T, E, ld, dev = _need_rows(logits, "logits", _FLOATS)
     k = ids.shape[-1]
-    _need(ids, "ids", (T, k), torch.int32, logits)
-    _need(counts, "counts", (E,), torch.int32, logits)
-    _need(routed, "routed", (1,), torch.int32, logits)
-    m = 0
+    p_ids = _need(ids, "ids", (T, k), _I32, dev)
+    p_counts = _need(counts, "counts", (E,), _I32, dev)
+    p_routed = _need(routed, "routed", (1,), _I32, dev)
     if row_of is None:
-        _need(dprob, "dprob", (T, k), torch.float32, logits)
+        m, p_row, p_dprob = 0, None, _need(dprob, "dprob", (T, k), _F32, dev)
     else:
-        _need(row_of, "row_of", (T, k), torch.int32, logits)
-        _need(dprob, "dprob", (None,), torch.float32, logits)
-        m = dprob.shape[0]
-    if dbalance is not None:
-        _need(dbalance, "dbalance", (1,), torch.float32, logits)
-    _need(dlogits, "dlogits", (T, E), logits.dtype, logits)
-    _check(L.gg_route_bwd(_ptr(logits), _TORCH_DTYPE[logits.dtype], _pitch(logits), T, E, k, score,
-                          scale, flags, _ptr(ids), _ptr(counts), _ptr(routed), _ptr(dprob),
-                          _ptr(row_of), m, _ptr(dbalance), _ptr(dlogits), _stream(stream)))
+        m = _extent(dprob, "dprob")
+        p_row, p_dprob = _need(row_of, "row_of", (T, k), _I32, dev), _need(dprob, "dprob", (m,), _F32, dev)
+    p_db = None if dbalance is None else _need(dbalance, "dbalance", (1,), _F32, dev)
+    p_d = _need(dlogits, "dlogits", (T, E), logits.dtype, dev)
+    _check(L.gg_route_bwd(px, _TORCH_DTYPE[logits.dtype], ld, T, E, k, score, scale, flags, p_ids,
+                          p_counts, p_routed, p_dprob, p_row, m, p_db, p_d, _raw_stream(stream, dev)))
 
 
 def gg_plan(ids, counts, padded_offsets, row_of, m_rows, granule=256, prob=None, prob_rows=None,
@@ -424,20 +445,20 @@ def gg_plan(ids, counts, padded_offsets, row_of, m_rows, granule=256, prob=None,
     row_of int32 (T, top_k) and prob_rows float32 (m_rows,) are written.
     Returns the workspace used (gg_device_error reads its error word)."""
     L = load_library()
-    _need(ids, "ids", (None, None), torch.int32)
-    T, k = ids.shape
-    _need(counts, "counts", (None,), torch.int32, ids)
-    E = counts.shape[0]
-    _need(padded_offsets, "padded_offsets", (E,), torch.int32, ids)
-    _need(row_of, "row_of", (T, k), torch.int32, ids)
-    if prob is not None:
-        _need(prob, "prob", (T, k), torch.float32, ids)
-    if prob_rows is not None:
-        _need(prob_rows, "prob_rows", (m_rows,), torch.float32, ids)
-    ws, nbytes = _workspace(workspace, L.gg_plan_workspace_size(T, E), ids, stream)
-    _check(L.gg_plan(_ptr(ids), T, k, E, granule, m_rows, _ptr(prob), _ptr(counts),
-                     _ptr(padded_offsets), _ptr(row_of), _ptr(prob_rows), _ptr(ws), nbytes,
-                     _stream(stream)))
+    if ids.dim() != 2:
+        raise GGError(2, f"ids has shape {tuple(ids.shape)}, not two dimensions")
+    shape, dev, E = ids.shape, ids.get_device(), _extent(counts, "counts")
+    T, k = shape
+    p_ids = _need(ids, "ids", shape, _I32, dev)
+    p_counts = _need(counts, "counts", (E,), _I32, dev)
+    p_ends = _need(padded_offsets, "padded_offsets", (E,), _I32, dev)
+    p_row = _need(row_of, "row_of", shape, _I32, dev)
+    p_prob = None if prob is None else _need(prob, "prob", shape, _F32, dev)
+    p_rows = None if prob_rows is None else _need(prob_rows, "prob_rows", (m_rows,), _F32, dev)
+    ws, nbytes = _workspace(workspace, L.gg_plan_workspace_size(T, E) if workspace is None else 0,
+                            ids, stream)
+    _check(L.gg_plan(p_ids, T, k, E, granule, m_rows, p_prob, p_counts, p_ends, p_row, p_rows,
+                     ws.data_ptr(), nbytes, _raw_stream(stream, dev)))
     return ws
 
 
@@ -446,32 +467,27 @@ def gg_permute(x, row_of, counts, padded_offsets, x_rows, stream=None):
     gg_moe.h): x (T, width) at any row pitch, x_rows (m_rows, width); one- to
     four-byte types."""
     L = load_library()
-    _need(x, "x", (None, None), _FLOATS + _BYTES, rows=True)
-    T, width = x.shape
-    k = row_of.shape[-1]
-    _need(row_of, "row_of", (T, k), torch.int32, x)
-    _need(counts, "counts", (None,), torch.int32, x)
-    E = counts.shape[0]
-    _need(padded_offsets, "padded_offsets", (E,), torch.int32, x)
-    _need(x_rows, "x_rows", (None, width), x.dtype, x)
-    _check(L.gg_permute(_ptr(x), _TORCH_DTYPE.get(x.dtype, GG_F8E4M3), _pitch(x), T, width,
-                        _ptr(row_of), k, _ptr(counts), _ptr(padded_offsets), E, x_rows.shape[0],
-                        _ptr(x_rows), _stream(stream)))
+    px, T, width, ld, dev = _need_rows(x, "x", _FLOATS + _BYTES)
+    k, E, m = row_of.shape[-1], _extent(counts, "counts"), x_rows.shape[0]
+    p_row = _need(row_of, "row_of", (T, k), _I32, dev)
+    p_counts = _need(counts, "counts", (E,), _I32, dev)
+    p_ends = _need(padded_offsets, "padded_offsets", (E,), _I32, dev)
+    p_out = _need(x_rows, "x_rows", (m, width), x.dtype, dev)
+    _check(L.gg_permute(px, _TORCH_DTYPE.get(x.dtype, GG_F8E4M3), ld, T, width, p_row, k, p_counts,
+                        p_ends, E, m, p_out, _raw_stream(stream, dev)))
 
 
 def gg_combine(y_rows, row_of, out, weights=None, stream=None):
     """out[t] = sum_j weights[t, j] y_rows[row_of[t, j]] (gg_combine of
     gg_moe.h); weights None: 1.  out (T, width) at any row pitch."""
     L = load_library()
-    _need(out, "out", (None, None), _FLOATS, rows=True)
-    T, width = out.shape
-    k = row_of.shape[-1]
-    _need(y_rows, "y_rows", (None, width), out.dtype, out)
-    _need(row_of, "row_of", (T, k), torch.int32, out)
-    if weights is not None:
-        _need(weights, "weights", (T, k), torch.float32, out)
-    _check(L.gg_combine(_ptr(y_rows), _TORCH_DTYPE[out.dtype], y_rows.shape[0], width, _ptr(row_of), T,
-                        k, _ptr(weights), _ptr(out), _pitch(out), _stream(stream)))
+    p_out, T, width, ld, dev = _need_rows(out, "out", _FLOATS)
+    k, m = row_of.shape[-1], y_rows.shape[0]
+    p_y = _need(y_rows, "y_rows", (m, width), out.dtype, dev)
+    p_row = _need(row_of, "row_of", (T, k), _I32, dev)
+    p_w = None if weights is None else _need(weights, "weights", (T, k), _F32, dev)
+    _check(L.gg_combine(p_y, _TORCH_DTYPE[out.dtype], m, width, p_row, T, k, p_w, p_out, ld,
+                        _raw_stream(stream, dev)))
 
 
 def gg_combine_bwd(dout, y_rows, row_of, weights, counts, padded_offsets, dy_rows, dweights,
@@ -479,21 +495,17 @@ def gg_combine_bwd(dout, y_rows, row_of, weights, counts, padded_offsets, dy_row
     """The gradients of gg_combine (gg_combine_bwd of gg_moe.h): dy_rows
     (m_rows, width), zeros in the padding, and dweights float32 (T, top_k)."""
     L = load_library()
-    _need(dout, "dout", (None, None), _FLOATS, rows=True)
-    T, width = dout.shape
-    k = row_of.shape[-1]
-    _need(y_rows, "y_rows", (None, width), dout.dtype, dout)
-    m = y_rows.shape[0]
-    _need(row_of, "row_of", (T, k), torch.int32, dout)
-    _need(weights, "weights", (T, k), torch.float32, dout)
-    _need(counts, "counts", (None,), torch.int32, dout)
-    E = counts.shape[0]
-    _need(padded_offsets, "padded_offsets", (E,), torch.int32, dout)
-    _need(dy_rows, "dy_rows", (m, width), dout.dtype, dout)
-    _need(dweights, "dweights", (T, k), torch.float32, dout)
-    _check(L.gg_combine_bwd(_ptr(dout), _TORCH_DTYPE[dout.dtype], _pitch(dout), T, width, _ptr(y_rows),
-                            m, _ptr(weights), _ptr(row_of), k, _ptr(counts), _ptr(padded_offsets), E,
-                            _ptr(dy_rows), _ptr(dweights), _stream(stream)))
+    p_d, T, width, ld, dev = _need_rows(dout, "dout", _FLOATS)
+    k, E, m = row_of.shape[-1], _extent(counts, "counts"), y_rows.shape[0]
+    p_y = _need(y_rows, "y_rows", (m, width), dout.dtype, dev)
+    p_row = _need(row_of, "row_of", (T, k), _I32, dev)
+    p_w = _need(weights, "weights", (T, k), _F32, dev)
+    p_counts = _need(counts, "counts", (E,), _I32, dev)
+    p_ends = _need(padded_offsets, "padded_offsets", (E,), _I32, dev)
+    p_dy = _need(dy_rows, "dy_rows", (m, width), dout.dtype, dev)
+    p_dw = _need(dweights, "dweights", (T, k), _F32, dev)
+    _check(L.gg_combine_bwd(p_d, _TORCH_DTYPE[dout.dtype], ld, T, width, p_y, m, p_w, p_row, k, p_counts,
+                            p_ends, E, p_dy, p_dw, _raw_stream(stream, dev)))
 
 
 def grad_table(tensors):
@@ -518,12 +530,9 @@ def grad_table(tensors):
 
 
 def _need_table(ptrs, ends, dtypes, sumsq):
-    _need(ptrs, "ptrs", (None,), torch.int64)
-    n = ptrs.shape[0]
-    _need(ends, "ends", (n,), torch.int64, ptrs)
-    _need(dtypes, "dtypes", (n,), torch.int32, ptrs)
-    _need(sumsq, "sumsq", (1,), torch.float64, ptrs)
-    return n
+    n, dev = _extent(ptrs, "ptrs"), ptrs.get_device()
+    return (_need(ptrs, "ptrs", (n,), torch.int64, dev), _need(ends, "ends", (n,), torch.int64, dev),
+            _need(dtypes, "dtypes", (n,), _I32, dev), n, _need(sumsq, "sumsq", (1,), torch.float64, dev), dev)
 
 
 def gg_grad_norm(ptrs, ends, dtypes, total, sumsq, accumulate=False, workspace=None, stream=None):
@@ -531,10 +540,10 @@ def gg_grad_norm(ptrs, ends, dtypes, total, sumsq, accumulate=False, workspace=N
     (gg_grad_norm of gg_moe.h; grad_table makes the first four arguments).
     Returns the workspace used."""
     L = load_library()
-    n = _need_table(ptrs, ends, dtypes, sumsq)
-    ws, nbytes = _workspace(workspace, L.gg_grad_workspace_size(), ptrs, stream)
-    _check(L.gg_grad_norm(_ptr(ptrs), _ptr(ends), _ptr(dtypes), n, total, _ptr(sumsq),
-                          int(bool(accumulate)), _ptr(ws), nbytes, _stream(stream)))
+    p_ptrs, p_ends, p_dt, n, p_sum, dev = _need_table(ptrs, ends, dtypes, sumsq)
+    ws, nbytes = _workspace(workspace, L.gg_grad_workspace_size() if workspace is None else 0, ptrs, stream)
+    _check(L.gg_grad_norm(p_ptrs, p_ends, p_dt, n, total, p_sum, int(bool(accumulate)), ws.data_ptr(),
+                          nbytes, _raw_stream(stream, dev)))
     return ws
 
 
@@ -544,9 +553,8 @@ def gg_grad_clip(ptrs, ends, dtypes, total, sumsq, max_norm, norm, eps=1e-6, out
     or into out_ptrs' tensors; norm (float32, (2,)) = the norm and the factor
     (gg_grad_clip of gg_moe.h)."""
     L = load_library()
-    n = _need_table(ptrs, ends, dtypes, sumsq)
-    _need(norm, "norm", (2,), torch.float32, ptrs)
-    if out_ptrs is not None:
-        _need(out_ptrs, "out_ptrs", (n,), torch.int64, ptrs)
-    _check(L.gg_grad_clip(_ptr(ptrs), _ptr(ends), _ptr(dtypes), n, total, _ptr(sumsq), max_norm, eps,
-                          _ptr(norm), _ptr(out_ptrs), _stream(stream)))
+    p_ptrs, p_ends, p_dt, n, p_sum, dev = _need_table(ptrs, ends, dtypes, sumsq)
+    p_norm = _need(norm, "norm", (2,), _F32, dev)
+    p_out = None if out_ptrs is None else _need(out_ptrs, "out_ptrs", (n,), torch.int64, dev)
+    _check(L.gg_grad_clip(p_ptrs, p_ends, p_dt, n, total, p_sum, max_norm, eps, p_norm, p_out,
+                          _raw_stream(stream, dev)))
