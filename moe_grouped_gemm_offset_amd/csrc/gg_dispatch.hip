@@ -20,132 +20,172 @@ namespace {
 // plan_assign_kernel counts for itself.
 //
 // An id outside 0 .. E-1, or one that its token has already used, has no row.
+// A second use shows as a bit that was set before; only a chunk with one
+// looks for the first uses.
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kChunk = 256;                          // tokens of a bitmap
 constexpr int kWords = kChunk / 32;
 constexpr int kMaxExperts = 1024;
 
-// Whether slot i (token t, choice j) of the ids has a row; f |= a flag if the
-// id is neither a valid one nor -1.
-__device__ __forceinline__ bool plan_slot(const PlanArgs& p, int64_t i, int64_t t, int& e, int& f) {
-    e = p.ids[i];
-    if (e < 0 || e >= p.E) {
-        if (e != -1)
-            f |= GG_DEVERR_IDS;
-        return false;
-    }
-    for (int64_t q = t * p.k; q < i; q++)
-        if (p.ids[q] == e) {
-            f |= GG_DEVERR_IDS;
+// i / k for slots i of a chunk (i < 256 * 32, k <= 32): with m = ceil(2^18 /
+// k), i m / 2^18 exceeds i / k by less than i k / (2^18 k) < 1 / k.
+struct SlotDiv {
+    uint32_t m;
+    __device__ explicit SlotDiv(int k) : m(((1u << 18) + k - 1) / k) {}
+    __device__ __forceinline__ int operator()(int i) const { return (int)(((uint32_t)i * m) >> 18); }
+};
+
+// Whether slot i of the chunk's ids (token t of it) is its token's first use
+// of its expert.
+__device__ __forceinline__ bool first_use(const int32_t* ids, int i, int t, int k, int e) {
+    for (int q = t * k; q < i; q++)
+        if (ids[q] == e)
             return false;
-        }
     return true;
 }
 
-// Sets the chunk's bits; every thread of the block calls it.
-__device__ void plan_bits(const PlanArgs& p, int64_t t0, uint32_t* bits, int& f) {
-    for (int i = threadIdx.x; i < p.E * kWords; i += kPlanThreads)
-        bits[i] = 0;
-    __syncthreads();
-    const int64_t t1 = min(p.T, t0 + kChunk);
-    for (int64_t i = t0 * p.k + threadIdx.x; i < t1 * p.k; i += kPlanThreads) {
-        const int64_t t = i / p.k;
-        int e;
-        if (plan_slot(p, i, t, e, f)) {
-            const int b = (int)(t - t0);
-            atomicOr(&bits[e * kWords + (b >> 5)], 1u << (b & 31));
+// Sets the bits of a chunk of n tokens (bit t % 32 of bits[t / 32 * E + e]);
+// every thread of the block calls it.  bits holds zeros on entry.  Returns
+// whether a token uses an expert twice; f |= a flag for ids that are neither
+// an expert nor -1, or used twice.
+__device__ __forceinline__ bool plan_bits(const PlanArgs& p, const int32_t* ids, int n, SlotDiv div,
+                                          uint32_t* bits, int32_t* twice, int& f) {
+    for (int i = threadIdx.x; i < n * p.k; i += kPlanThreads) {
+        const int e = ids[i], t = div(i);
+        if (e >= 0 && e < p.E) {
+            const uint32_t bit = 1u << (t & 31);
+            if (atomicOr(&bits[(t >> 5) * p.E + e], bit) & bit) {
+                *twice = 1;
+                f |= GG_DEVERR_IDS;
+            }
+        } else if (e != -1) {
+            f |= GG_DEVERR_IDS;
         }
     }
     __syncthreads();
+    return *twice != 0;
 }
 
-__device__ __forceinline__ int plan_ones(const uint32_t* bits, int e) {
+__device__ __forceinline__ int plan_ones(const uint32_t* bits, int E, int e) {
     int c = 0;
 #pragma unroll
     for (int w = 0; w < kWords; w++)
-        c += __popc(bits[e * kWords + w]);
+        c += __popc(bits[w * E + e]);
     return c;
 }
 
-// Workspace: header (int32 0: the error word), then [blocks][E + 1] int32:
-// each block's counts and its flags.
+__device__ __forceinline__ void plan_clear(uint32_t* bits, int E) {
+    for (int i = threadIdx.x; i < E * kWords; i += kPlanThreads)
+        bits[i] = 0;
+    __syncthreads();
+}
+
+// Workspace: header (int32 0: the error word), then [blocks][E] int32 counts
+// and [blocks] flags.
 __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(PlanArgs p, int64_t run) {
     __shared__ uint32_t bits[kMaxExperts * kWords];
-    __shared__ int32_t flags;
+    __shared__ int32_t flags, twice;
     const int e = threadIdx.x;
     if (e == 0)
-        flags = 0;
+        flags = twice = 0;
+    const SlotDiv div(p.k);
     int count = 0, f = 0;
     const int64_t t1 = min(p.T, (int64_t)(blockIdx.x + 1) * run);
     for (int64_t t = blockIdx.x * run; t < t1; t += kChunk) {
-        plan_bits(p, t, bits, f);
+        plan_clear(bits, p.E);
+        plan_bits(p, p.ids + t * p.k, (int)min((int64_t)kChunk, t1 - t), div, bits, &twice, f);
         if (e < p.E)
-            count += plan_ones(bits, e);
+            count += plan_ones(bits, p.E, e);
         __syncthreads();
     }
     if (f)
         atomicOr(&flags, f);
     __syncthreads();
-    int32_t* part = p.ws + kWsHeader / 4 + (int64_t)blockIdx.x * (p.E + 1);
+    int32_t* part = p.ws + kWsHeader / 4;
     if (e < p.E)
-        part[e] = count;
+        part[(int64_t)blockIdx.x * p.E + e] = count;
     if (e == 0)
-        part[p.E] = flags;
+        part[(int64_t)gridDim.x * p.E + blockIdx.x] = flags;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_assign_kernel(PlanArgs p, int64_t run, int blocks) {
+__global__ void __launch_bounds__(kPlanThreads) plan_assign_kernel(PlanArgs p, int64_t run, int blocks,
+                                                                   int lanes) {
     __shared__ uint32_t bits[kMaxExperts * kWords];
     __shared__ int32_t base[kMaxExperts];            // row of the block's next token of an expert
     __shared__ int32_t stop[kMaxExperts];            // end of the group, within m_rows
     __shared__ int32_t fill[kMaxExperts];            // first padding row
-    __shared__ int64_t scan[kPlanThreads];
-    __shared__ int32_t flags;
-    const int e = threadIdx.x, E = p.E;
+    __shared__ int32_t wave_sums[kPlanWaves];
+    __shared__ int32_t flags, twice;
+    const int e = threadIdx.x, E = p.E, lane = e & 63, wave = e >> 6;
+    const SlotDiv div(p.k);
     if (e == 0)
-        flags = 0;
+        flags = twice = 0;
+    base[e] = stop[e] = 0;
+    plan_clear(bits, E);
     int f = 0;
     // counts of the blocks before this one, and of all
     int before = 0, all = 0;
+    bool dup = false;
     if (blocks > 1) {
-        if (e < E) {
-            for (int b = 0; b < blocks; b++) {
-                const int c = p.ws[kWsHeader / 4 + (int64_t)b * (E + 1) + e];
-                before += b < (int)blockIdx.x ? c : 0;
-                all += c;
+        // `lanes` threads along the experts (a power of two >= E), the rest
+        // along the blocks
+        const int x = e & (lanes - 1), rows = kPlanThreads / lanes;
+        const int32_t* part = p.ws + kWsHeader / 4;
+        int b0 = 0, a0 = 0;
+        if (x < E) {
+#pragma unroll 8
+            for (int b = e / lanes; b < blocks; b += rows) {
+                const int c = part[(int64_t)b * E + x];
+                b0 += b < (int)blockIdx.x ? c : 0;
+                a0 += c;
             }
+            atomicAdd(&base[x], b0);
+            atomicAdd(&stop[x], a0);
         }
         if (blockIdx.x == 0 && e < blocks)
-            f |= p.ws[kWsHeader / 4 + (int64_t)e * (E + 1) + E];
+            f |= part[(int64_t)blocks * E + e];
+        __syncthreads();
+        before = base[e];
+        all = stop[e];
+        __syncthreads();
     } else {
         for (int64_t t = 0; t < p.T; t += kChunk) {
-            plan_bits(p, t, bits, f);
+            if (t)
+                plan_clear(bits, E);
+            dup = plan_bits(p, p.ids + t * p.k, (int)min((int64_t)kChunk, p.T - t), div, bits, &twice, f);
             if (e < E)
-                all += plan_ones(bits, e);
+                all += plan_ones(bits, E, e);
             __syncthreads();
         }
     }
-    // the padded groups' ends: a scan over the experts
-    const int64_t padded = e < E ? ((int64_t)all + p.granule - 1) / p.granule * p.granule : 0;
-    scan[e] = padded;
-    __syncthreads();
-    for (int h = 1; h < kPlanThreads; h <<= 1) {
-        const int64_t v = e >= h ? scan[e - h] : 0;
-        __syncthreads();
-        scan[e] += v;
-        __syncthreads();
+    // the padded groups' ends: a scan over the experts (below 2^31: at most
+    // 2^28 choices and 255 rows of padding for each expert)
+    const int padded = e < E ? (all + p.granule - 1) & -p.granule : 0;
+    int sum = padded;
+#pragma unroll
+    for (int h = 1; h < 64; h <<= 1) {
+        const int v = __shfl_up(sum, h);
+        sum += lane >= h ? v : 0;
     }
+    if (lane == 63)
+        wave_sums[wave] = sum;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; w++)
+        sum += w < wave ? wave_sums[w] : 0;
     // groups are cut off where the rows end
-    const int64_t limit = p.m_rows / p.granule * p.granule;
-    const int64_t b0 = min(scan[e] - padded, limit), b1 = min(scan[e], limit);
-    const int kept = (int)min((int64_t)all, b1 - b0);
+    const int limit = (int)(p.m_rows & -(int64_t)p.granule);
+    const int b0 = min(sum - padded, limit), b1 = min(sum, limit);
+    const int kept = min(all, b1 - b0);
     if (e < E) {
-        base[e] = (int)(b0 + min((int64_t)before, b1 - b0));
-        stop[e] = (int)b1;
-        fill[e] = (int)(b0 + kept);
+        base[e] = b0 + min(before, b1 - b0);
+        stop[e] = b1;
+        fill[e] = b0 + kept;
         if (blockIdx.x == 0) {
             p.counts[e] = kept;
-            p.ends[e] = (int)b1;
+            p.ends[e] = b1;
             if (kept < all)
                 f |= GG_DEVERR_LAST;
         }
@@ -154,40 +194,49 @@ __global__ void __launch_bounds__(kPlanThreads) plan_assign_kernel(PlanArgs p, i
     const int64_t t1 = min(p.T, (int64_t)(blockIdx.x + 1) * run);
     int seen = 0;
     for (int64_t t0 = blockIdx.x * run; t0 < t1; t0 += kChunk) {
-        plan_bits(p, t0, bits, seen);
-        const int64_t i1 = min(t1, t0 + kChunk) * p.k;
-        for (int64_t i = t0 * p.k + threadIdx.x; i < i1; i += kPlanThreads) {
-            const int64_t t = i / p.k;
-            int x;
-            int32_t row = -1;
-            if (plan_slot(p, i, t, x, seen)) {
-                const int b = (int)(t - t0);
-                int rank = __popc(bits[x * kWords + (b >> 5)] & ((1u << (b & 31)) - 1u));
-                for (int w = 0; w < (b >> 5); w++)
-                    rank += __popc(bits[x * kWords + w]);
-                const int64_t r = (int64_t)base[x] + rank;
-                if (r < stop[x])
-                    row = (int32_t)r;
-            }
-            p.row_of[i] = row;
-            if (p.prob_rows && row >= 0)
-                p.prob_rows[row] = p.prob[i];
+        const int32_t* ids = p.ids + t0 * p.k;
+        const int n = (int)min((int64_t)kChunk, t1 - t0);
+        // a single chunk's bits are there already; the first chunk of
+        // several blocks' finds cleared ones
+        if (blocks > 1 || p.T > kChunk) {
+            if (t0 != blockIdx.x * run || blocks == 1)
+                plan_clear(bits, E);
+            dup = plan_bits(p, ids, n, div, bits, &twice, seen);
         }
-        __syncthreads();
-        if (e < E)
-            base[e] = min(base[e] + plan_ones(bits, e), stop[e]);
-        __syncthreads();
+        for (int i = threadIdx.x; i < n * p.k; i += kPlanThreads) {
+            const int x = ids[i], t = div(i);
+            int row = -1;
+            if (x >= 0 && x < E && (!dup || first_use(ids, i, t, p.k, x))) {
+                int rank = __popc(bits[(t >> 5) * E + x] & ((1u << (t & 31)) - 1u));
+                for (int w = 0; w < (t >> 5); w++)
+                    rank += __popc(bits[w * E + x]);
+                if (rank < stop[x] - base[x])
+                    row = base[x] + rank;
+            }
+            const int64_t slot = t0 * p.k + i;
+            p.row_of[slot] = row;
+            if (p.prob_rows && row >= 0)
+                p.prob_rows[row] = p.prob[slot];
+        }
+        if (t0 + kChunk < t1) {
+            __syncthreads();
+            if (e < E)
+                base[e] += min(plan_ones(bits, E, e), stop[e] - base[e]);
+            __syncthreads();
+        }
     }
     // padding rows, the experts dealt to the blocks
     if (p.prob_rows)
-        for (int x = blockIdx.x; x < E; x += gridDim.x)
-            for (int r = fill[x] + threadIdx.x; r < stop[x]; r += kPlanThreads)
+        for (int x = blockIdx.x * kPlanWaves + wave; x < E; x += gridDim.x * kPlanWaves)
+            for (int r = fill[x] + lane; r < stop[x]; r += 64)
                 p.prob_rows[r] = 0.0f;
-    if (f)
-        atomicOr(&flags, f);
-    __syncthreads();
-    if (blockIdx.x == 0 && e == 0)
-        p.ws[0] = flags;
+    if (blockIdx.x == 0) {
+        if (f)
+            atomicOr(&flags, f);
+        __syncthreads();
+        if (e == 0)
+            p.ws[0] = flags;
+    }
 }
 
 // ---- rows ------------------------------------------------------------------
@@ -402,7 +451,7 @@ static int64_t plan_blocks(int64_t T) {
 }
 
 size_t plan_workspace(int64_t T, int E) {
-    return kWsHeader + (size_t)plan_blocks(T) * (E + 1) * 4;
+    return kWsHeader + (size_t)plan_blocks(T) * ((size_t)E + 1) * 4;
 }
 
 hipError_t launch_plan(const PlanArgs& p, hipStream_t s, LaunchInfo* info) {
@@ -417,8 +466,11 @@ hipError_t launch_plan(const PlanArgs& p, hipStream_t s, LaunchInfo* info) {
         e = hipGetLastError();
     }
     if (e == hipSuccess) {
+        int lanes = 64;
+        while (lanes < p.E)
+            lanes *= 2;
         hipLaunchKernelGGL(plan_assign_kernel, dim3((unsigned)blocks), dim3(kPlanThreads), 0, s, p, run,
-                           (int)blocks);
+                           (int)blocks, lanes);
         e = hipGetLastError();
     }
     if (info) {
