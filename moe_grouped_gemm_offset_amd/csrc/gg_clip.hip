@@ -104,21 +104,9 @@ __device__ __forceinline__ void scale_range(const void* base, void* out, int64_t
         o[i] = from_f32<DT>(to_f32<DT>(q[i]) * factor);
 }
 
-// Sum of v over the block, in thread 0; the same tree at every call.
-__device__ __forceinline__ double block_sum(double v, double* tmp) {
-    tmp[threadIdx.x] = v;
-    __syncthreads();
-    for (int h = kThreads / 2; h > 0; h >>= 1) {
-        if ((int)threadIdx.x < h)
-            tmp[threadIdx.x] += tmp[threadIdx.x + h];
-        __syncthreads();
-    }
-    return tmp[0];
-}
-
 // Workspace: header, then a double per block.
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(GradArgs p, int64_t piece) {
-    __shared__ double tmp[kThreads];
+    __shared__ double tmp[kThreads / 64];
     double s = 0.0;
     for (int64_t lo = (int64_t)blockIdx.x * piece; lo < p.total; lo += (int64_t)gridDim.x * piece)
         walk(p, lo, min(p.total, lo + piece), [&](int i, int dt, int64_t a, int64_t b) {
@@ -130,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(GradArgs p, int64_t
             else if (dt == GG_F32)
                 s += sum_squares<GG_F32>(q, a, b);
         });
-    const double all = block_sum(s, tmp);
+    const double all = block_sum<kThreads>(s, tmp);
     if (threadIdx.x == 0) {
         if (gridDim.x == 1)
             p.sumsq[0] = p.accumulate ? p.sumsq[0] + all : all;
@@ -140,12 +128,12 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(GradArgs p, int64_t
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(GradArgs p, int blocks) {
-    __shared__ double tmp[kThreads];
+    __shared__ double tmp[kThreads / 64];
     const double* part = (const double*)(p.ws + kWsHeader / 4);
     double s = 0.0;
     for (int b = threadIdx.x; b < blocks; b += kThreads)
         s += part[b];
-    const double all = block_sum(s, tmp);
+    const double all = block_sum<kThreads>(s, tmp);
     if (threadIdx.x == 0)
         p.sumsq[0] = p.accumulate ? p.sumsq[0] + all : all;
 }

@@ -136,7 +136,7 @@ struct OpAddF {
 };
 
 // Lowest lane of this lane's group of W for which the predicate holds, as an
-// index within the group (undefined if there is none).
+// index within the group (-1 if there is none).
 template <int W>
 __device__ __forceinline__ int group_first(bool pred, int lane) {
     const uint64_t m = __ballot(pred);
@@ -144,6 +144,30 @@ __device__ __forceinline__ int group_first(bool pred, int lane) {
         return __ffsll((unsigned long long)m) - 1;
     else
         return __ffs((int)((uint32_t)(m >> (lane & ~(W - 1))) & (W == 32 ? ~0u : (1u << W) - 1u))) - 1;
+}
+
+// Sum of v over the wave, in every lane (the same tree at every call).
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int h = 32; h > 0; h >>= 1)
+        v += __shfl_xor(v, h);
+    return v;
+}
+
+// Sum of v over a block of THREADS, in every thread, through tmp[THREADS /
+// 64] in LDS; the same order at every call.
+template <int THREADS>
+__device__ __forceinline__ double block_sum(double v, double* tmp) {
+    v = wave_sum(v);
+    __syncthreads();                                 // tmp may still be read
+    if ((threadIdx.x & 63) == 0)
+        tmp[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = tmp[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; w++)
+        s += tmp[w];
+    return s;
 }
 
 }  // namespace gg

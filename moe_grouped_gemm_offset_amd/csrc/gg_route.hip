@@ -4,6 +4,8 @@
 // Both kernels give each token a group of LPT lanes, each lane EPL
 // consecutive experts, so that one pass over the logits holds a token's row
 // in registers.  Statistics, weights and gradients are in fp32.
+#include <cfloat>
+
 #include "gg_internal.hpp"
 #include "gg_lane.hpp"
 
@@ -19,15 +21,14 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
 }
 
-// Order of the choice as unsigned integers: fp32 order with -0 = +0, NaN on
-// top; 0 for what is never chosen (a logit or a sum of -inf).
+// Order of the choice as unsigned integers: fp32 order with -0 = +0 and NaN on
+// top.  kNever and below: a logit or key of -inf, never chosen; 0: taken.
+constexpr uint32_t kNever = 0x007FFFFFu;             // the key of -inf
+
 __device__ __forceinline__ uint32_t order_key(float logit, float bias) {
     const float s = logit + bias + 0.0f;
-    const uint32_t u = __builtin_bit_cast(uint32_t, s);
-    const uint32_t key = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-    if (s != s)
-        return logit == -INFINITY ? 0u : ~0u;
-    return logit == -INFINITY || s == -INFINITY ? 0u : key;
+    const uint32_t u = s != s ? 0x7FC00000u : __builtin_bit_cast(uint32_t, s);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // The EPL experts of a lane, -inf past the row's end.
@@ -76,6 +77,11 @@ __device__ __forceinline__ void store_row(typename Elem<DT>::T* row, int first, 
     }
 }
 
+// 1 / a sum of scores.
+__device__ __forceinline__ float inverse_sum(float sum, bool softmax) {
+    return softmax ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f / (sum + kTiny);
+}
+
 // A token's softmax or sigmoid over its row: x becomes the scores, `inv` what
 // turns them into the balance probabilities (softmax: x are exp(x - top), so
 // that p = x inv is the softmax as well; a row of -inf gives all zeros).
@@ -95,7 +101,7 @@ __device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float&
             sum += x[i];
         }
         sum = group_all<LPT>(sum, OpAddF());
-        inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        inv = inverse_sum(sum, true);
     } else {
         top = 0.0f;
 #pragma unroll
@@ -104,8 +110,19 @@ __device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float&
             sum += x[i];
         }
         sum = group_all<LPT>(sum, OpAddF());
-        inv = 1.0f / (sum + kTiny);
+        inv = inverse_sum(sum, false);
     }
+}
+
+// Largest of the chosen logits (0 if there is none).
+template <int LPT, int NJ>
+__device__ __forceinline__ float choice_top(const float (&v)[NJ]) {
+    float m = v[0];
+#pragma unroll
+    for (int s = 1; s < NJ; s++)
+        m = fmaxf(m, v[s]);
+    m = group_all<LPT>(m, OpMaxF());
+    return m == -INFINITY ? 0.0f : m;
 }
 
 }  // namespace
@@ -124,6 +141,7 @@ template <int DT, int LPT, int EPL>
 __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     static_assert(EPL <= LPT, "a group rescans one lane's keys in one read");
     constexpr int TPW = 64 / LPT;                    // tokens per wave
+    constexpr int NJ = LPT >= 32 ? 1 : 32 / LPT;     // choices a lane may hold
     constexpr int kPitch = EPL + 4;                  // words of a lane's keys
     constexpr int kCap = LPT * EPL;
     __shared__ __align__(16) uint32_t keys[kWaves * 64 * kPitch];
@@ -149,8 +167,11 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     }
     float bias[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; i++)
-        bias[i] = p.bias && first + i < E ? p.bias[first + i] : 0.0f;
+    for (int i = 0; i < EPL; i++) {
+        // +inf and NaN as the largest finite bias: a logit of -inf stays one
+        const float v = p.bias && first + i < E ? p.bias[first + i] : 0.0f;
+        bias[i] = v <= FLT_MAX ? v : FLT_MAX;
+    }
     float psum[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; i++)
@@ -186,8 +207,17 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
             if (g == from)
                 best = next;
             if (g == 0)
-                my_sel[j] = top ? from * EPL + at : -1;
+                my_sel[j] = top > kNever ? from * EPL + at : -1;
             wave_sync();
+        }
+        // the chosen experts, a lane each (NJ of them if top_k > LPT)
+        int32_t e[NJ];
+        float v[NJ];
+#pragma unroll
+        for (int s = 0; s < NJ; s++) {
+            const int j = g + s * LPT;
+            e[s] = live && j < k ? my_sel[j] : -1;
+            v[s] = e[s] >= 0 ? to_f32<DT>(row[e[s]]) : -INFINITY;
         }
         float top = 0.0f, inv = 0.0f;
         if (stats || (softmax && !p.normalize)) {
@@ -195,48 +225,33 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
             if (stats) {
 #pragma unroll
                 for (int i = 0; i < EPL; i++)
-                    psum[i] += x[i] * inv;
+                    psum[i] = fmaf(x[i], inv, psum[i]);
             }
         }
-        // the chosen experts' weights, a lane each
-        float norm = 1.0f;
+        float norm = softmax ? inv : 1.0f;
+        if (p.normalize && softmax)
+            top = choice_top<LPT, NJ>(v);
+        float sum = 0.0f;
+#pragma unroll
+        for (int s = 0; s < NJ; s++) {
+            v[s] = softmax ? __expf(v[s] - top) : sigmoid(v[s]);
+            sum += v[s];
+        }
         if (p.normalize) {
-            float sum = 0.0f;
-            if (softmax) {
-                float m = -INFINITY;
-                for (int j = g; j < k; j += LPT) {
-                    const int e = my_sel[j];
-                    if (e >= 0)
-                        m = fmaxf(m, to_f32<DT>(row[e]));
-                }
-                m = group_all<LPT>(m, OpMaxF());
-                top = m == -INFINITY ? 0.0f : m;
-            }
-            for (int j = g; j < k; j += LPT) {
-                const int e = my_sel[j];
-                if (e >= 0) {
-                    const float v = to_f32<DT>(row[e]);
-                    sum += softmax ? __expf(v - top) : sigmoid(v);
-                }
-            }
             sum = group_all<LPT>(sum, OpAddF());
-            norm = softmax ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f / (sum + kTiny);
-        } else if (softmax) {
-            norm = inv;
+            norm = inverse_sum(sum, softmax);
         }
-        if (live) {
-            for (int j = g; j < k; j += LPT) {
-                const int e = my_sel[j];
-                float w = 0.0f;
-                if (e >= 0) {
-                    const float v = to_f32<DT>(row[e]);
-                    w = p.scale * ((softmax ? __expf(v - top) : sigmoid(v)) * norm);
-                    atomicAdd(&hist[e], 1);
-                    if (j == 0)
-                        atomicAdd(&nrouted, 1);
-                }
-                p.ids[t * k + j] = e;
-                p.prob[t * k + j] = w;
+#pragma unroll
+        for (int s = 0; s < NJ; s++) {
+            const int j = g + s * LPT;
+            if (!live || j >= k)
+                continue;
+            p.ids[t * k + j] = e[s];
+            p.prob[t * k + j] = e[s] >= 0 ? p.scale * (v[s] * norm) : 0.0f;
+            if (e[s] >= 0) {
+                atomicAdd(&hist[e[s]], 1);
+                if (j == 0)
+                    atomicAdd(&nrouted, 1);
             }
         }
     }
@@ -272,31 +287,24 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     }
     // a single block finishes here
     __syncthreads();
-    double* tmp = (double*)keys;
-    tmp[tid] = loss;
-    __syncthreads();
-    for (int h = kThreads / 2; h > 0; h >>= 1) {
-        if (tid < h)
-            tmp[tid] += tmp[tid + h];
-        __syncthreads();
-    }
+    loss = block_sum<kThreads>(loss, (double*)keys);
     if (tid == 0) {
         p.routed[0] = nrouted;
         if (stats) {
             const double n = nrouted > 0 ? (double)nrouted : 1.0;
-            p.balance[0] = (float)((double)E * tmp[0] / ((double)k * n * n));
+            p.balance[0] = (float)((double)E * loss / ((double)k * n * n));
         }
     }
 }
 
-// Joins the blocks' counts and probability sums: 16 experts a block, 16
+// Joins the blocks' counts and probability sums: 16 experts a block, 64
 // runs of blocks each; the block that finishes last adds up the loss.
-constexpr int kJoinExperts = 16, kJoinRuns = 16;
+constexpr int kJoinExperts = 16, kJoinRuns = 64, kJoinThreads = kJoinExperts * kJoinRuns;
 
-__global__ void __launch_bounds__(256) route_join_kernel(RouteArgs p, int blocks) {
+__global__ void __launch_bounds__(kJoinThreads) route_join_kernel(RouteArgs p, int blocks) {
     __shared__ int32_t cnt[kJoinRuns][kJoinExperts];
     __shared__ double sum[kJoinRuns][kJoinExperts];
-    __shared__ double tmp[256];
+    __shared__ double tmp[kJoinThreads / 64];
     __shared__ int32_t is_last;
     const int tid = threadIdx.x, E = p.E;
     const int run = tid / kJoinExperts, lane = tid % kJoinExperts;
@@ -335,142 +343,134 @@ __global__ void __launch_bounds__(256) route_join_kernel(RouteArgs p, int blocks
         return;
     double loss = 0.0;
     int32_t n = 0;
-    for (int i = tid; i < E; i += 256)
+    for (int i = tid; i < E; i += kJoinThreads)
         loss += __hip_atomic_load(&terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int b = tid; b < blocks; b += 256)
+    for (int b = tid; b < blocks; b += kJoinThreads)
         n += part[b * pitch + 2 * E];
-    __shared__ int32_t ntmp[256];
-    tmp[tid] = loss;
-    ntmp[tid] = n;
-    __syncthreads();
-    for (int h = 128; h > 0; h >>= 1) {
-        if (tid < h) {
-            tmp[tid] += tmp[tid + h];
-            ntmp[tid] += ntmp[tid + h];
-        }
-        __syncthreads();
-    }
+    loss = block_sum<kJoinThreads>(loss, tmp);
+    n = (int32_t)block_sum<kJoinThreads>((double)n, tmp);
     if (tid == 0) {
-        p.routed[0] = ntmp[0];
+        p.routed[0] = n;
         if (p.balance) {
-            const double m = ntmp[0] > 0 ? (double)ntmp[0] : 1.0;
-            p.balance[0] = (float)((double)E * tmp[0] / ((double)p.k * m * m));
+            const double m = n > 0 ? (double)n : 1.0;
+            p.balance[0] = (float)((double)E * loss / ((double)p.k * m * m));
         }
     }
 }
 
-// The gradient of the logits.  The chosen experts' gradients are added into
-// an LDS row by a lane each, and every lane takes its EPL from there.
+// The gradient of the logits.  The chosen experts' gradients go into an LDS
+// row, a lane each, and every lane takes its EPL from there.  A block walks
+// over tokens, so that a lane's counts are loaded once.
 template <int DT, int LPT, int EPL>
 __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
-    constexpr int TPW = 64 / LPT, kCap = LPT * EPL;
-    __shared__ __align__(16) float at_all[4][TPW][kCap];
+    constexpr int TPW = 64 / LPT;
+    constexpr int NJ = LPT >= 32 ? 1 : 32 / LPT;
+    constexpr int kPitch = EPL + 4;
+    __shared__ __align__(16) float at_all[4 * 64 * kPitch];
     typedef typename Elem<DT>::T T;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int g = lane & (LPT - 1), sub = lane / LPT;
     const int first = g * EPL, E = p.E, k = p.k;
-    float* at = at_all[wave][sub];
-    const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * TPW;
-    if (t0 >= p.T)
-        return;                                      // a whole wave
-    const int64_t t = t0 + sub;
-    const bool live = t < p.T;
-    const T* row = (const T*)p.logits + (live ? t : 0) * p.ld;
-    const int32_t* ids = p.ids + (live ? t : 0) * k;
-
-    float x[EPL];
-    load_row<DT, EPL>(row, first, E, live, x);
-    float top = 0.0f, inv = 0.0f;
-    row_scores<LPT, EPL>(x, p.softmax, top, inv);
+    float* at = at_all + (wave * 64 + sub * LPT) * kPitch;
+    float* my_at = at + g * kPitch;
 
     // c = dL/dp of the balance loss
     float c[EPL];
-    float pc = 0.0f;
     const float n = fmaxf((float)p.routed[0], 1.0f);
     const float cb = p.dbalance ? p.dbalance[0] * (float)E / ((float)k * n * n) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        c[i] = p.dbalance && first + i < E ? cb * (float)p.counts[first + i] : 0.0f;
-        pc += x[i] * inv * c[i];
-    }
-    pc = group_all<LPT>(pc, OpAddF());
-
-#pragma unroll
     for (int i = 0; i < EPL; i++)
-        at[first + i] = 0.0f;
-    wave_sync();
-    // a lane per choice: G = scale * dprob, the weight q, and sum q G
-    float chosen = 0.0f, qg = 0.0f, ctop = 0.0f;
-    bool any = false;
-    if (p.normalize && p.softmax) {
-        float m = -INFINITY;
-        for (int j = g; j < k; j += LPT) {
-            const int e = live ? ids[j] : -1;
-            if (e >= 0 && e < E)
-                m = fmaxf(m, to_f32<DT>(row[e]));
-        }
-        m = group_all<LPT>(m, OpMaxF());
-        ctop = m == -INFINITY ? 0.0f : m;
-    }
-    for (int j = g; j < k; j += LPT) {
-        const int e = live ? ids[j] : -1;
-        if (e >= 0 && e < E) {
-            any = true;
-            int64_t r = t * k + j;
-            bool have = true;
-            if (p.row_of) {
-                r = p.row_of[t * k + j];
-                have = r >= 0 && r < p.m_rows;
-            }
-            const float G = have ? p.scale * p.dprob[r] : 0.0f;
-            const float v = to_f32<DT>(row[e]);
-            const float s = p.softmax ? __expf(v - (p.normalize ? ctop : top)) : sigmoid(v);
-            chosen += s;
-            qg += s * G;
-        }
-    }
-    chosen = group_all<LPT>(chosen, OpAddF());
-    qg = group_all<LPT>(qg, OpAddF());
-    // softmax over the chosen, s / sum of the chosen, or the plain score
-    const float cinv = p.softmax ? (chosen == 0.0f ? 0.0f : 1.0f / chosen) : 1.0f / (chosen + kTiny);
-    const float mean = p.normalize ? qg * cinv : p.softmax ? qg * inv : 0.0f;
-    for (int j = g; j < k; j += LPT) {
-        const int e = live ? ids[j] : -1;
-        if (e >= 0 && e < E) {
-            int64_t r = t * k + j;
-            bool have = true;
-            if (p.row_of) {
-                r = p.row_of[t * k + j];
-                have = r >= 0 && r < p.m_rows;
-            }
-            const float G = have ? p.scale * p.dprob[r] : 0.0f;
-            const float v = to_f32<DT>(row[e]);
-            float d;                                 // added to dx (softmax) or ds (sigmoid)
-            if (p.softmax)
-                d = p.normalize ? __expf(v - ctop) * cinv * (G - mean) : __expf(v - top) * inv * G;
-            else
-                d = p.normalize ? (G - mean) * cinv : G;
-            atomicAdd(&at[e], d);
-        }
-    }
-    wave_sync();
-    const bool routed = __ballot(any) >> (lane & ~(LPT - 1)) & (LPT == 64 ? ~0ull : (1ull << (LPT & 63)) - 1ull);
-    if (!live)
-        return;
-    float dx[EPL];
+        c[i] = p.dbalance && first + i < E ? cb * (float)p.counts[first + i] : 0.0f;
+
+    const int64_t step = (int64_t)gridDim.x * 4 * TPW;
+    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * TPW; t0 < p.T; t0 += step) {
+        const int64_t t = t0 + sub;
+        const bool live = t < p.T;
+        const T* row = (const T*)p.logits + (live ? t : 0) * p.ld;
+
+        // a lane per choice: its expert, G = scale * dprob, its logit
+        int32_t e[NJ];
+        float G[NJ], v[NJ];
+        bool any = false;
 #pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const float a = at[first + i];
-        if (p.softmax) {
-            const float pull = c[i] - pc - (p.normalize ? 0.0f : mean);
-            dx[i] = x[i] * inv * pull + a;
-        } else {
-            dx[i] = ((c[i] - pc) * inv + a) * x[i] * (1.0f - x[i]);
+        for (int s = 0; s < NJ; s++) {
+            const int j = g + s * LPT;
+            e[s] = -1;
+            G[s] = 0.0f;
+            if (live && j < k) {
+                const int64_t i = t * k + j;
+                e[s] = p.ids[i];
+                if (e[s] >= E)
+                    e[s] = -1;
+                const int64_t r = p.row_of ? (int64_t)p.row_of[i] : i;
+                if (!p.row_of || (r >= 0 && r < p.m_rows))
+                    G[s] = p.scale * p.dprob[r];
+            }
         }
-        if (!routed)
-            dx[i] = 0.0f;
+        float x[EPL];
+        load_row<DT, EPL>(row, first, E, live, x);
+#pragma unroll
+        for (int s = 0; s < NJ; s++) {
+            v[s] = e[s] >= 0 ? to_f32<DT>(row[e[s]]) : -INFINITY;
+            any |= e[s] >= 0;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            my_at[i] = 0.0f;
+        wave_sync();
+
+        float top = 0.0f, inv = 0.0f;
+        row_scores<LPT, EPL>(x, p.softmax, top, inv);
+        float pc = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            pc = fmaf(x[i], c[i], pc);
+        pc = group_all<LPT>(pc, OpAddF()) * inv;
+
+        // weights q (before scale) and their mean gradient sum q G
+        if (p.normalize && p.softmax)
+            top = choice_top<LPT, NJ>(v);
+        float chosen = 0.0f, qg = 0.0f;
+#pragma unroll
+        for (int s = 0; s < NJ; s++) {
+            v[s] = p.softmax ? __expf(v[s] - top) : sigmoid(v[s]);
+            if (e[s] < 0)
+                v[s] = G[s] = 0.0f;
+            chosen += v[s];
+            qg = fmaf(v[s], G[s], qg);
+        }
+        chosen = group_all<LPT>(chosen, OpAddF());
+        qg = group_all<LPT>(qg, OpAddF());
+        const float norm = p.normalize ? inverse_sum(chosen, p.softmax) : p.softmax ? inv : 1.0f;
+        const float mean = qg * norm;
+        // what a choice adds: to dx (softmax), to ds (sigmoid)
+#pragma unroll
+        for (int s = 0; s < NJ; s++) {
+            if (e[s] < 0)
+                continue;
+            const float centred = p.normalize ? G[s] - mean : G[s];
+            const float d = p.softmax ? v[s] * norm * centred : centred * norm;
+            atomicAdd(&at[e[s] / EPL * kPitch + e[s] % EPL], d);
+        }
+        wave_sync();
+        const bool routed = group_first<LPT>(any, lane) >= 0;
+        const float pull = pc + (p.softmax && !p.normalize ? mean : 0.0f);
+        if (live) {
+            float dx[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                const float a = my_at[i];
+                if (p.softmax)
+                    dx[i] = fmaf(x[i] * inv, c[i] - pull, a);
+                else
+                    dx[i] = fmaf(c[i] - pc, inv, a) * x[i] * (1.0f - x[i]);
+                if (!routed)
+                    dx[i] = 0.0f;
+            }
+            store_row<DT, EPL>((T*)p.dlogits + t * E, first, E, dx);
+        }
+        wave_sync();
     }
-    store_row<DT, EPL>((T*)p.dlogits + t * E, first, E, dx);
 }
 
 // ---- launches --------------------------------------------------------------
@@ -513,7 +513,7 @@ static hipError_t route_dt(const RouteArgs& p, hipStream_t s, LaunchInfo* info) 
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && blocks > 1) {
         hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)((p.E + kJoinExperts - 1) / kJoinExperts)),
-                           dim3(256), 0, s, p, (int)blocks);
+                           dim3(kJoinThreads), 0, s, p, (int)blocks);
         e = hipGetLastError();
     }
     if (info) {
@@ -534,7 +534,10 @@ hipError_t launch_route(const RouteArgs& p, int dtype, hipStream_t s, LaunchInfo
 
 template <int DT, int LPT, int EPL>
 static hipError_t route_bwd_go(const RouteBwdArgs& p, hipStream_t s, LaunchInfo* info) {
-    const int64_t per = 4 * (64 / LPT), blocks = (p.T + per - 1) / per;
+    const int64_t per = 4 * (64 / LPT);
+    int64_t blocks = (p.T + per - 1) / per;
+    if (blocks > 2048)
+        blocks = 2048;                               // eight to a CU, then more passes each
     hipLaunchKernelGGL((route_bwd_kernel<DT, LPT, EPL>), dim3((unsigned)blocks), dim3(256), 0, s, p);
     if (info) {
         snprintf(info->kernel, sizeof info->kernel, "route_bwd_kernel<%s, %d lanes a token>",
