@@ -514,9 +514,10 @@ size_t gg_route_workspace_size(int64_t tokens, int32_t num_experts);
  * loss.  Per token t, with x its logits:
  *   key_e   = x_e + bias_e                     (one fp32 addition)
  *   ids     = the top_k experts of the largest keys, largest first, ties to
- *             the lower index.  -0 and +0 are equal, NaN is above +inf.  A
- *             logit or key of -inf is never chosen: where fewer than top_k
- *             are above it, the rest of ids is -1 and of prob 0.
+ *             the lower index.  -0 and +0 are equal; a NaN is above +inf, or
+ *             with its sign set below -inf.  A logit or key of -inf or below
+ *             is never chosen: where fewer than top_k are above it, the rest
+ *             of ids is -1 and of prob 0.
  *   scores  = softmax(x) over all experts (GG_SOFTMAX) or sigmoid(x)
  *             (GG_SIGMOID), without the bias
  *   prob    = scale * score of the chosen; with GG_FLAG_NORMALIZE
@@ -534,7 +535,8 @@ size_t gg_route_workspace_size(int64_t tokens, int32_t num_experts);
  *            (t, e) at logits[t*ld + e], ld >= num_experts; aligned to its
  *            element.
  * tokens     0 .. 2^23.  num_experts 1..1024.
- * bias       float[num_experts], or NULL for none.
+ * bias       float[num_experts], or NULL for none; +inf and NaN count as the
+ *            largest finite value.
  * top_k      1 .. min(32, num_experts).  scale: finite.
  * ids, prob  (tokens, top_k) int32 / float outputs.
  * counts     int32[num_experts], routed int32[1]: outputs.

@@ -71,6 +71,32 @@ struct Vec {
         else
             return to_f32<DT>((uint16_t)(raw[i >> 1] >> (16 * (i & 1))));
     }
+    // Moves element d + i to i (0 <= d < N; what comes in at the top is
+    // unspecified).
+    __device__ __forceinline__ void drop(int d) {
+        constexpr int W = kBytes / 4;
+        const int words = DT == GG_F32 ? d : d >> 1;
+        uint32_t r[W];
+#pragma unroll
+        for (int i = 0; i < W; i++)
+            r[i] = raw[i];
+        if constexpr (W == 4) {
+            r[0] = words & 2 ? raw[2] : raw[0];
+            r[1] = words & 2 ? raw[3] : raw[1];
+        }
+#pragma unroll
+        for (int i = 0; i + 1 < W; i++)
+            r[i] = words & 1 ? r[i + 1] : r[i];
+        if constexpr (DT != GG_F32) {
+            const uint32_t sh = 16 * (d & 1);
+#pragma unroll
+            for (int i = 0; i < W; i++)
+                r[i] = __builtin_amdgcn_alignbit(r[i + 1 < W ? i + 1 : i], r[i], sh);
+        }
+#pragma unroll
+        for (int i = 0; i < W; i++)
+            raw[i] = r[i];
+    }
     __device__ __forceinline__ void set(const float (&f)[N]) {
         if constexpr (DT == GG_F32) {
 #pragma unroll
@@ -143,7 +169,7 @@ __device__ __forceinline__ int group_first(bool pred, int lane) {
     if constexpr (W == 64)
         return __ffsll((unsigned long long)m) - 1;
     else
-        return __ffs((int)((uint32_t)(m >> (lane & ~(W - 1))) & (W == 32 ? ~0u : (1u << W) - 1u))) - 1;
+        return __ffs((int)((uint32_t)(m >> (lane & ~(W - 1))) & (uint32_t)((1ull << W) - 1))) - 1;
 }
 
 // Sum of v over the wave, in every lane (the same tree at every call).

@@ -5,6 +5,7 @@
 // consecutive experts, so that one pass over the logits holds a token's row
 // in registers.  Statistics, weights and gradients are in fp32.
 #include <cfloat>
+#include <type_traits>
 
 #include "gg_internal.hpp"
 #include "gg_lane.hpp"
@@ -15,49 +16,82 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr float kTiny = 1e-20f;          // added to sums of sigmoids, which can underflow
 
 __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
 }
 
-// Order of the choice as unsigned integers: fp32 order with -0 = +0 and NaN on
-// top.  kNever and below: a logit or key of -inf, never chosen; 0: taken.
+// Order of the choice as unsigned integers: fp32 order with -0 = +0 (bias is
+// never -0), a NaN above +inf, or below -inf if its sign is set.  kNever and
+// below, a logit or key of -inf, is never chosen; 0: taken.
 constexpr uint32_t kNever = 0x007FFFFFu;             // the key of -inf
 
 __device__ __forceinline__ uint32_t order_key(float logit, float bias) {
-    const float s = logit + bias + 0.0f;
-    const uint32_t u = s != s ? 0x7FC00000u : __builtin_bit_cast(uint32_t, s);
+    const uint32_t u = __builtin_bit_cast(uint32_t, logit + bias);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// The EPL experts of a lane, -inf past the row's end.
+// Words of LDS from a lane's first element to the next lane's, where a group
+// keeps EPL of each lane: 16-byte vectors that lanes write at once then fall
+// into different banks.
+template <int EPL>
+constexpr int lane_pitch() {
+    return EPL + 4;
+}
+
+// How a lane loads its experts: kWholeRows are whole vectors, kOddRows are
+// not but hold one, kShortRows are shorter than one.
+enum RowKind { kWholeRows = 0, kOddRows = 1, kShortRows = 2 };
+
 template <int DT, int EPL>
+constexpr int row_vector() {
+    return EPL * (int)sizeof(typename Elem<DT>::T) >= 16 ? 16 / (int)sizeof(typename Elem<DT>::T) : EPL;
+}
+
+// The EPL experts of a lane, -inf past the row's end and where !live.  The
+// loads are unconditional, at clamped addresses: a branch around a load
+// makes the wave wait for it before the next.
+template <int DT, int EPL, int KIND>
 __device__ __forceinline__ void load_row(const typename Elem<DT>::T* row, int first, int E, bool live,
                                          float (&x)[EPL]) {
-    constexpr int N = EPL * (int)sizeof(typename Elem<DT>::T) >= 16
-                          ? 16 / (int)sizeof(typename Elem<DT>::T) : EPL;
+    constexpr int N = row_vector<DT, EPL>();
+    // `first` as a value of its own in every pass over this: compares with it
+    // would otherwise be kept from pass to pass, a register pair each
+    asm volatile("" : "+v"(first));
+    if constexpr (KIND == kShortRows) {
 #pragma unroll
-    for (int c = 0; c < EPL; c += N) {
-        if (live && first + c + N <= E) {
-            Vec<DT, N> v;
-            v.load(row + first + c);
+        for (int i = 0; i < EPL; i++)
+            x[i] = to_f32<DT>(row[min(first + i, E - 1)]);
+    } else {
+        // (odd rows: the vector that crosses the row's end is read N before
+        // the end and moved down by what came before it)
+        Vec<DT, N> v[EPL / N];
+#pragma unroll
+        for (int c = 0; c < EPL; c += N)
+            v[c / N].load(row + min(first + c, E - N));
+#pragma unroll
+        for (int c = 0; c < EPL; c += N) {
+            if constexpr (KIND == kOddRows)
+                v[c / N].drop(first + c - min(first + c, E - N));
 #pragma unroll
             for (int i = 0; i < N; i++)
-                x[c + i] = v.get(i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i++)
-                x[c + i] = live && first + c + i < E ? to_f32<DT>(row[first + c + i]) : -INFINITY;
+                x[c + i] = v[c / N].get(i);
         }
     }
+    // past the row's end, or no row: waves of whole rows skip this
+    if (__ballot(!live || first + EPL > E))
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            x[i] = live && first + i < E ? x[i] : -INFINITY;
 }
 
 template <int DT, int EPL>
 __device__ __forceinline__ void store_row(typename Elem<DT>::T* row, int first, int E,
                                           const float (&x)[EPL]) {
-    constexpr int N = EPL * (int)sizeof(typename Elem<DT>::T) >= 16
-                          ? 16 / (int)sizeof(typename Elem<DT>::T) : EPL;
+    constexpr int N = row_vector<DT, EPL>();
 #pragma unroll
     for (int c = 0; c < EPL; c += N) {
         if (first + c + N <= E) {
@@ -137,26 +171,25 @@ __host__ __device__ inline int64_t route_partial(int E) { return 2 * (int64_t)E 
 // lowest lane, so the lowest experts), rescans that lane's keys -- in LDS,
 // one per lane of the group -- for the expert, removes it and hands the lane
 // its next largest.
-template <int DT, int LPT, int EPL>
+template <int DT, int LPT, int EPL, int KIND>
 __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     static_assert(EPL <= LPT, "a group rescans one lane's keys in one read");
     constexpr int TPW = 64 / LPT;                    // tokens per wave
     constexpr int NJ = LPT >= 32 ? 1 : 32 / LPT;     // choices a lane may hold
-    constexpr int kPitch = EPL + 4;                  // words of a lane's keys
     constexpr int kCap = LPT * EPL;
+    constexpr int kPitch = lane_pitch<EPL>();
     __shared__ __align__(16) uint32_t keys[kWaves * 64 * kPitch];
+    __shared__ __align__(16) float bias[LPT * kPitch];
     __shared__ int32_t hist[kCap];
-    __shared__ int32_t sel[kWaves][TPW][32];
     __shared__ int32_t nrouted;
     typedef typename Elem<DT>::T T;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // a scalar: loops over it are the wave's
     const int g = lane & (LPT - 1), sub = lane / LPT;
     const int first = g * EPL;
     const int E = p.E, k = p.k;
     const bool softmax = p.softmax, stats = p.balance != nullptr;
-    uint32_t* group_keys = keys + (wave * 64 + sub * LPT) * kPitch;
-    uint32_t* my_keys = group_keys + g * kPitch;
-    int32_t* my_sel = sel[wave][sub];
+    uint32_t* group_keys = keys + (wave * TPW + sub) * LPT * kPitch;
 
     for (int e = tid; e < kCap; e += kThreads)
         hist[e] = 0;
@@ -165,12 +198,10 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         if (blockIdx.x == 0)
             p.ws[1] = 0;
     }
-    float bias[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        // +inf and NaN as the largest finite bias: a logit of -inf stays one
-        const float v = p.bias && first + i < E ? p.bias[first + i] : 0.0f;
-        bias[i] = v <= FLT_MAX ? v : FLT_MAX;
+    // +inf and NaN as the largest finite bias: a logit of -inf stays one
+    for (int e = tid; e < kCap; e += kThreads) {
+        const float b = p.bias && e < E ? p.bias[e] : 0.0f;
+        bias[e / EPL * kPitch + e % EPL] = b <= FLT_MAX ? b + 0.0f : FLT_MAX;
     }
     float psum[EPL];
 #pragma unroll
@@ -178,46 +209,25 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         psum[i] = 0.0f;
     __syncthreads();
 
-    const int64_t step = (int64_t)gridDim.x * kWaves * TPW;
-    for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * TPW; t0 < p.T; t0 += step) {
-        const int64_t t = t0 + sub;
-        const bool live = t < p.T;
+    const int T_ = (int)p.T;                         // at most 2^23
+    const int step = (int)gridDim.x * kWaves * TPW;
+    for (int t0 = ((int)blockIdx.x * kWaves + wave) * TPW; t0 < T_; t0 += step) {
+        const int t = t0 + sub;
+        const bool live = t < T_;
         const T* row = (const T*)p.logits + (live ? t : 0) * p.ld;
         float x[EPL];
-        load_row<DT, EPL>(row, first, E, live, x);
+        load_row<DT, EPL, KIND>(row, first, E, live, x);
         uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const uint32_t key = order_key(x[i], bias[i]);
-            my_keys[i] = key;
-            best = best > key ? best : key;
-        }
-        wave_sync();
-        for (int j = 0; j < k; j++) {
-            const uint32_t top = group_all<LPT>(best, OpMaxU());
-            const int from = group_first<LPT>(best == top, lane);
-            uint32_t* theirs = group_keys + from * kPitch;
-            uint32_t v = g < EPL ? theirs[g] : 0u;
-            const int at = group_first<LPT>(v == top && g < EPL, lane);
-            if (g == at) {
-                v = 0;
-                theirs[g] = 0;
-            }
-            const uint32_t next = group_all<LPT>(v, OpMaxU());
-            if (g == from)
-                best = next;
-            if (g == 0)
-                my_sel[j] = top > kNever ? from * EPL + at : -1;
-            wave_sync();
-        }
-        // the chosen experts, a lane each (NJ of them if top_k > LPT)
-        int32_t e[NJ];
-        float v[NJ];
+        for (int c = 0; c < EPL; c += 4) {
+            u32x4 four;
+            const f32x4 b = *(const f32x4*)(bias + g * kPitch + c);
 #pragma unroll
-        for (int s = 0; s < NJ; s++) {
-            const int j = g + s * LPT;
-            e[s] = live && j < k ? my_sel[j] : -1;
-            v[s] = e[s] >= 0 ? to_f32<DT>(row[e[s]]) : -INFINITY;
+            for (int i = 0; i < 4; i++) {
+                four[i] = order_key(x[c + i], b[i]);
+                best = best > four[i] ? best : four[i];
+            }
+            *(u32x4*)(group_keys + g * kPitch + c) = four;
         }
         float top = 0.0f, inv = 0.0f;
         if (stats || (softmax && !p.normalize)) {
@@ -228,6 +238,38 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
                     psum[i] = fmaf(x[i], inv, psum[i]);
             }
         }
+        if constexpr (EPL < LPT)
+            group_keys[g * kPitch + EPL] = 0;        // read and written by the lanes past EPL
+        // the choice; lane j % LPT keeps choice j, NJ of them if top_k > LPT
+        int32_t e[NJ];
+        float v[NJ];
+#pragma unroll
+        for (int s = 0; s < NJ; s++) {
+            int32_t id = -1;
+            uint32_t kept = 0;
+            const int n = __builtin_amdgcn_readfirstlane(min(LPT, k - s * LPT));
+            for (int j = 0; j < n; j++) {
+                wave_sync();
+                const uint32_t most = group_all<LPT>(best, OpMaxU());
+                const int from = group_first<LPT>(best == most, lane);
+                uint32_t* mine = group_keys + from * kPitch + min(g, EPL);
+                uint32_t key = *mine;
+                const int at = group_first<LPT>(key == most, lane);
+                key = g == at ? 0u : key;
+                *mine = key;
+                const uint32_t next = group_all<LPT>(key, OpMaxU());
+                best = g == from ? next : best;
+                id = g == j ? from * EPL + at : id;
+                kept = g == j ? most : kept;
+            }
+            e[s] = live && kept > kNever ? id : -1;
+            v[s] = -INFINITY;
+            if (s * LPT < k) {
+                v[s] = to_f32<DT>(row[max(e[s], 0)]);
+                v[s] = e[s] >= 0 ? v[s] : -INFINITY;
+            }
+        }
+        wave_sync();
         float norm = softmax ? inv : 1.0f;
         if (p.normalize && softmax)
             top = choice_top<LPT, NJ>(v);
@@ -265,12 +307,13 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     }
     __syncthreads();
     const bool last = gridDim.x == 1;
+    const int groups = (int)min((int64_t)kWaves * TPW, p.T);     // that had a token
     int32_t* part = p.ws + kWsHeader / 4 + blockIdx.x * route_partial(E);
     double loss = 0.0;
     for (int e = tid; e < E; e += kThreads) {
         float s = 0.0f;
         if (stats)
-            for (int w = 0; w < kWaves * TPW; w++)
+            for (int w = 0; w < groups; w++)
                 s += sums[w * kCap + e];
         if (last) {
             p.counts[e] = hist[e];
@@ -359,64 +402,73 @@ __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(RouteArgs p, i
 }
 
 // The gradient of the logits.  The chosen experts' gradients go into an LDS
-// row, a lane each, and every lane takes its EPL from there.  A block walks
-// over tokens, so that a lane's counts are loaded once.
-template <int DT, int LPT, int EPL>
+// row, a lane each, and every lane takes its EPL from there.
+template <int DT, int LPT, int EPL, int KIND>
 __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
     constexpr int TPW = 64 / LPT;
     constexpr int NJ = LPT >= 32 ? 1 : 32 / LPT;
-    constexpr int kPitch = EPL + 4;
+    constexpr int kCap = LPT * EPL, kPitch = lane_pitch<EPL>();
     __shared__ __align__(16) float at_all[4 * 64 * kPitch];
     typedef typename Elem<DT>::T T;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // a scalar: loops over it are the wave's
     const int g = lane & (LPT - 1), sub = lane / LPT;
     const int first = g * EPL, E = p.E, k = p.k;
-    float* at = at_all + (wave * 64 + sub * LPT) * kPitch;
-    float* my_at = at + g * kPitch;
+    float* at = at_all + (wave * TPW + sub) * LPT * kPitch;
 
     // c = dL/dp of the balance loss
-    float c[EPL];
+    __shared__ __align__(16) float c[LPT * kPitch];
     const float n = fmaxf((float)p.routed[0], 1.0f);
     const float cb = p.dbalance ? p.dbalance[0] * (float)E / ((float)k * n * n) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < EPL; i++)
-        c[i] = p.dbalance && first + i < E ? cb * (float)p.counts[first + i] : 0.0f;
+    for (int e = tid; e < kCap; e += 256)
+        c[e / EPL * kPitch + e % EPL] = e < E ? cb * (float)p.counts[e] : 0.0f;
+    __syncthreads();
+    auto c_at = [&](int i) { return (*(const f32x4*)(c + g * kPitch + (i & ~3)))[i & 3]; };
 
-    const int64_t step = (int64_t)gridDim.x * 4 * TPW;
-    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * TPW; t0 < p.T; t0 += step) {
-        const int64_t t = t0 + sub;
-        const bool live = t < p.T;
+    const int64_t rows = p.row_of ? p.m_rows : p.T * k;
+    const int T_ = (int)p.T;                         // at most 2^23
+    const int step = (int)gridDim.x * 4 * TPW;
+    for (int t0 = ((int)blockIdx.x * 4 + wave) * TPW; t0 < T_; t0 += step) {
+        const int t = t0 + sub;
+        const bool live = t < T_;
         const T* row = (const T*)p.logits + (live ? t : 0) * p.ld;
 
-        // a lane per choice: its expert, G = scale * dprob, its logit
-        int32_t e[NJ];
+        // a lane per choice: its expert, G = scale * dprob, its logit (loads at
+        // clamped addresses, as in load_row)
+        int32_t e[NJ], r[NJ];
         float G[NJ], v[NJ];
         bool any = false;
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
             const int j = g + s * LPT;
-            e[s] = -1;
-            G[s] = 0.0f;
-            if (live && j < k) {
-                const int64_t i = t * k + j;
+            e[s] = r[s] = -1;
+            if (s * LPT < k) {
+                const int i = live && j < k ? t * k + j : 0;
                 e[s] = p.ids[i];
-                if (e[s] >= E)
+                r[s] = p.row_of ? p.row_of[i] : i;
+                if (!live || j >= k || e[s] >= E)
                     e[s] = -1;
-                const int64_t r = p.row_of ? (int64_t)p.row_of[i] : i;
-                if (!p.row_of || (r >= 0 && r < p.m_rows))
-                    G[s] = p.scale * p.dprob[r];
             }
         }
         float x[EPL];
-        load_row<DT, EPL>(row, first, E, live, x);
+        load_row<DT, EPL, KIND>(row, first, E, live, x);
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
-            v[s] = e[s] >= 0 ? to_f32<DT>(row[e[s]]) : -INFINITY;
-            any |= e[s] >= 0;
+            G[s] = 0.0f;
+            v[s] = -INFINITY;
+            if (s * LPT < k) {
+                const bool have = r[s] >= 0 && r[s] < rows;
+                if (rows > 0)
+                    G[s] = p.dprob[have ? r[s] : 0];
+                v[s] = to_f32<DT>(row[max(e[s], 0)]);
+                G[s] = have && e[s] >= 0 ? p.scale * G[s] : 0.0f;
+                v[s] = e[s] >= 0 ? v[s] : -INFINITY;
+                any |= e[s] >= 0;
+            }
         }
 #pragma unroll
-        for (int i = 0; i < EPL; i++)
-            my_at[i] = 0.0f;
+        for (int i = 0; i < EPL; i += 4)
+            *(f32x4*)(at + g * kPitch + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         wave_sync();
 
         float top = 0.0f, inv = 0.0f;
@@ -424,7 +476,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         float pc = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; i++)
-            pc = fmaf(x[i], c[i], pc);
+            pc = fmaf(x[i], c_at(i), pc);
         pc = group_all<LPT>(pc, OpAddF()) * inv;
 
         // weights q (before scale) and their mean gradient sum q G
@@ -434,8 +486,6 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
             v[s] = p.softmax ? __expf(v[s] - top) : sigmoid(v[s]);
-            if (e[s] < 0)
-                v[s] = G[s] = 0.0f;
             chosen += v[s];
             qg = fmaf(v[s], G[s], qg);
         }
@@ -459,15 +509,15 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
             float dx[EPL];
 #pragma unroll
             for (int i = 0; i < EPL; i++) {
-                const float a = my_at[i];
+                const float a = (*(const f32x4*)(at + g * kPitch + (i & ~3)))[i & 3];
                 if (p.softmax)
-                    dx[i] = fmaf(x[i] * inv, c[i] - pull, a);
+                    dx[i] = fmaf(x[i] * inv, c_at(i) - pull, a);
                 else
-                    dx[i] = fmaf(c[i] - pc, inv, a) * x[i] * (1.0f - x[i]);
+                    dx[i] = fmaf(c_at(i) - pc, inv, a) * x[i] * (1.0f - x[i]);
                 if (!routed)
                     dx[i] = 0.0f;
             }
-            store_row<DT, EPL>((T*)p.dlogits + t * E, first, E, dx);
+            store_row<DT, EPL>((T*)p.dlogits + (int64_t)t * E, first, E, dx);
         }
         wave_sync();
     }
@@ -489,28 +539,41 @@ size_t route_workspace(int64_t T, int E) {
     return kWsHeader + ((size_t)route_blocks(T, E) * route_partial(E) + 1) / 2 * 8 + 8 * (size_t)E;
 }
 
+// Calls f with the kernels' parameters for E experts of a type: lanes a token,
+// experts a lane, how the rows load.
+template <int DT, class F>
+static hipError_t by_experts(int E, F f) {
+    constexpr int N = row_vector<DT, 8>();
+#define GG_KIND(LPT, EPL)                                                     \
+    (E % N == 0 ? f(std::integral_constant<int, LPT>(), std::integral_constant<int, EPL>(),    \
+                    std::integral_constant<int, kWholeRows>())                                     \
+                : f(std::integral_constant<int, LPT>(), std::integral_constant<int, EPL>(),    \
+                    std::integral_constant<int, kOddRows>()))
+    if (E < N)
+        return f(std::integral_constant<int, 8>(), std::integral_constant<int, 8>(),
+                 std::integral_constant<int, kShortRows>());
+    if (E <= 64)
+        return GG_KIND(8, 8);
+    if (E <= 128)
+        return GG_KIND(16, 8);
+    if (E <= 256)
+        return GG_KIND(16, 16);
+    if (E <= 512)
+        return GG_KIND(32, 16);
+    return GG_KIND(64, 16);
+#undef GG_KIND
+}
+
 template <int DT>
 static hipError_t route_dt(const RouteArgs& p, hipStream_t s, LaunchInfo* info) {
     const int64_t blocks = route_blocks(p.T, p.E);
-    const dim3 grid((unsigned)blocks), th(kThreads);
-    int lpt;
-    if (p.E <= 64) {
-        lpt = 8;
-        hipLaunchKernelGGL((route_kernel<DT, 8, 8>), grid, th, 0, s, p);
-    } else if (p.E <= 128) {
-        lpt = 16;
-        hipLaunchKernelGGL((route_kernel<DT, 16, 8>), grid, th, 0, s, p);
-    } else if (p.E <= 256) {
-        lpt = 16;
-        hipLaunchKernelGGL((route_kernel<DT, 16, 16>), grid, th, 0, s, p);
-    } else if (p.E <= 512) {
-        lpt = 32;
-        hipLaunchKernelGGL((route_kernel<DT, 32, 16>), grid, th, 0, s, p);
-    } else {
-        lpt = 64;
-        hipLaunchKernelGGL((route_kernel<DT, 64, 16>), grid, th, 0, s, p);
-    }
-    hipError_t e = hipGetLastError();
+    int lanes = 0;
+    hipError_t e = by_experts<DT>(p.E, [&](auto LPT, auto EPL, auto KIND) {
+        lanes = LPT.value;
+        hipLaunchKernelGGL((route_kernel<DT, LPT.value, EPL.value, KIND.value>), dim3((unsigned)blocks),
+                           dim3(kThreads), 0, s, p);
+        return hipGetLastError();
+    });
     if (e == hipSuccess && blocks > 1) {
         hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)((p.E + kJoinExperts - 1) / kJoinExperts)),
                            dim3(kJoinThreads), 0, s, p, (int)blocks);
@@ -518,7 +581,7 @@ static hipError_t route_dt(const RouteArgs& p, hipStream_t s, LaunchInfo* info) 
     }
     if (info) {
         snprintf(info->kernel, sizeof info->kernel, "route_kernel<%s, %d lanes a token>%s",
-                 dtype_name(DT), lpt, blocks > 1 ? " + join" : "");
+                 dtype_name(DT), lanes, blocks > 1 ? " + join" : "");
         info->tm = (int)route_tokens_per_block(p.E);
         info->tn = p.E;
         info->waves = kWaves;
@@ -532,35 +595,25 @@ hipError_t launch_route(const RouteArgs& p, int dtype, hipStream_t s, LaunchInfo
            : dtype == GG_F16 ? route_dt<GG_F16>(p, s, info) : route_dt<GG_F32>(p, s, info);
 }
 
-template <int DT, int LPT, int EPL>
-static hipError_t route_bwd_go(const RouteBwdArgs& p, hipStream_t s, LaunchInfo* info) {
-    const int64_t per = 4 * (64 / LPT);
-    int64_t blocks = (p.T + per - 1) / per;
-    if (blocks > 2048)
-        blocks = 2048;                               // eight to a CU, then more passes each
-    hipLaunchKernelGGL((route_bwd_kernel<DT, LPT, EPL>), dim3((unsigned)blocks), dim3(256), 0, s, p);
-    if (info) {
-        snprintf(info->kernel, sizeof info->kernel, "route_bwd_kernel<%s, %d lanes a token>",
-                 dtype_name(DT), LPT);
-        info->tm = (int)per;
-        info->tn = p.E;
-        info->waves = 4;
-        info->grid = blocks;
-    }
-    return hipGetLastError();
-}
-
 template <int DT>
 static hipError_t route_bwd_dt(const RouteBwdArgs& p, hipStream_t s, LaunchInfo* info) {
-    if (p.E <= 64)
-        return route_bwd_go<DT, 8, 8>(p, s, info);
-    if (p.E <= 128)
-        return route_bwd_go<DT, 16, 8>(p, s, info);
-    if (p.E <= 256)
-        return route_bwd_go<DT, 16, 16>(p, s, info);
-    if (p.E <= 512)
-        return route_bwd_go<DT, 32, 16>(p, s, info);
-    return route_bwd_go<DT, 64, 16>(p, s, info);
+    return by_experts<DT>(p.E, [&](auto LPT, auto EPL, auto KIND) {
+        const int64_t per = 4 * (64 / LPT.value);
+        int64_t blocks = (p.T + per - 1) / per;
+        if (blocks > 2048)
+            blocks = 2048;                           // eight to a CU, then more passes each
+        hipLaunchKernelGGL((route_bwd_kernel<DT, LPT.value, EPL.value, KIND.value>),
+                           dim3((unsigned)blocks), dim3(256), 0, s, p);
+        if (info) {
+            snprintf(info->kernel, sizeof info->kernel, "route_bwd_kernel<%s, %d lanes a token>",
+                     dtype_name(DT), LPT.value);
+            info->tm = (int)per;
+            info->tn = p.E;
+            info->waves = 4;
+            info->grid = blocks;
+        }
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_route_bwd(const RouteBwdArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
