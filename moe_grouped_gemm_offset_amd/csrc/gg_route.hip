@@ -161,17 +161,37 @@ __device__ __forceinline__ float choice_top(const float (&v)[NJ]) {
 
 }  // namespace
 
-// Workspace: header (int32 1: the finishing ticket), then per block the
-// int32 counts and fp32 probability sums of the E experts and the routed
-// tokens, [blocks][2E + 1], then a double per expert.
-__host__ __device__ inline int64_t route_partial(int E) { return 2 * (int64_t)E + 1; }
+// Workspace: header (int32 1: the finishing ticket; 4 + 2q, 5 + 2q: quarter
+// q's routed tokens as a double), then the blocks' counts and probability
+// sums as pairs, 16 experts (a 128-byte line) of a block after another's:
+// [ceil(E / 16)][blocks][16], the blocks' routed tokens, and what the joining
+// blocks have made of a quarter of the blocks each, [4][E].
+struct RoutePair {
+    int32_t count;
+    float sum;
+};
+struct RouteJoined {
+    double sum;
+    int64_t count;
+};
+constexpr int kMaxRouteBlocks = 768;                 // three to a CU, then more passes each
+constexpr int kLine = 16, kQuarters = 4;
+
+__host__ __device__ inline int64_t route_lines(int E) { return (E + kLine - 1) / kLine; }
+__device__ inline RoutePair* route_pairs(int32_t* ws) { return (RoutePair*)(ws + kWsHeader / 4); }
+__device__ inline int32_t* route_routed(int32_t* ws, int E, int blocks) {
+    return (int32_t*)(route_pairs(ws) + route_lines(E) * blocks * kLine);
+}
+__device__ inline RouteJoined* route_joined(int32_t* ws, int E, int blocks) {
+    return (RouteJoined*)(route_routed(ws, E, blocks) + (blocks + 3) / 4 * 4);
+}
 
 // One token per group of LPT lanes and pass.  The choice: every lane keeps
 // the largest key of its EPL; a step takes the group's largest (ties: the
 // lowest lane, so the lowest experts), rescans that lane's keys -- in LDS,
 // one per lane of the group -- for the expert, removes it and hands the lane
 // its next largest.
-template <int DT, int LPT, int EPL, int KIND>
+template <int DT, int LPT, int EPL, int KIND, int SCORE>
 __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     static_assert(EPL <= LPT, "a group rescans one lane's keys in one read");
     constexpr int TPW = 64 / LPT;                    // tokens per wave
@@ -188,7 +208,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     const int g = lane & (LPT - 1), sub = lane / LPT;
     const int first = g * EPL;
     const int E = p.E, k = p.k;
-    const bool softmax = p.softmax, stats = p.balance != nullptr;
+    constexpr bool softmax = SCORE == GG_SOFTMAX;
+    const bool stats = p.balance != nullptr;
     uint32_t* group_keys = keys + (wave * TPW + sub) * LPT * kPitch;
 
     for (int e = tid; e < kCap; e += kThreads)
@@ -308,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     __syncthreads();
     const bool last = gridDim.x == 1;
     const int groups = (int)min((int64_t)kWaves * TPW, p.T);     // that had a token
-    int32_t* part = p.ws + kWsHeader / 4 + blockIdx.x * route_partial(E);
+    const int blocks = gridDim.x;
     double loss = 0.0;
     for (int e = tid; e < E; e += kThreads) {
         float s = 0.0f;
@@ -319,13 +340,12 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
             p.counts[e] = hist[e];
             loss += (double)hist[e] * (double)s;
         } else {
-            part[e] = hist[e];
-            part[E + e] = __builtin_bit_cast(int32_t, s);
+            route_pairs(p.ws)[((int64_t)(e / kLine) * blocks + blockIdx.x) * kLine + e % kLine] = {hist[e], s};
         }
     }
     if (!last) {
         if (tid == 0)
-            part[2 * E] = nrouted;
+            route_routed(p.ws, E, blocks)[blockIdx.x] = nrouted;
         return;
     }
     // a single block finishes here
@@ -340,63 +360,108 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     }
 }
 
-// Joins the blocks' counts and probability sums: 16 experts a block, 64
-// runs of blocks each; the block that finishes last adds up the loss.
-constexpr int kJoinExperts = 16, kJoinRuns = 64, kJoinThreads = kJoinExperts * kJoinRuns;
+// Joins the blocks' counts and probability sums: a block takes 16 experts
+// over a quarter of the blocks, eight lanes a line; the one that finishes
+// last adds up the quarters and the loss.
+constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(RouteArgs p, int blocks) {
-    __shared__ int32_t cnt[kJoinRuns][kJoinExperts];
-    __shared__ double sum[kJoinRuns][kJoinExperts];
+    constexpr int kRows = kJoinThreads / 8;          // lines read at once
+    constexpr int kEach = kMaxRouteBlocks / kQuarters / kRows;
+    static_assert(kEach * kRows * kQuarters == kMaxRouteBlocks, "a quarter's lines are whole rows");
+    __shared__ RouteJoined part[kJoinThreads / 64][kLine];
     __shared__ double tmp[kJoinThreads / 64];
     __shared__ int32_t is_last;
-    const int tid = threadIdx.x, E = p.E;
-    const int run = tid / kJoinExperts, lane = tid % kJoinExperts;
-    const int e = blockIdx.x * kJoinExperts + lane;
-    const int32_t* part = p.ws + kWsHeader / 4;
-    const int64_t pitch = route_partial(E);
-    const int each = (blocks + kJoinRuns - 1) / kJoinRuns;
-    const int b1 = min(blocks, (run + 1) * each);
-    int32_t c = 0;
-    double s = 0.0;
-    if (e < E) {
-        for (int b = run * each; b < b1; b++) {
-            c += part[b * pitch + e];
-            s += (double)__builtin_bit_cast(float, part[b * pitch + E + e]);
+    const int tid = threadIdx.x, E = p.E, lane = tid & 63, wave = tid >> 6;
+    const int group = blockIdx.x, quarter = blockIdx.y;
+    const int b0 = quarter * (kMaxRouteBlocks / kQuarters);
+    const RoutePair* lines = route_pairs(p.ws) + (int64_t)group * blocks * kLine + (tid & 7) * 2;
+    // all loads at once, at clamped addresses
+    RoutePair in[kEach][2];
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        const RoutePair* q = lines + min(b0 + i * kRows + tid / 8, blocks - 1) * kLine;
+        in[i][0] = q[0];
+        in[i][1] = q[1];
+    }
+    int32_t c[2] = {0, 0};
+    double s[2] = {0.0, 0.0};
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        const bool have = b0 + i * kRows + tid / 8 < blocks;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            c[h] += have ? in[i][h].count : 0;
+            s[h] += have ? (double)in[i][h].sum : 0.0;
         }
     }
-    cnt[run][lane] = c;
-    sum[run][lane] = s;
-    __syncthreads();
-    double* terms = (double*)(p.ws + kWsHeader / 4 + ((int64_t)blocks * pitch + 1) / 2 * 2);
-    if (run == 0 && e < E) {
-        for (int r = 1; r < kJoinRuns; r++) {
-            c += cnt[r][lane];
-            s += sum[r][lane];
+    double routed = 0.0;
+    if (group == 0) {
+        const int32_t* n = route_routed(p.ws, E, blocks);
+        const int b = b0 + tid;
+        routed = tid < kMaxRouteBlocks / kQuarters && b < blocks ? (double)n[b] : 0.0;
+        routed = block_sum<kJoinThreads>(routed, tmp);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+        for (int x = 8; x < 64; x <<= 1) {
+            c[h] += __shfl_xor(c[h], x);
+            s[h] += __shfl_xor(s[h], x);
         }
-        p.counts[e] = c;
-        __hip_atomic_store(&terms[e], (double)c * s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __threadfence();                             // before this block's ticket
+        if (lane < 8)
+            part[wave][lane * 2 + h] = {s[h], c[h]};
     }
     __syncthreads();
-    if (tid == 0)
-        is_last = __hip_atomic_fetch_add(&p.ws[1], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                  (int)gridDim.x - 1;
+    RouteJoined* joined = route_joined(p.ws, E, blocks);
+    double* header = (double*)p.ws + 2;              // each quarter's routed tokens
+    if (tid < 64) {                                  // one wave stores, then takes the ticket
+        const int e = group * kLine + tid;
+        if (tid < kLine && e < E) {
+            RouteJoined j = part[0][tid];
+#pragma unroll
+            for (int w = 1; w < kJoinThreads / 64; w++) {
+                j.sum += part[w][tid].sum;
+                j.count += part[w][tid].count;
+            }
+            RouteJoined* to = &joined[(int64_t)quarter * E + e];
+            __hip_atomic_store(&to->sum, j.sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&to->count, j.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (group == 0 && tid == 0)
+            __hip_atomic_store(&header[quarter], routed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __threadfence();
+        if (tid == 0)
+            is_last = __hip_atomic_fetch_add(&p.ws[1], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                      (int)(gridDim.x * gridDim.y) - 1;
+    }
     __syncthreads();
     if (!is_last)
         return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     double loss = 0.0;
-    int32_t n = 0;
-    for (int i = tid; i < E; i += kJoinThreads)
-        loss += __hip_atomic_load(&terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int b = tid; b < blocks; b += kJoinThreads)
-        n += part[b * pitch + 2 * E];
+    for (int e = tid; e < E; e += kJoinThreads) {
+        RouteJoined j = {0.0, 0};
+#pragma unroll
+        for (int q = 0; q < kQuarters; q++) {
+            j.sum += __hip_atomic_load(&joined[(int64_t)q * E + e].sum, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+            j.count += __hip_atomic_load(&joined[(int64_t)q * E + e].count, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+        }
+        p.counts[e] = (int32_t)j.count;
+        loss += (double)j.count * j.sum;
+    }
+    double n = 0.0;
+#pragma unroll
+    for (int q = 0; q < kQuarters; q++)
+        n += __hip_atomic_load(&header[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     loss = block_sum<kJoinThreads>(loss, tmp);
-    n = (int32_t)block_sum<kJoinThreads>((double)n, tmp);
     if (tid == 0) {
-        p.routed[0] = n;
+        p.routed[0] = (int32_t)n;
         if (p.balance) {
-            const double m = n > 0 ? (double)n : 1.0;
-            p.balance[0] = (float)((double)E * loss / ((double)p.k * m * m));
+            n = n > 0.0 ? n : 1.0;
+            p.balance[0] = (float)((double)E * loss / ((double)p.k * n * n));
         }
     }
 }
@@ -525,18 +590,19 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
 
 // ---- launches --------------------------------------------------------------
 
-// Blocks of a route call: a block takes kWaves waves of tokens a pass; up to
-// 512 of them (two to a CU), then more passes each.
+// Blocks of a route call: a block takes kWaves waves of tokens a pass.
 static int64_t route_tokens_per_block(int E) { return kWaves * (E <= 64 ? 8 : E <= 256 ? 4 : E <= 512 ? 2 : 1); }
 
 int64_t route_blocks(int64_t T, int E) {
     const int64_t per = route_tokens_per_block(E);
     const int64_t b = (T + per - 1) / per;
-    return b < 1 ? 1 : b > 512 ? 512 : b;
+    return b < 1 ? 1 : b > kMaxRouteBlocks ? kMaxRouteBlocks : b;
 }
 
 size_t route_workspace(int64_t T, int E) {
-    return kWsHeader + ((size_t)route_blocks(T, E) * route_partial(E) + 1) / 2 * 8 + 8 * (size_t)E;
+    const size_t b = (size_t)route_blocks(T, E);
+    return kWsHeader + (size_t)route_lines(E) * b * kLine * sizeof(RoutePair) + (b + 3) / 4 * 16 +
+           kQuarters * (size_t)E * sizeof(RouteJoined);
 }
 
 // Calls f with the kernels' parameters for E experts of a type: lanes a token,
@@ -570,12 +636,16 @@ static hipError_t route_dt(const RouteArgs& p, hipStream_t s, LaunchInfo* info) 
     int lanes = 0;
     hipError_t e = by_experts<DT>(p.E, [&](auto LPT, auto EPL, auto KIND) {
         lanes = LPT.value;
-        hipLaunchKernelGGL((route_kernel<DT, LPT.value, EPL.value, KIND.value>), dim3((unsigned)blocks),
-                           dim3(kThreads), 0, s, p);
+        if (p.softmax)
+            hipLaunchKernelGGL((route_kernel<DT, LPT.value, EPL.value, KIND.value, GG_SOFTMAX>),
+                               dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
+        else
+            hipLaunchKernelGGL((route_kernel<DT, LPT.value, EPL.value, KIND.value, GG_SIGMOID>),
+                               dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
         return hipGetLastError();
     });
     if (e == hipSuccess && blocks > 1) {
-        hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)((p.E + kJoinExperts - 1) / kJoinExperts)),
+        hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)route_lines(p.E), kQuarters),
                            dim3(kJoinThreads), 0, s, p, (int)blocks);
         e = hipGetLastError();
     }
