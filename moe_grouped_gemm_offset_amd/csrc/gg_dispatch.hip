@@ -1,6 +1,8 @@
 // gg_dispatch.hip -- tokens to the expert-sorted rows the grouped GEMMs take,
 // and back: the row of every (token, choice), the copies, the weighted sum
 // of a token's rows and that sum's gradients.
+#include <type_traits>
+
 #include "gg_internal.hpp"
 #include "gg_lane.hpp"
 
@@ -254,9 +256,15 @@ struct RowElem {
     static constexpr int N = 16 / (int)sizeof(T);
 };
 
+// Which of its block's tokens a wave works on (a scalar: tx is 64 at least).
+__device__ __forceinline__ int wave_token(int tx) {
+    return __builtin_amdgcn_readfirstlane((int)threadIdx.x / tx);
+}
+
 // x_rows[row_of[t, j]] = x[t], zeros in the padding.  SIZE: bytes of an
-// element; the values are copied as they are.
-template <int SIZE>
+// element; the values are copied as they are.  Every row of x is read once
+// and written k times.
+template <int SIZE, bool NT>
 __global__ void __launch_bounds__(kRowThreads) permute_kernel(RowsArgs p, int tx, int pads) {
     typedef typename Raw<16>::T V;
     const int col = threadIdx.x % tx + (int)blockIdx.y * tx;
@@ -266,6 +274,12 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(RowsArgs p, int tx
         return;
     const bool whole = at + 16 <= bytes;
     char* out = (char*)p.rows_out;
+    auto put = [&](int64_t r, V v) {
+        if constexpr (NT)
+            __builtin_nontemporal_store(v, (V*)(out + r * bytes + at));
+        else
+            *(V*)(out + r * bytes + at) = v;
+    };
     if ((int)blockIdx.x < pads) {
         const int e = blockIdx.x / kPadParts, part = blockIdx.x % kPadParts;
         const int ty = kRowThreads / tx;
@@ -274,42 +288,48 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(RowsArgs p, int tx
         for (int64_t r = (int64_t)max(begin, 0) + max(p.counts[e], 0) + part * ty + threadIdx.x / tx; r < r1;
              r += kPadParts * ty) {
             if (whole)
-                *(V*)(out + r * bytes + at) = V{0, 0, 0, 0};
+                put(r, V{0, 0, 0, 0});
             else
                 for (int64_t b = at; b < bytes; b++)
                     out[r * bytes + b] = 0;
         }
         return;
     }
-    const int64_t t = (int64_t)(blockIdx.x - pads) * (kRowThreads / tx) + threadIdx.x / tx;
+    const int64_t t = (int64_t)(blockIdx.x - pads) * (kRowThreads / tx) + wave_token(tx);
     if (t >= p.T)
         return;
     const char* in = (const char*)p.tokens + t * p.ld * SIZE;
-    if (whole) {
-        const V v = *(const V*)(in + at);
-        for (int j = 0; j < p.k; j++) {
-            const int64_t r = p.row_of[t * p.k + j];
-            if (r >= 0 && r < p.m_rows)
-                *(V*)(out + r * bytes + at) = v;
-        }
-    } else {
-        for (int j = 0; j < p.k; j++) {
-            const int64_t r = p.row_of[t * p.k + j];
-            if (r >= 0 && r < p.m_rows)
+    const int32_t* row_of = p.row_of + t * p.k;
+    V v = {0, 0, 0, 0};
+    if (whole)
+        v = *(const V*)(in + at);
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        int r[8];                                    // eight rows' numbers before the stores
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            r[j] = row_of[min(j0 + j, p.k - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if (j0 + j >= p.k || r[j] < 0 || r[j] >= p.m_rows)
+                continue;
+            if (whole)
+                put(r[j], v);
+            else
                 for (int64_t b = at; b < bytes; b++)
-                    out[r * bytes + b] = in[b];
+                    out[r[j] * bytes + b] = in[b];
         }
     }
 }
 
 // out[t] = sum_j w[t, j] y[row_of[t, j]], in fp32 in the order of j, rounded
-// once.
-template <int DT>
+// once.  KB rows' loads at once; a choice without a row loads row 0 and adds
+// nothing.
+template <int DT, int KB, bool NT>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(RowsArgs p, int tx) {
     typedef typename Elem<DT>::T T;
     constexpr int N = RowElem<DT>::N;
     const int c = (threadIdx.x % tx + (int)blockIdx.y * tx) * N;
-    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / tx) + threadIdx.x / tx;
+    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / tx) + wave_token(tx);
     if (t >= p.T || c >= p.width)
         return;
     const T* y = (const T*)p.rows_in;
@@ -321,20 +341,30 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(RowsArgs p, int tx
 #pragma unroll
         for (int i = 0; i < N; i++)
             acc[i] = 0.0f;
-        for (int j = 0; j < p.k; j++) {
-            const int64_t r = row_of[j];
-            if (r < 0 || r >= p.m_rows)
-                continue;
-            Vec<DT, N> v;
-            v.load(y + r * p.width + c);
-            const float wj = w ? w[j] : 1.0f;
+        for (int j0 = 0; p.m_rows > 0 && j0 < p.k; j0 += KB) {
+            int r[KB];
+            float wj[KB];
+            Vec<DT, N> v[KB];
 #pragma unroll
-            for (int i = 0; i < N; i++)
-                acc[i] = fmaf(wj, v.get(i), acc[i]);
+            for (int j = 0; j < KB; j++) {
+                const int at = min(j0 + j, p.k - 1);
+                r[j] = row_of[at];
+                r[j] = j0 + j < p.k && r[j] < p.m_rows ? r[j] : -1;
+                wj[j] = w ? w[at] : 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < KB; j++)
+                v[j].template load<NT>(y + (int64_t)max(r[j], 0) * p.width + c);
+#pragma unroll
+            for (int j = 0; j < KB; j++)
+                if (r[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < N; i++)
+                        acc[i] = fmaf(wj[j], v[j].get(i), acc[i]);
         }
         Vec<DT, N> v;
         v.set(acc);
-        v.store(out + c);
+        v.template store<NT>(out + c);
     } else {
         for (int i = c; i < p.width; i++) {
             float acc = 0.0f;
@@ -349,30 +379,29 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(RowsArgs p, int tx
 }
 
 // dy[row_of[t, j]] = w[t, j] dout[t] (rounded once; zeros in the padding),
-// dw[t, j] = <dout[t], y[row_of[t, j]]> in fp32.  A block a token; the first
-// `pads` blocks clear the padding.
-template <int DT>
+// dw[t, j] = <dout[t], y[row_of[t, j]]> in fp32.  A block a token; KB rows by
+// U vectors of loads at once.  The first `pads` blocks clear the padding.
+template <int DT, int KB, int U, bool NT>
 __global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(RowsArgs p, int pads) {
     typedef typename Elem<DT>::T T;
-    constexpr int N = RowElem<DT>::N, KB = 8;
+    constexpr int N = RowElem<DT>::N;
     __shared__ float part[kRowThreads / 64][KB];
     T* dy = (T*)p.rows_out;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, threads = blockDim.x;
+    const int vecs = p.width / N;                    // whole ones; the rest is `rest` elements
+    const int rest = p.width - vecs * N;
     if ((int)blockIdx.x < pads) {
         const int e = blockIdx.x / kPadParts, sub = blockIdx.x % kPadParts;
         const int begin = e ? p.ends[e - 1] : 0;
         const int64_t r1 = min((int64_t)p.ends[e], p.m_rows);
-        for (int64_t r = (int64_t)max(begin, 0) + max(p.counts[e], 0) + sub; r < r1; r += kPadParts)
-            for (int c = tid * N; c < p.width; c += kRowThreads * N) {
-                if (c + N <= p.width) {
-                    Vec<DT, N> z;
-                    z.raw = 0;
-                    z.store(dy + r * p.width + c);
-                } else {
-                    for (int i = c; i < p.width; i++)
-                        dy[r * p.width + i] = 0;
-                }
-            }
+        for (int64_t r = (int64_t)max(begin, 0) + max(p.counts[e], 0) + sub; r < r1; r += kPadParts) {
+            Vec<DT, N> z;
+            z.raw = 0;
+            for (int i = tid; i < vecs; i += threads)
+                z.template store<NT>(dy + r * p.width + i * N);
+            if (tid < rest)
+                dy[r * p.width + vecs * N + tid] = 0;
+        }
         return;
     }
     const int64_t t = blockIdx.x - pads;
@@ -380,45 +409,58 @@ __global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(RowsArgs p, in
     const T* y = (const T*)p.rows_in;
     for (int j0 = 0; j0 < p.k; j0 += KB) {
         const int kb = min(KB, p.k - j0);
-        int64_t row[KB];
+        int row[KB];
         float w[KB], dot[KB];
 #pragma unroll
         for (int j = 0; j < KB; j++) {
-            const int64_t r = j < kb ? p.row_of[t * p.k + j0 + j] : -1;
-            row[j] = r >= 0 && r < p.m_rows ? r : -1;
-            w[j] = j < kb ? p.weights[t * p.k + j0 + j] : 0.0f;
+            const int64_t at = t * p.k + j0 + min(j, kb - 1);
+            row[j] = p.row_of[at];
+            row[j] = j < kb && row[j] < p.m_rows ? row[j] : -1;
+            w[j] = p.weights[at];
             dot[j] = 0.0f;
         }
-        for (int c = tid * N; c < p.width; c += kRowThreads * N) {
-            if (c + N <= p.width) {
-                Vec<DT, N> d;
-                d.load(dout + c);
+        // (with no rows at all there is nothing to load)
+        for (int i0 = tid; p.m_rows > 0 && i0 < vecs; i0 += U * threads) {
+            Vec<DT, N> d[U], v[U][KB];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int c = min(i0 + u * threads, vecs - 1) * N;
+                d[u].template load<NT>(dout + c);
+#pragma unroll
+                for (int j = 0; j < KB; j++)
+                    v[u][j].template load<NT>(y + (int64_t)max(row[j], 0) * p.width + c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                if (i0 + u * threads >= vecs)
+                    break;
+                const int c = (i0 + u * threads) * N;
 #pragma unroll
                 for (int j = 0; j < KB; j++) {
                     if (row[j] < 0)
                         continue;
-                    Vec<DT, N> v;
+                    Vec<DT, N> o;
                     float f[N];
-                    v.load(y + row[j] * p.width + c);
 #pragma unroll
                     for (int i = 0; i < N; i++) {
-                        dot[j] = fmaf(d.get(i), v.get(i), dot[j]);
-                        f[i] = w[j] * d.get(i);
+                        dot[j] = fmaf(d[u].get(i), v[u][j].get(i), dot[j]);
+                        f[i] = w[j] * d[u].get(i);
                     }
-                    v.set(f);
-                    v.store(dy + row[j] * p.width + c);
-                }
-            } else {
-                for (int i = c; i < p.width; i++) {
-                    const float d = to_f32<DT>(dout[i]);
-#pragma unroll
-                    for (int j = 0; j < KB; j++)
-                        if (row[j] >= 0) {
-                            dot[j] = fmaf(d, to_f32<DT>(y[row[j] * p.width + i]), dot[j]);
-                            dy[row[j] * p.width + i] = from_f32<DT>(w[j] * d);
-                        }
+                    o.set(f);
+                    o.template store<NT>(dy + (int64_t)row[j] * p.width + c);
                 }
             }
+        }
+        if (tid < rest) {
+            const int c = vecs * N + tid;
+            const float d = to_f32<DT>(dout[c]);
+#pragma unroll
+            for (int j = 0; j < KB; j++)
+                if (row[j] >= 0) {
+                    const int64_t at = (int64_t)row[j] * p.width + c;
+                    dot[j] = fmaf(d, to_f32<DT>(y[at]), dot[j]);
+                    dy[at] = from_f32<DT>(w[j] * d);
+                }
         }
 #pragma unroll
         for (int j = 0; j < KB; j++) {
@@ -427,15 +469,20 @@ __global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(RowsArgs p, in
                 part[tid >> 6][j] = s;
         }
         __syncthreads();
-        if (tid < kb)
-            p.dweights[t * p.k + j0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        if (tid < kb) {
+            float s = part[0][tid];
+            for (int x = 1; x < threads / 64; x++)
+                s += part[x][tid];
+            p.dweights[t * p.k + j0 + tid] = s;
+        }
         __syncthreads();
     }
 }
 
-// Threads of a block along a row of `vecs` vectors: a power of two up to 256.
+// Threads of a block along a row of `vecs` vectors: a power of two, whole waves,
+// up to 256.
 int row_threads(int64_t vecs) {
-    int tx = 1;
+    int tx = 64;
     while (tx < vecs && tx < kRowThreads)
         tx *= 2;
     return tx;
@@ -496,18 +543,44 @@ static void rows_info(LaunchInfo* info, const char* name, int dtype, int tokens,
 
 static int elem_bytes(int dtype) { return dtype == GG_F32 ? 4 : dtype == GG_BF16 || dtype == GG_F16 ? 2 : 1; }
 
+// Whether the expert rows of a call are more than the 256 MB cache in front
+// of the memory holds: they then pass it by.
+static bool past_cache(const RowsArgs& p, int size) {
+    return p.T * p.k * (int64_t)p.width * size > (int64_t)256 << 20;
+}
+
+// f(std::integral_constant) of a type, of a truth value.
+template <class F>
+static void by_dtype(int dtype, F f) {
+    if (dtype == GG_BF16)
+        f(std::integral_constant<int, GG_BF16>());
+    else if (dtype == GG_F16)
+        f(std::integral_constant<int, GG_F16>());
+    else
+        f(std::integral_constant<int, GG_F32>());
+}
+template <class F>
+static void by_bool(bool b, F f) {
+    if (b)
+        f(std::true_type());
+    else
+        f(std::false_type());
+}
+
 hipError_t launch_permute(const RowsArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
     const int size = elem_bytes(dtype);
     const int64_t vecs = ((int64_t)p.width * size + 15) / 16;
     const int tx = row_threads(vecs), ty = kRowThreads / tx;
     const int pads = p.E * kPadParts;
     const dim3 grid((unsigned)(pads + (p.T + ty - 1) / ty), (unsigned)((vecs + tx - 1) / tx));
-    if (size == 1)
-        hipLaunchKernelGGL((permute_kernel<1>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
-    else if (size == 2)
-        hipLaunchKernelGGL((permute_kernel<2>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
-    else
-        hipLaunchKernelGGL((permute_kernel<4>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
+    by_bool(past_cache(p, size), [&](auto NT) {
+        if (size == 1)
+            hipLaunchKernelGGL((permute_kernel<1, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
+        else if (size == 2)
+            hipLaunchKernelGGL((permute_kernel<2, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
+        else
+            hipLaunchKernelGGL((permute_kernel<4, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx, pads);
+    });
     rows_info(info, "permute_kernel", dtype, ty, tx * 16 / size, (int64_t)grid.x * grid.y);
     return hipGetLastError();
 }
@@ -519,25 +592,36 @@ hipError_t launch_combine(const RowsArgs& p, int dtype, hipStream_t s, LaunchInf
     const int64_t vecs = ((int64_t)p.width * size + 15) / 16;
     const int tx = row_threads(vecs), ty = kRowThreads / tx;
     const dim3 grid((unsigned)((p.T + ty - 1) / ty), (unsigned)((vecs + tx - 1) / tx));
-    if (dtype == GG_BF16)
-        hipLaunchKernelGGL((combine_kernel<GG_BF16>), grid, dim3(kRowThreads), 0, s, p, tx);
-    else if (dtype == GG_F16)
-        hipLaunchKernelGGL((combine_kernel<GG_F16>), grid, dim3(kRowThreads), 0, s, p, tx);
-    else
-        hipLaunchKernelGGL((combine_kernel<GG_F32>), grid, dim3(kRowThreads), 0, s, p, tx);
+    by_dtype(dtype, [&](auto DT) {
+        by_bool(past_cache(p, size), [&](auto NT) {
+            if (p.k <= 2)
+                hipLaunchKernelGGL((combine_kernel<DT.value, 2, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx);
+            else if (p.k <= 4)
+                hipLaunchKernelGGL((combine_kernel<DT.value, 4, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx);
+            else
+                hipLaunchKernelGGL((combine_kernel<DT.value, 8, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx);
+        });
+    });
     rows_info(info, "combine_kernel", dtype, ty, tx * 16 / size, (int64_t)grid.x * grid.y);
     return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const RowsArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
+    const int size = elem_bytes(dtype);
     const int pads = p.E * kPadParts;
     const dim3 grid((unsigned)(pads + p.T));
-    if (dtype == GG_BF16)
-        hipLaunchKernelGGL((combine_bwd_kernel<GG_BF16>), grid, dim3(kRowThreads), 0, s, p, pads);
-    else if (dtype == GG_F16)
-        hipLaunchKernelGGL((combine_bwd_kernel<GG_F16>), grid, dim3(kRowThreads), 0, s, p, pads);
-    else
-        hipLaunchKernelGGL((combine_bwd_kernel<GG_F32>), grid, dim3(kRowThreads), 0, s, p, pads);
+    const int64_t vecs = ((int64_t)p.width * size + 15) / 16;
+    const dim3 threads((unsigned)(vecs >= kRowThreads ? kRowThreads : (vecs + 63) / 64 * 64));
+    by_dtype(dtype, [&](auto DT) {
+        by_bool(past_cache(p, size), [&](auto NT) {
+            if (p.k <= 2)
+                hipLaunchKernelGGL((combine_bwd_kernel<DT.value, 2, 4, NT.value>), grid, threads, 0, s, p, pads);
+            else if (p.k <= 4)
+                hipLaunchKernelGGL((combine_bwd_kernel<DT.value, 4, 2, NT.value>), grid, threads, 0, s, p, pads);
+            else
+                hipLaunchKernelGGL((combine_bwd_kernel<DT.value, 8, 1, NT.value>), grid, threads, 0, s, p, pads);
+        });
+    });
     rows_info(info, "combine_bwd_kernel", dtype, 1, p.width, grid.x);
     return hipGetLastError();
 }

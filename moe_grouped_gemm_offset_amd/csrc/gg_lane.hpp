@@ -63,8 +63,18 @@ struct Vec {
     typedef typename Raw<kBytes>::T T;
     T raw;
 
-    __device__ __forceinline__ void load(const typename Elem<DT>::T* p) { raw = *(const T*)p; }
-    __device__ __forceinline__ void store(typename Elem<DT>::T* p) const { *(T*)p = raw; }
+    // NT: values that are not used again soon pass the caches by
+    template <bool NT = false>
+    __device__ __forceinline__ void load(const typename Elem<DT>::T* p) {
+        raw = NT ? __builtin_nontemporal_load((const T*)p) : *(const T*)p;
+    }
+    template <bool NT = false>
+    __device__ __forceinline__ void store(typename Elem<DT>::T* p) const {
+        if constexpr (NT)
+            __builtin_nontemporal_store(raw, (T*)p);
+        else
+            *(T*)p = raw;
+    }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (DT == GG_F32)
             return __builtin_bit_cast(float, (uint32_t)raw[i]);
