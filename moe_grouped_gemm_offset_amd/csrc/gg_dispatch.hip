@@ -322,9 +322,8 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(RowsArgs p, int tx
 }
 
 // out[t] = sum_j w[t, j] y[row_of[t, j]], in fp32 in the order of j, rounded
-// once.  KB rows' loads at once; a choice without a row loads row 0 and adds
-// nothing.
-template <int DT, int KB, bool NT>
+// once.
+template <int DT, bool NT>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(RowsArgs p, int tx) {
     typedef typename Elem<DT>::T T;
     constexpr int N = RowElem<DT>::N;
@@ -341,26 +340,16 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(RowsArgs p, int tx
 #pragma unroll
         for (int i = 0; i < N; i++)
             acc[i] = 0.0f;
-        for (int j0 = 0; p.m_rows > 0 && j0 < p.k; j0 += KB) {
-            int r[KB];
-            float wj[KB];
-            Vec<DT, N> v[KB];
+        for (int j = 0; j < p.k; j++) {
+            const int64_t r = row_of[j];
+            if (r < 0 || r >= p.m_rows)
+                continue;
+            Vec<DT, N> v;
+            v.template load<NT>(y + r * p.width + c);
+            const float wj = w ? w[j] : 1.0f;
 #pragma unroll
-            for (int j = 0; j < KB; j++) {
-                const int at = min(j0 + j, p.k - 1);
-                r[j] = row_of[at];
-                r[j] = j0 + j < p.k && r[j] < p.m_rows ? r[j] : -1;
-                wj[j] = w ? w[at] : 1.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < KB; j++)
-                v[j].template load<NT>(y + (int64_t)max(r[j], 0) * p.width + c);
-#pragma unroll
-            for (int j = 0; j < KB; j++)
-                if (r[j] >= 0)
-#pragma unroll
-                    for (int i = 0; i < N; i++)
-                        acc[i] = fmaf(wj[j], v[j].get(i), acc[i]);
+            for (int i = 0; i < N; i++)
+                acc[i] = fmaf(wj, v.get(i), acc[i]);
         }
         Vec<DT, N> v;
         v.set(acc);
@@ -594,12 +583,7 @@ hipError_t launch_combine(const RowsArgs& p, int dtype, hipStream_t s, LaunchInf
     const dim3 grid((unsigned)((p.T + ty - 1) / ty), (unsigned)((vecs + tx - 1) / tx));
     by_dtype(dtype, [&](auto DT) {
         by_bool(past_cache(p, size), [&](auto NT) {
-            if (p.k <= 2)
-                hipLaunchKernelGGL((combine_kernel<DT.value, 2, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx);
-            else if (p.k <= 4)
-                hipLaunchKernelGGL((combine_kernel<DT.value, 4, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx);
-            else
-                hipLaunchKernelGGL((combine_kernel<DT.value, 8, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx);
+            hipLaunchKernelGGL((combine_kernel<DT.value, NT.value>), grid, dim3(kRowThreads), 0, s, p, tx);
         });
     });
     rows_info(info, "combine_kernel", dtype, ty, tx * 16 / size, (int64_t)grid.x * grid.y);
