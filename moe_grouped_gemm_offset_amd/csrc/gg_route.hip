@@ -88,7 +88,7 @@ __device__ __forceinline__ void load_row(const typename Elem<DT>::T* row, int fi
             x[i] = live && first + i < E ? x[i] : -INFINITY;
 }
 
-template <int DT, int EPL>
+template <int DT, int EPL, int KIND>
 __device__ __forceinline__ void store_row(typename Elem<DT>::T* row, int first, int E,
                                           const float (&x)[EPL]) {
     constexpr int N = row_vector<DT, EPL>();
@@ -102,7 +102,7 @@ __device__ __forceinline__ void store_row(typename Elem<DT>::T* row, int first, 
                 f[i] = x[c + i];
             v.set(f);
             v.store(row + first + c);
-        } else {
+        } else if constexpr (KIND != kWholeRows) {
 #pragma unroll
             for (int i = 0; i < N; i++)
                 if (first + c + i < E)
@@ -468,8 +468,9 @@ __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(RouteArgs p, i
 
 // The gradient of the logits.  The chosen experts' gradients go into an LDS
 // row, a lane each, and every lane takes its EPL from there.
-template <int DT, int LPT, int EPL, int KIND>
+template <int DT, int LPT, int EPL, int KIND, int SCORE>
 __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
+    constexpr bool softmax = SCORE == GG_SOFTMAX;
     constexpr int TPW = 64 / LPT;
     constexpr int NJ = LPT >= 32 ? 1 : 32 / LPT;
     constexpr int kCap = LPT * EPL, kPitch = lane_pitch<EPL>();
@@ -488,7 +489,6 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
     for (int e = tid; e < kCap; e += 256)
         c[e / EPL * kPitch + e % EPL] = e < E ? cb * (float)p.counts[e] : 0.0f;
     __syncthreads();
-    auto c_at = [&](int i) { return (*(const f32x4*)(c + g * kPitch + (i & ~3)))[i & 3]; };
 
     const int64_t rows = p.row_of ? p.m_rows : p.T * k;
     const int T_ = (int)p.T;                         // at most 2^23
@@ -511,8 +511,6 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
                 const int i = live && j < k ? t * k + j : 0;
                 e[s] = p.ids[i];
                 r[s] = p.row_of ? p.row_of[i] : i;
-                if (!live || j >= k || e[s] >= E)
-                    e[s] = -1;
             }
         }
         float x[EPL];
@@ -523,6 +521,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
             v[s] = -INFINITY;
             if (s * LPT < k) {
                 const bool have = r[s] >= 0 && r[s] < rows;
+                e[s] = live && g + s * LPT < k && e[s] < E ? e[s] : -1;
                 if (rows > 0)
                     G[s] = p.dprob[have ? r[s] : 0];
                 v[s] = to_f32<DT>(row[max(e[s], 0)]);
@@ -537,26 +536,30 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         wave_sync();
 
         float top = 0.0f, inv = 0.0f;
-        row_scores<LPT, EPL>(x, p.softmax, top, inv);
+        row_scores<LPT, EPL>(x, softmax, top, inv);
         float pc = 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPL; i++)
-            pc = fmaf(x[i], c_at(i), pc);
+        for (int i = 0; i < EPL; i += 4) {
+            const f32x4 four = *(const f32x4*)(c + g * kPitch + i);
+#pragma unroll
+            for (int h = 0; h < 4; h++)
+                pc = fmaf(x[i + h], four[h], pc);
+        }
         pc = group_all<LPT>(pc, OpAddF()) * inv;
 
         // weights q (before scale) and their mean gradient sum q G
-        if (p.normalize && p.softmax)
+        if (p.normalize && softmax)
             top = choice_top<LPT, NJ>(v);
         float chosen = 0.0f, qg = 0.0f;
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
-            v[s] = p.softmax ? __expf(v[s] - top) : sigmoid(v[s]);
+            v[s] = softmax ? __expf(v[s] - top) : sigmoid(v[s]);
             chosen += v[s];
             qg = fmaf(v[s], G[s], qg);
         }
         chosen = group_all<LPT>(chosen, OpAddF());
         qg = group_all<LPT>(qg, OpAddF());
-        const float norm = p.normalize ? inverse_sum(chosen, p.softmax) : p.softmax ? inv : 1.0f;
+        const float norm = p.normalize ? inverse_sum(chosen, softmax) : softmax ? inv : 1.0f;
         const float mean = qg * norm;
         // what a choice adds: to dx (softmax), to ds (sigmoid)
 #pragma unroll
@@ -564,25 +567,29 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
             if (e[s] < 0)
                 continue;
             const float centred = p.normalize ? G[s] - mean : G[s];
-            const float d = p.softmax ? v[s] * norm * centred : centred * norm;
+            const float d = softmax ? v[s] * norm * centred : centred * norm;
             atomicAdd(&at[e[s] / EPL * kPitch + e[s] % EPL], d);
         }
         wave_sync();
         const bool routed = group_first<LPT>(any, lane) >= 0;
-        const float pull = pc + (p.softmax && !p.normalize ? mean : 0.0f);
+        const float pull = pc + (softmax && !p.normalize ? mean : 0.0f);
         if (live) {
-            float dx[EPL];
+            // a row without a choice has no gradient
 #pragma unroll
-            for (int i = 0; i < EPL; i++) {
-                const float a = (*(const f32x4*)(at + g * kPitch + (i & ~3)))[i & 3];
-                if (p.softmax)
-                    dx[i] = fmaf(x[i] * inv, c_at(i) - pull, a);
-                else
-                    dx[i] = fmaf(c_at(i) - pc, inv, a) * x[i] * (1.0f - x[i]);
-                if (!routed)
-                    dx[i] = 0.0f;
+            for (int i = 0; i < EPL; i += 4) {
+                const f32x4 a = *(const f32x4*)(at + g * kPitch + i), b = *(const f32x4*)(c + g * kPitch + i);
+#pragma unroll
+                for (int h = 0; h < 4; h++) {
+                    const float v = x[i + h];
+                    float d;
+                    if constexpr (softmax)
+                        d = fmaf(v * inv, b[h] - pull, a[h]);
+                    else
+                        d = fmaf(b[h] - pc, inv, a[h]) * v * (1.0f - v);
+                    x[i + h] = routed ? d : 0.0f;
+                }
             }
-            store_row<DT, EPL>((T*)p.dlogits + (int64_t)t * E, first, E, dx);
+            store_row<DT, EPL, KIND>((T*)p.dlogits + (int64_t)t * E, first, E, x);
         }
         wave_sync();
     }
@@ -672,8 +679,12 @@ static hipError_t route_bwd_dt(const RouteBwdArgs& p, hipStream_t s, LaunchInfo*
         int64_t blocks = (p.T + per - 1) / per;
         if (blocks > 2048)
             blocks = 2048;                           // eight to a CU, then more passes each
-        hipLaunchKernelGGL((route_bwd_kernel<DT, LPT.value, EPL.value, KIND.value>),
-                           dim3((unsigned)blocks), dim3(256), 0, s, p);
+        if (p.softmax)
+            hipLaunchKernelGGL((route_bwd_kernel<DT, LPT.value, EPL.value, KIND.value, GG_SOFTMAX>),
+                               dim3((unsigned)blocks), dim3(256), 0, s, p);
+        else
+            hipLaunchKernelGGL((route_bwd_kernel<DT, LPT.value, EPL.value, KIND.value, GG_SIGMOID>),
+                               dim3((unsigned)blocks), dim3(256), 0, s, p);
         if (info) {
             snprintf(info->kernel, sizeof info->kernel, "route_bwd_kernel<%s, %d lanes a token>",
                      dtype_name(DT), LPT.value);
