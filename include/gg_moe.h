@@ -525,8 +525,8 @@ size_t gg_route_workspace_size(int64_t tokens, int32_t num_experts);
  *             scale * s / (sum of the chosen s + 1e-20) (GG_SIGMOID)
  *   counts_e = tokens that chose e;  N = routed = tokens with a choice
  *   balance = num_experts * sum_e (counts_e / (top_k N)) (1/N) sum_t p_te,
- *             p the softmax, or s / (sum over all experts of s + 1e-20); a
- *             token whose logits are all -inf adds nothing; 0 if N is 0
+ *             over the N tokens, p the softmax, or s / (sum over all experts
+ *             of s + 1e-20); 0 if N is 0
  * A NaN or +inf logit makes NaN of what the formulas say it enters.
  * fp32 arithmetic; the loss is summed in an order that depends on the sizes
  * alone, so equal calls give equal bits.

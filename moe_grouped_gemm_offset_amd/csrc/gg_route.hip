@@ -250,13 +250,15 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
             }
             *(u32x4*)(group_keys + g * kPitch + c) = four;
         }
+        uint32_t most = group_all<LPT>(best, OpMaxU());
         float top = 0.0f, inv = 0.0f;
         if (stats || (softmax && !p.normalize)) {
             row_scores<LPT, EPL>(x, softmax, top, inv);
             if (stats) {
+                const float share = most > kNever ? inv : 0.0f;      // no choice: no part in the loss
 #pragma unroll
                 for (int i = 0; i < EPL; i++)
-                    psum[i] = fmaf(x[i], inv, psum[i]);
+                    psum[i] = fmaf(x[i], share, psum[i]);
             }
         }
         if constexpr (EPL < LPT)
@@ -271,7 +273,6 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
             const int n = __builtin_amdgcn_readfirstlane(min(LPT, k - s * LPT));
             for (int j = 0; j < n; j++) {
                 wave_sync();
-                const uint32_t most = group_all<LPT>(best, OpMaxU());
                 const int from = group_first<LPT>(best == most, lane);
                 uint32_t* mine = group_keys + from * kPitch + min(g, EPL);
                 uint32_t key = *mine;
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
                 best = g == from ? next : best;
                 id = g == j ? from * EPL + at : id;
                 kept = g == j ? most : kept;
+                most = group_all<LPT>(best, OpMaxU());
             }
             e[s] = live && kept > kNever ? id : -1;
             v[s] = -INFINITY;

@@ -70,6 +70,7 @@ def ref_route(logits, bias, k, softmax, normalize, scale, ids=None):
     counts = torch.zeros(E, dtype=torch.int64)
     counts.index_add_(0, at.flatten(), there.flatten().long())
     n = int(there[:, 0].sum()) if T else 0
+    p = torch.where(there[:, :1], p, torch.zeros_like(p))      # the loss is over the tokens with a choice
     loss = E / (k * max(n, 1) ** 2) * (counts.double() * p.sum(0)).sum()
     return dict(ids=ids, prob=scale * w, counts=counts, routed=n, balance=loss)
 
@@ -173,6 +174,24 @@ def test_route_bias_only_chooses():
         for normalize in (False, True):
             say("route bias", score, normalize)
             check_route(x, 3, bias, score, normalize, 1.0)
+
+
+@pytest.mark.gpu
+def test_route_bias_takes_every_choice():
+    """A token whose bias leaves it no choice takes no part in the loss, though
+    its logits are finite, nor has it a gradient."""
+    x = torch.randn(9, 20, generator=torch.Generator().manual_seed(2))
+    x[3:6, 15:] = -INF
+    bias = torch.zeros(20)
+    bias[:15] = -INF
+    for score in (B.GG_SOFTMAX, B.GG_SIGMOID):
+        say("route bias takes all", score)
+        check_route(x, 4, bias, score, False, 1.0)
+        o = run_route(x.cuda(), 4, bias.cuda(), score)
+        assert int(o["routed"]) == 6 and bool((o["ids"][3:6] == -1).all())
+        d = run_bwd(x.cuda(), o["ids"], o["counts"], o["routed"], torch.ones(9, 4).cuda(), score, False, 1.0,
+                    dbalance=torch.ones(1).cuda())
+        assert bool((d[3:6] == 0).all()) and bool((d[:3].abs().sum(1) > 0).all())
 
 
 @pytest.mark.gpu
