@@ -11,7 +11,11 @@
 // only reads, runs at 6.9 TB/s with 2048 blocks of non-temporal loads (5.2
 // without the hint and one load in flight); the scaling writes as much as it
 // reads and wants many short blocks -- pieces of 8192 elements 6.5 TB/s, of
-// 32768 5.8, of 4096 4.9 (64 tensors of 4096 x 2048 bf16).
+// 32768 5.8, of 4096 4.9 (64 tensors of 4096 x 2048 bf16: 156 and 332 us).
+// Walking the pieces backwards, or loads that stay in the cache, change
+// nothing at 64 MB to 1 GB: the scaling finds nothing of the norm's pass.  96
+// small tensors of mixed types (10 MB): 6, 3.5 and 8 us, the latency of the
+// search, the addresses and the values behind one another.
 #include "gg_internal.hpp"
 #include "gg_lane.hpp"
 

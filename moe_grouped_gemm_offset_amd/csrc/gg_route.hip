@@ -4,6 +4,18 @@
 // Both kernels give each token a group of LPT lanes, each lane EPL
 // consecutive experts, so that one pass over the logits holds a token's row
 // in registers.  Statistics, weights and gradients are in fp32.
+//
+// Measured at 65536 tokens x 256 experts, bf16, 8 choices (34 MB of logits):
+// - route_kernel 19.5 us and route_join_kernel 5 us.  Bound by the vector ALU:
+//   a wave spends some 450 vector instructions and 33 transcendental ones on
+//   four tokens, 43% of them in the 8 steps of the choice; 80% of its cycles
+//   issue one.  Occupancies of 4, 6 and 8 waves a SIMD give the same time.
+//   Twice the experts a lane (8 lanes x 32) halves what the reductions cost
+//   a token but leaves half the passes to hide latency: 21.8 us.
+// - route_bwd_kernel 18.6 us, 73 MB read and written once and half a million
+//   scattered 4-byte reads of dprob: latency of the chain ids -> rows -> dprob.
+//   8 lanes a token 26.9 us, 32 lanes 21.6.
+// A few tokens (5 x 256): 5 us, the launch and four dependent loads.
 #include <cfloat>
 #include <type_traits>
 
@@ -619,7 +631,8 @@ size_t route_workspace(int64_t T, int E) {
 }
 
 // Calls f with the kernels' parameters for E experts of a type: lanes a token,
-// experts a lane, how the rows load.
+// experts a lane (the fewest lanes that leave a lane 16 experts at most, 8 up
+// to 128 experts: see the measurements above), how the rows load.
 template <int DT, class F>
 static hipError_t by_experts(int E, F f) {
     constexpr int N = row_vector<DT, 8>();
