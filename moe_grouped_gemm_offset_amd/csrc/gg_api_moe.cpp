@@ -7,6 +7,7 @@
 #include <cmath>
 
 #include "gg_host.hpp"
+#include "gg_step.hpp"
 
 using namespace gg;
 

@@ -16,8 +16,8 @@
 // nothing at 64 MB to 1 GB: the scaling finds nothing of the norm's pass.  96
 // small tensors of mixed types (10 MB): 6, 3.5 and 8 us, the latency of the
 // search, the addresses and the values behind one another.
-#include "gg_internal.hpp"
 #include "gg_lane.hpp"
+#include "gg_step.hpp"
 
 namespace gg {
 

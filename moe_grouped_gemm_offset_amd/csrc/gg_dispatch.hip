@@ -3,8 +3,8 @@
 // of a token's rows and that sum's gradients.
 #include <type_traits>
 
-#include "gg_internal.hpp"
 #include "gg_lane.hpp"
+#include "gg_step.hpp"
 
 namespace gg {
 

@@ -19,8 +19,8 @@
 #include <cfloat>
 #include <type_traits>
 
-#include "gg_internal.hpp"
 #include "gg_lane.hpp"
+#include "gg_step.hpp"
 
 namespace gg {
 
