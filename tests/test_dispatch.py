@@ -236,6 +236,38 @@ def test_combine(dtype, weighted):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.uint8])
+def test_widths_around_a_vector(dtype):
+    """Widths just below and past whole 16-byte vectors, waves and blocks, at
+    odd starts: permute writes its rows and nothing else, and combine of one
+    choice without weights is a copy back, bit for bit."""
+    n = 16 // torch.empty(0, dtype=dtype).element_size()
+    for H in (1, n - 1, n, n + 1, 2 * n - 1, 2 * n + 1, 64 * n - 1, 64 * n + 1, 256 * n + 1, 513 * n - 1):
+        say("widths", H, dtype)
+        T, E = 37, 5
+        counts, ends, row_of, m, g = rows_case(T, 1, E, H, dtype, 8, H)
+        x = torch.randint(1, 100, (T, H + 3), generator=g).to(dtype)[:, 1:1 + H]
+        out = torch.full((m + 1, H), 7, dtype=dtype, device="cuda")
+        wide = torch.empty(T, H + 3, dtype=dtype, device="cuda")
+        wide[:, 1:1 + H] = x.cuda()
+        B.gg_permute(wide[:, 1:1 + H], row_of.cuda(), counts.cuda(), ends.cuda(), out[:m])
+        torch.cuda.synchronize()
+        want = torch.full((m + 1, H), 7, dtype=dtype)
+        want[: int(ends[-1])] = 0
+        ok = row_of[:, 0] >= 0
+        want[row_of[ok, 0].long()] = x[ok]
+        assert torch.equal(out.cpu(), want)
+        if dtype == torch.uint8:
+            continue
+        back = torch.full((T, H + 3), 9, dtype=dtype, device="cuda")
+        B.gg_combine(out[:m], row_of.cuda(), back[:, 1:1 + H])
+        torch.cuda.synchronize()
+        want = torch.full((T, H + 3), 9, dtype=dtype)
+        want[:, 1:1 + H] = torch.where(ok[:, None], x, torch.zeros_like(x))
+        assert torch.equal(back.cpu(), want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", FLOATS)
 def test_combine_bwd(dtype):
     for i, (T, k, E, H, granule) in enumerate(CASES):
