@@ -367,8 +367,11 @@ def _extent(t, what):
 
 
 def _raw_stream(stream, dev):
-    """The hipStream_t of a call's stream argument (None: the current stream of
-    the arguments' device)."""
+    """The hipStream_t of a call's stream argument (None: the current stream).
+    The arguments' device has to be the current one, where the library
+    launches."""
+    if dev >= 0 and torch._C._cuda_getDevice() != dev:
+        raise GGError(9, f"the arguments are on device {dev}, which is not the current one")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
     return stream if isinstance(stream, int) else stream.cuda_stream

@@ -453,3 +453,13 @@ def test_binding_rejects():
                                    prob_rows=torch.zeros(15), workspace=ws)):
         with pytest.raises(B.GGError):
             call()
+
+
+def test_binding_rejects_another_device(monkeypatch):
+    """The library launches on the current device; a call whose arguments are
+    on another one is refused before anything is launched there."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    with pytest.raises(B.GGError) as e:
+        B._raw_stream(None, 1)
+    assert e.value.status == 9
+    assert B._raw_stream(1234, 0) == 1234 and B._raw_stream(None, -1) is None
