@@ -514,10 +514,10 @@ size_t gg_route_workspace_size(int64_t tokens, int32_t num_experts);
  * loss.  Per token t, with x its logits:
  *   key_e   = x_e + bias_e                     (one fp32 addition)
  *   ids     = the top_k experts of the largest keys, largest first, ties to
- *             the lower index.  -0 and +0 are equal; a NaN is above +inf, or
- *             with its sign set below -inf.  A logit or key of -inf or below
- *             is never chosen: where fewer than top_k are above it, the rest
- *             of ids is -1 and of prob 0.
+ *             the lower index.  -0 and +0 are equal; a NaN of either sign is
+ *             above +inf.  A logit, bias or key of -inf is never chosen:
+ *             where fewer than top_k experts are left, the rest of ids is -1
+ *             and of prob 0.
  *   scores  = softmax(x) over all experts (GG_SOFTMAX) or sigmoid(x)
  *             (GG_SIGMOID), without the bias
  *   prob    = scale * score of the chosen; with GG_FLAG_NORMALIZE

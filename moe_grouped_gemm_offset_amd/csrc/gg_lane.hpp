@@ -165,7 +165,8 @@ struct OpMaxU {
     __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
 struct OpMaxF {
-    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+    // (NaN if either is; fmaxf would first quiet both, an instruction each)
+    __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
 };
 struct OpAddF {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }

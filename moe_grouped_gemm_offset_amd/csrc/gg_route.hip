@@ -6,13 +6,13 @@
 // in registers.  Statistics, weights and gradients are in fp32.
 //
 // Measured at 65536 tokens x 256 experts, bf16, 8 choices (34 MB of logits):
-// - route_kernel 19.5 us and route_join_kernel 5 us.  Bound by the vector ALU:
+// - route_kernel 19.7 us and route_join_kernel 5 us.  Bound by the vector ALU:
 //   a wave spends some 450 vector instructions and 33 transcendental ones on
 //   four tokens, 43% of them in the 8 steps of the choice; 80% of its cycles
 //   issue one.  Occupancies of 4, 6 and 8 waves a SIMD give the same time.
 //   Twice the experts a lane (8 lanes x 32) halves what the reductions cost
 //   a token but leaves half the passes to hide latency: 21.8 us.
-// - route_bwd_kernel 18.6 us, 73 MB read and written once and half a million
+// - route_bwd_kernel 18.5 us, 73 MB read and written once and half a million
 //   scattered 4-byte reads of dprob: latency of the chain ids -> rows -> dprob.
 //   8 lanes a token 26.9 us, 32 lanes 21.6.
 // A few tokens (5 x 256): 5 us, the launch and four dependent loads.
@@ -37,13 +37,19 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 
 // Order of the choice as unsigned integers: fp32 order with -0 = +0 (bias is
-// never -0), a NaN above +inf, or below -inf if its sign is set.  kNever and
-// below, a logit or key of -inf, is never chosen; 0: taken.
+// never -0).  kNever, a key of -inf, is never chosen; 0: taken.  ODD: the wave
+// has a logit that is +inf or NaN.  An invalid operation of this hardware gives
+// a NaN whose sign is set, which the plain order has below -inf.
 constexpr uint32_t kNever = 0x007FFFFFu;             // the key of -inf
 
+template <bool ODD>
 __device__ __forceinline__ uint32_t order_key(float logit, float bias) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, logit + bias);
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    const float sum = logit + bias;
+    const uint32_t u = __builtin_bit_cast(uint32_t, sum);
+    const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    if (ODD && sum != sum)
+        return bias == -INFINITY ? kNever : 0xFFFFFFFFu;
+    return key;
 }
 
 // Words of LDS from a lane's first element to the next lane's, where a group
@@ -123,6 +129,16 @@ __device__ __forceinline__ void store_row(typename Elem<DT>::T* row, int first, 
     }
 }
 
+// Largest of a lane's values, NaN if one is.
+template <int EPL>
+__device__ __forceinline__ float lane_top(const float (&x)[EPL]) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < EPL; i++)
+        m = __builtin_elementwise_maximum(m, x[i]);
+    return m;
+}
+
 // 1 / a sum of scores.
 __device__ __forceinline__ float inverse_sum(float sum, bool softmax) {
     return softmax ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f / (sum + kTiny);
@@ -130,15 +146,12 @@ __device__ __forceinline__ float inverse_sum(float sum, bool softmax) {
 
 // A token's softmax or sigmoid over its row: x becomes the scores, `inv` what
 // turns them into the balance probabilities (softmax: x are exp(x - top), so
-// that p = x inv is the softmax as well; a row of -inf gives all zeros).
+// that p = x inv is the softmax as well; a row of -inf gives all zeros, one
+// with a NaN all NaN).  m is the lane's lane_top.
 template <int LPT, int EPL>
-__device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float& top, float& inv) {
+__device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float m, float& top, float& inv) {
     float sum = 0.0f;
     if (softmax) {
-        float m = x[0];
-#pragma unroll
-        for (int i = 1; i < EPL; i++)
-            m = fmaxf(m, x[i]);
         m = group_all<LPT>(m, OpMaxF());
         top = m == -INFINITY ? 0.0f : m;
 #pragma unroll
@@ -160,14 +173,10 @@ __device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float&
     }
 }
 
-// Largest of the chosen logits (0 if there is none).
+// Largest of the chosen logits (0 if there is none, NaN if one is).
 template <int LPT, int NJ>
 __device__ __forceinline__ float choice_top(const float (&v)[NJ]) {
-    float m = v[0];
-#pragma unroll
-    for (int s = 1; s < NJ; s++)
-        m = fmaxf(m, v[s]);
-    m = group_all<LPT>(m, OpMaxF());
+    const float m = group_all<LPT>(lane_top(v), OpMaxF());
     return m == -INFINITY ? 0.0f : m;
 }
 
@@ -251,21 +260,30 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         float x[EPL];
         load_row<DT, EPL, KIND>(row, first, E, live, x);
         uint32_t best = 0;
+        auto make_keys = [&](auto odd) {
 #pragma unroll
-        for (int c = 0; c < EPL; c += 4) {
-            u32x4 four;
-            const f32x4 b = *(const f32x4*)(bias + g * kPitch + c);
+            for (int c = 0; c < EPL; c += 4) {
+                u32x4 four;
+                const f32x4 b = *(const f32x4*)(bias + g * kPitch + c);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                four[i] = order_key(x[c + i], b[i]);
-                best = best > four[i] ? best : four[i];
+                for (int i = 0; i < 4; i++) {
+                    four[i] = order_key<odd.value>(x[c + i], b[i]);
+                    best = best > four[i] ? best : four[i];
+                }
+                *(u32x4*)(group_keys + g * kPitch + c) = four;
             }
-            *(u32x4*)(group_keys + g * kPitch + c) = four;
-        }
+        };
+        // (the wave's choice of the two: 1% of this case; as one instruction
+        // more in every key 2%)
+        const float m = lane_top(x);
+        if (__ballot(!(m < INFINITY)))
+            make_keys(std::true_type());
+        else
+            make_keys(std::false_type());
         uint32_t most = group_all<LPT>(best, OpMaxU());
         float top = 0.0f, inv = 0.0f;
         if (stats || (softmax && !p.normalize)) {
-            row_scores<LPT, EPL>(x, softmax, top, inv);
+            row_scores<LPT, EPL>(x, softmax, m, top, inv);
             if (stats) {
                 const float share = most > kNever ? inv : 0.0f;      // no choice: no part in the loss
 #pragma unroll
@@ -550,7 +568,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         wave_sync();
 
         float top = 0.0f, inv = 0.0f;
-        row_scores<LPT, EPL>(x, softmax, top, inv);
+        row_scores<LPT, EPL>(x, softmax, softmax ? lane_top(x) : 0.0f, top, inv);
         float pc = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; i += 4) {

@@ -195,6 +195,47 @@ def test_route_bias_takes_every_choice():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_route_nan_with_its_sign_set(dtype):
+    """A NaN is chosen first whatever its sign (an invalid operation gives
+    either, by the machine), also beside a bias and in a row of -inf."""
+    size = torch.empty(0, dtype=dtype).element_size()
+    x = torch.randn(6, 61, generator=torch.Generator().manual_seed(4)).to(dtype)
+    x[2:4] = -INF
+    bits = {torch.bfloat16: -0x40, torch.float16: -0x200, torch.float32: -0x400000}[dtype]    # 0xFFC0, 0xFE00
+    raw = x.view(torch.int16 if size == 2 else torch.int32)
+    raw[1, 60] = raw[2, 7] = raw[2, 30] = raw[4, 0] = bits
+    assert bool(torch.isnan(x[1, 60])) and int(raw[1, 60]) < 0
+    for bias in (None, torch.randn(61, generator=torch.Generator().manual_seed(5))):
+        o = run_route(x.cuda(), 4, bias=None if bias is None else bias.cuda())
+        r = ref_route(x.double(), bias, 4, True, False, 1.0)
+        assert torch.equal(o["ids"].cpu().long(), r["ids"])
+        assert int(o["ids"][1, 0]) == 60 and o["ids"][2].tolist() == [7, 30, -1, -1]
+        assert int(o["routed"]) == r["routed"] == 5
+        assert torch.equal(o["counts"].cpu().long(), r["counts"])
+        nan = torch.isnan(o["prob"].cpu())
+        assert torch.equal(nan, torch.isnan(r["prob"]))
+        assert bool(nan[1].all()) and bool(nan[2, :2].all()) and not bool(nan[[0, 3, 5]].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_route_bias_of_minus_infinity(dtype):
+    """An expert whose bias is -inf is never chosen, whatever its logit."""
+    bias = torch.zeros(61)
+    bias[33] = -INF
+    y = torch.randn(4, 61, generator=torch.Generator().manual_seed(6)).to(dtype)
+    y[1, 33], y[2, 33], y[3, 33] = INF, float("nan"), -INF
+    y[2, 5] = INF
+    o = run_route(y.cuda(), 3, bias=bias.cuda())
+    masked = y.clone()
+    masked[:, 33] = -INF
+    r = ref_route(masked.double(), None, 3, True, False, 1.0)
+    assert torch.equal(o["ids"].cpu().long(), r["ids"]) and int(o["ids"][2, 0]) == 5
+    assert torch.equal(o["counts"].cpu().long(), r["counts"]) and int(o["routed"]) == 4
+
+
+@pytest.mark.gpu
 def test_route_nan_and_inf():
     """NaN and +inf logits: valid, distinct ids (NaN above +inf), NaN where
     the formulas give it, other tokens untouched."""
