@@ -359,6 +359,27 @@ def _need_rows(t, what, dtypes):
     return t.data_ptr(), n, width, pitch if n > 1 else width, t.get_device()
 
 
+def _scratch(ws, size, stream, dev, *of):
+    """(address, bytes, tensor) of a call's workspace: the caller's, or a new
+    one of size(*of) bytes."""
+    if ws is None:
+        if dev < 0:
+            raise GGError(9, "the arguments are not on a GPU")
+        with torch.cuda.stream(_torch_stream(stream)):
+            ws = torch.empty(size(*of), dtype=torch.uint8, device=dev)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(ws, "workspace", ws.shape, ws.dtype, dev, False)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _first(t):
+    return t.shape[0] if t.dim() else 0
+
+
+def _last(t):
+    return t.shape[-1] if t.dim() else 0
+
+
 def _extent(t, what):
     """The length of a one-dimensional tensor argument."""
     if t.dim() != 1:
@@ -370,10 +391,12 @@ def _raw_stream(stream, dev):
     """The hipStream_t of a call's stream argument (None: the current stream).
     The arguments' device has to be the current one, where the library
     launches."""
-    if dev >= 0 and torch._C._cuda_getDevice() != dev:
+    if dev < 0:
+        raise GGError(9, "the arguments are not on a GPU")
+    if torch._C._cuda_getDevice() != dev:
         raise GGError(9, f"the arguments are on device {dev}, which is not the current one")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -405,17 +428,16 @@ def gg_route(logits, ids, prob, counts, routed, balance=None, bias=None, score=G
     and balance float32 (1,) are written.  Returns the workspace used."""
     L = load_library()
     px, T, E, ld, dev = _need_rows(logits, "logits", _FLOATS)
-    k = ids.shape[-1]
+    k = _last(ids)
     p_ids = _need(ids, "ids", (T, k), _I32, dev)
     p_prob = _need(prob, "prob", (T, k), _F32, dev)
     p_counts = _need(counts, "counts", (E,), _I32, dev)
     p_routed = _need(routed, "routed", (1,), _I32, dev)
     p_bal = None if balance is None else _need(balance, "balance", (1,), _F32, dev)
     p_bias = None if bias is None else _need(bias, "bias", (E,), _F32, dev)
-    ws, nbytes = _workspace(workspace, L.gg_route_workspace_size(T, E) if workspace is None else 0,
-                            logits, stream)
+    p_ws, nbytes, ws = _scratch(workspace, L.gg_route_workspace_size, stream, dev, T, E)
     _check(L.gg_route(px, _TORCH_DTYPE[logits.dtype], ld, T, E, p_bias, k, score, scale, flags, p_ids,
-                      p_prob, p_counts, p_routed, p_bal, ws.data_ptr(), nbytes, _raw_stream(stream, dev)))
+                      p_prob, p_counts, p_routed, p_bal, p_ws, nbytes, _raw_stream(stream, dev)))
     return ws
 
 
@@ -426,7 +448,7 @@ def gg_route_bwd(logits, ids, counts, routed, dprob, dlogits, row_of=None, dbala
     (m_rows,), as gg_dglu and gg_dsrelu write it."""
     L = load_library()
     px, T, E, ld, dev = _need_rows(logits, "logits", _FLOATS)
-    k = ids.shape[-1]
+    k = _last(ids)
     p_ids = _need(ids, "ids", (T, k), _I32, dev)
     p_counts = _need(counts, "counts", (E,), _I32, dev)
     p_routed = _need(routed, "routed", (1,), _I32, dev)
@@ -458,10 +480,9 @@ def gg_plan(ids, counts, padded_offsets, row_of, m_rows, granule=256, prob=None,
     p_row = _need(row_of, "row_of", shape, _I32, dev)
     p_prob = None if prob is None else _need(prob, "prob", shape, _F32, dev)
     p_rows = None if prob_rows is None else _need(prob_rows, "prob_rows", (m_rows,), _F32, dev)
-    ws, nbytes = _workspace(workspace, L.gg_plan_workspace_size(T, E) if workspace is None else 0,
-                            ids, stream)
+    p_ws, nbytes, ws = _scratch(workspace, L.gg_plan_workspace_size, stream, dev, T, E)
     _check(L.gg_plan(p_ids, T, k, E, granule, m_rows, p_prob, p_counts, p_ends, p_row, p_rows,
-                     ws.data_ptr(), nbytes, _raw_stream(stream, dev)))
+                     p_ws, nbytes, _raw_stream(stream, dev)))
     return ws
 
 
@@ -471,7 +492,7 @@ def gg_permute(x, row_of, counts, padded_offsets, x_rows, stream=None):
     four-byte types."""
     L = load_library()
     px, T, width, ld, dev = _need_rows(x, "x", _FLOATS + _BYTES)
-    k, E, m = row_of.shape[-1], _extent(counts, "counts"), x_rows.shape[0]
+    k, E, m = _last(row_of), _extent(counts, "counts"), _first(x_rows)
     p_row = _need(row_of, "row_of", (T, k), _I32, dev)
     p_counts = _need(counts, "counts", (E,), _I32, dev)
     p_ends = _need(padded_offsets, "padded_offsets", (E,), _I32, dev)
@@ -485,7 +506,7 @@ def gg_combine(y_rows, row_of, out, weights=None, stream=None):
     gg_moe.h); weights None: 1.  out (T, width) at any row pitch."""
     L = load_library()
     p_out, T, width, ld, dev = _need_rows(out, "out", _FLOATS)
-    k, m = row_of.shape[-1], y_rows.shape[0]
+    k, m = _last(row_of), _first(y_rows)
     p_y = _need(y_rows, "y_rows", (m, width), out.dtype, dev)
     p_row = _need(row_of, "row_of", (T, k), _I32, dev)
     p_w = None if weights is None else _need(weights, "weights", (T, k), _F32, dev)
@@ -499,7 +520,7 @@ def gg_combine_bwd(dout, y_rows, row_of, weights, counts, padded_offsets, dy_row
     (m_rows, width), zeros in the padding, and dweights float32 (T, top_k)."""
     L = load_library()
     p_d, T, width, ld, dev = _need_rows(dout, "dout", _FLOATS)
-    k, E, m = row_of.shape[-1], _extent(counts, "counts"), y_rows.shape[0]
+    k, E, m = _last(row_of), _extent(counts, "counts"), _first(y_rows)
     p_y = _need(y_rows, "y_rows", (m, width), dout.dtype, dev)
     p_row = _need(row_of, "row_of", (T, k), _I32, dev)
     p_w = _need(weights, "weights", (T, k), _F32, dev)
@@ -544,9 +565,9 @@ def gg_grad_norm(ptrs, ends, dtypes, total, sumsq, accumulate=False, workspace=N
     Returns the workspace used."""
     L = load_library()
     p_ptrs, p_ends, p_dt, n, p_sum, dev = _need_table(ptrs, ends, dtypes, sumsq)
-    ws, nbytes = _workspace(workspace, L.gg_grad_workspace_size() if workspace is None else 0, ptrs, stream)
-    _check(L.gg_grad_norm(p_ptrs, p_ends, p_dt, n, total, p_sum, int(bool(accumulate)), ws.data_ptr(),
-                          nbytes, _raw_stream(stream, dev)))
+    p_ws, nbytes, ws = _scratch(workspace, L.gg_grad_workspace_size, stream, dev)
+    _check(L.gg_grad_norm(p_ptrs, p_ends, p_dt, n, total, p_sum, int(bool(accumulate)), p_ws, nbytes,
+                          _raw_stream(stream, dev)))
     return ws
 
 

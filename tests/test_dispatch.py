@@ -462,4 +462,56 @@ def test_binding_rejects_another_device(monkeypatch):
     with pytest.raises(B.GGError) as e:
         B._raw_stream(None, 1)
     assert e.value.status == 9
-    assert B._raw_stream(1234, 0) == 1234 and B._raw_stream(None, -1) is None
+    assert B._raw_stream(1234, 0) == 1234
+
+
+def host_calls(dev="cpu", ws="cpu"):
+    """Every call around the GEMMs with well-formed arguments on a device."""
+    f, i32, u8 = torch.zeros, torch.int32, torch.uint8
+    kw = dict(device=dev)
+    x, x_rows = f(4, 8, **kw), f(16, 8, **kw)
+    ids, p = f(4, 2, dtype=i32, **kw), f(4, 2, **kw)
+    c, one, fone = f(3, dtype=i32, **kw), f(1, dtype=i32, **kw), f(1, **kw)
+    logits, d = f(4, 3, **kw), f(4, 3, **kw)
+    tab = f(2, dtype=torch.int64, **kw), f(2, dtype=torch.int64, **kw), f(2, dtype=i32, **kw), 0
+    s = f(1, dtype=torch.float64, **kw)
+    w = None if ws is None else f(1 << 16, dtype=u8, device=ws)
+    return dict(
+        route=lambda: B.gg_route(logits, ids, p, c, one, fone, workspace=w),
+        route_bwd=lambda: B.gg_route_bwd(logits, ids, c, one, p, d),
+        plan=lambda: B.gg_plan(ids, c, c.clone(), ids.clone(), 16, workspace=w),
+        permute=lambda: B.gg_permute(x, ids, c, c, x_rows),
+        combine=lambda: B.gg_combine(x_rows, ids, x),
+        combine_bwd=lambda: B.gg_combine_bwd(x, x_rows, ids, p, c, c, x_rows.clone(), p.clone()),
+        grad_norm=lambda: B.gg_grad_norm(*tab, s, workspace=w),
+        grad_clip=lambda: B.gg_grad_clip(*tab, s, 1.0, f(2, **kw)))
+
+
+@pytest.mark.parametrize("ws", ["cpu", None])
+@pytest.mark.parametrize("call", list(host_calls()))
+def test_binding_rejects_host_tensors(call, ws):
+    """Kernels cannot read them: refused by the binding, with or without a GPU."""
+    with pytest.raises(B.GGError) as e:
+        host_calls(ws=ws)[call]()
+    assert e.value.status == 9
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["route", "plan", "grad_norm"])
+def test_binding_rejects_a_host_workspace(call):
+    with pytest.raises(B.GGError) as e:
+        host_calls(dev="cuda", ws="cpu")[call]()
+    assert e.value.status == 9
+
+
+def test_binding_rejects_scalars():
+    z = torch.zeros((), dtype=torch.int32)
+    x, ids, p, c = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), torch.zeros(8).int()
+    for call in (lambda: B.gg_route(x, z, p, c, c[:1]), lambda: B.gg_route_bwd(x, z, c, c[:1], p, x),
+                 lambda: B.gg_plan(z, c, c, ids, 16), lambda: B.gg_permute(x, z, c, c, x),
+                 lambda: B.gg_permute(x, ids, c, c, z.float()), lambda: B.gg_permute(z.float(), ids, c, c, x),
+                 lambda: B.gg_combine(z.float(), ids, x), lambda: B.gg_combine(x, z, x),
+                 lambda: B.gg_combine_bwd(x, x, z, p, c, c, x, p), lambda: B.gg_grad_norm(z, z, z, 0, z)):
+        with pytest.raises(B.GGError) as e:
+            call()
+        assert e.value.status == 2
