@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         // (the wave's choice of the two: 1% of this case; as one instruction
         // more in every key 2%)
         const float m = lane_top(x);
-        if (__ballot(!(m < INFINITY)))
+        const bool odd = __ballot(!(m < INFINITY)) != 0;
+        if (odd)
             make_keys(std::true_type());
         else
             make_keys(std::false_type());
@@ -285,7 +286,13 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         if (stats || (softmax && !p.normalize)) {
             row_scores<LPT, EPL>(x, softmax, m, top, inv);
             if (stats) {
-                const float share = most > kNever ? inv : 0.0f;      // no choice: no part in the loss
+                // no choice: no part in the loss, though a bias of -inf may
+                // have taken out a NaN, which 0 times does not
+                const float share = most > kNever ? inv : 0.0f;
+                if (odd)
+#pragma unroll
+                    for (int i = 0; i < EPL; i++)
+                        x[i] = most > kNever ? x[i] : 0.0f;
 #pragma unroll
                 for (int i = 0; i < EPL; i++)
                     psum[i] = fmaf(x[i], share, psum[i]);

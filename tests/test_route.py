@@ -236,6 +236,30 @@ def test_route_bias_of_minus_infinity(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 3000])
+@pytest.mark.parametrize("score", [B.GG_SOFTMAX, B.GG_SIGMOID])
+def test_route_loss_leaves_out_tokens_without_a_choice(score, T):
+    """A token whose only logits above -inf are NaN or +inf, at an expert that a
+    bias of -inf takes out, has no choice: the loss is that of the others, and
+    0 where no token has one."""
+    x = make_logits(T, 20, torch.float32, 91)
+    bias = torch.zeros(20)
+    bias[7] = -INF
+    x[1:4] = -INF
+    x[1, 7], x[2, 7] = float("nan"), INF
+    y = x.clone()
+    y[1:4] = -INF
+    o = run_route(x.cuda(), 3, bias.cuda(), score)
+    r = ref_route(y.double(), bias, 3, score == B.GG_SOFTMAX, False, 1.0)
+    assert torch.equal(o["ids"].cpu().long(), r["ids"])
+    assert int(o["routed"]) == r["routed"] == T - 3
+    say("loss", float(o["balance"]), float(r["balance"]))
+    assert abs(float(o["balance"]) - float(r["balance"])) <= 128 * U * float(r["balance"])
+    o = run_route(x[1:4].cuda(), 3, bias.cuda(), score)
+    assert int(o["routed"]) == 0 and float(o["balance"]) == 0.0
+
+
+@pytest.mark.gpu
 def test_route_nan_and_inf():
     """NaN and +inf logits: valid, distinct ids (NaN above +inf), NaN where
     the formulas give it, other tokens untouched."""
