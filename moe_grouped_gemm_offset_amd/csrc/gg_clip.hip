@@ -139,7 +139,8 @@ __device__ __forceinline__ void scale_range(const void* base, void* out, int64_t
         [&](int64_t i) { o[i] = from_f32<DT>(to_f32<DT>(q[i]) * factor); });
 }
 
-// Workspace: header, then a double per block.
+// Workspace: header (int32 0: the error word, always 0), then a double per
+// block.
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(GradArgs p, int64_t piece) {
     __shared__ double tmp[kThreads / 64];
     double s = 0.0;
@@ -155,6 +156,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(GradArgs p, int64_t
         });
     const double all = block_sum<kThreads>(s, tmp);
     if (threadIdx.x == 0) {
+        if (blockIdx.x == 0)
+            p.ws[0] = 0;
         if (gridDim.x == 1)
             p.sumsq[0] = p.accumulate ? p.sumsq[0] + all : all;
         else

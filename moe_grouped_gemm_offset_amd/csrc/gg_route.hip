@@ -182,11 +182,12 @@ __device__ __forceinline__ float choice_top(const float (&v)[NJ]) {
 
 }  // namespace
 
-// Workspace: header (int32 1: the finishing ticket; 4 + 2q, 5 + 2q: quarter
-// q's routed tokens as a double), then the blocks' counts and probability
-// sums as pairs, 16 experts (a 128-byte line) of a block after another's:
-// [ceil(E / 16)][blocks][16], the blocks' routed tokens, and what the joining
-// blocks have made of a quarter of the blocks each, [4][E].
+// Workspace: header (int32 0: the error word, always 0; 1: the finishing
+// ticket; 4 + 2q, 5 + 2q: quarter q's routed tokens as a double), then the
+// blocks' counts and probability sums as pairs, 16 experts (a 128-byte line)
+// of a block after another's: [ceil(E / 16)][blocks][16], the blocks' routed
+// tokens, and what the joining blocks have made of a quarter of the blocks
+// each, [4][E].
 struct RoutePair {
     int32_t count;
     float sum;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
     if (tid == 0) {
         nrouted = 0;
         if (blockIdx.x == 0)
-            p.ws[1] = 0;
+            p.ws[0] = p.ws[1] = 0;
     }
     // +inf and NaN as the largest finite bias: a logit of -inf stays one
     for (int e = tid; e < kCap; e += kThreads) {

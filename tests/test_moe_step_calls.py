@@ -150,6 +150,29 @@ def test_workspaces_hold_nothing_between_calls():
             assert same(s.results(), w)
 
 
+@pytest.mark.parametrize("T", [3, 3000])
+def test_error_word_is_each_calls_own(T):
+    """gg_device_error after a call reads that call's word: 0 after the router
+    and the norm, which set none, on a workspace never written before, and on
+    one where gg_plan has left its flags."""
+    s = Step(T=T)
+    bad = s.ids.clone().fill_(9999)
+    for fill in (255, None):
+        ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        for call in (
+                lambda: B.gg_route(s.logits, s.ids, s.prob, s.counts, s.routed, s.balance, workspace=ws),
+                lambda: B.gg_grad_norm(*s.table, s.sumsq, workspace=ws),
+                lambda: B.gg_grad_norm(*B.grad_table([s.norm]), s.sumsq, workspace=ws),
+                lambda: B.gg_grad_norm(*B.grad_table([]), s.sumsq, workspace=ws)):
+            if fill is None:
+                B.gg_plan(bad, s.rows_e, s.ends, s.row_of, s.m, workspace=ws)
+                assert B.gg_device_error(ws) == B.GG_DEVERR_IDS
+            else:
+                ws.fill_(fill)
+            call()
+            assert B.gg_device_error(ws) == 0
+
+
 def test_rows_past_32_bits():
     """Expert rows past 2^32 bytes from the first, and past 2^31 elements."""
     H, T, k = 8192, 6, 2
