@@ -691,7 +691,8 @@ gg_status gg_grad_norm(const int64_t* ptrs, const int64_t* ends, const int32_t* 
 
 /*
  * norm   = sqrt(sumsq)
- * factor = min(1, max_norm / (norm + eps))    (NaN if norm is NaN)
+ * factor = min(1, max_norm / (norm + eps))    (1 if max_norm >= norm + eps,
+ *          whatever the quotient; NaN if norm is NaN, and only then)
  * every element g becomes g * factor (one fp32 product, rounded once to its
  * type).
  *

@@ -182,9 +182,11 @@ __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(GradArgs p, in
 
 __global__ void __launch_bounds__(kThreads) grad_clip_kernel(GradArgs p, int64_t piece) {
     const double norm = sqrt(p.sumsq[0]);
-    // min(1, max_norm / (norm + eps)), a NaN kept
-    const float ratio = (float)((double)p.max_norm / (norm + (double)p.eps));
-    const float factor = ratio >= 1.0f ? 1.0f : ratio;
+    // 1 where the limit is not passed (0 / 0 and infinity / infinity among
+    // it), else max_norm / (norm + eps); a NaN is kept
+    const double with_eps = norm + (double)p.eps;
+    const float ratio = (float)((double)p.max_norm / with_eps);
+    const float factor = (double)p.max_norm >= with_eps || ratio >= 1.0f ? 1.0f : ratio;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.norm[0] = (float)norm;
         p.norm[1] = factor;

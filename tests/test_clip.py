@@ -151,6 +151,30 @@ def test_norm_repeats_bit_for_bit():
         assert a[0] == b[0] and torch.equal(a[1], b[1])
 
 
+@pytest.mark.gpu
+def test_clip_where_the_quotient_is_undefined():
+    """A limit that the norm does not pass leaves every bit: 0 / 0 (no norm, no
+    limit, no eps) and infinity / infinity (no limit asked for) as well.  Only a
+    norm that is NaN gives a factor that is NaN."""
+    for in_place in (True, False):
+        z = [torch.zeros(900, device="cuda"), torch.zeros(5, device="cuda").bfloat16()]
+        outs = None if in_place else [torch.full_like(t, 7.0) for t in z]
+        _, norm = run(z, 0.0, eps=0.0, outs=outs)
+        assert norm.tolist() == [0.0, 1.0]
+        assert all(bool((t == 0).all()) for t in (z if in_place else outs))
+        t = make([50, 40], 9)
+        t[0][7] = float("inf")
+        keep = [x.clone() for x in t]
+        outs = None if in_place else [torch.zeros_like(x) for x in t]
+        _, norm = run(t, float("inf"), outs=outs)
+        assert norm.tolist() == [float("inf"), 1.0]
+        for a, b in zip(keep, t if in_place else outs):
+            assert torch.equal(a, b)
+        t[1][3] = float("nan")
+        _, norm = run(t, float("inf"), outs=outs)
+        assert bool(torch.isnan(norm).all())
+
+
 # --------------------------------------------------------------------------
 # refusals, on the host (no GPU)
 # --------------------------------------------------------------------------
