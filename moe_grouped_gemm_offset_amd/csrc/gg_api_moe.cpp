@@ -21,6 +21,9 @@ constexpr int32_t kMaxWidth = 1 << 20;
 
 size_t size_of(gg_dtype d) { return d == GG_F32 ? 4 : d == GG_BF16 || d == GG_F16 ? 2 : 1; }
 
+// Rows that a plan's groups are padded to.
+bool is_granule(int32_t g) { return g >= 1 && g <= 256 && (g & (g - 1)) == 0; }
+
 bool off(const void* p, size_t align) { return ((uintptr_t)p & (align - 1)) != 0; }
 
 gg_status check_tokens(int64_t tokens, int32_t num_experts, int32_t top_k) {
@@ -200,7 +203,7 @@ size_t gg_plan_workspace_size(int64_t tokens, int32_t num_experts) {
 
 int64_t gg_plan_max_rows(int64_t tokens, int32_t top_k, int32_t num_experts, int32_t granule) {
     if (tokens < 0 || tokens > kMaxTokens || top_k < 1 || top_k > kMaxTopK || num_experts < 1 ||
-        num_experts > 1024 || granule < 1 || granule > 256)
+        num_experts > 1024 || !is_granule(granule))
         return 0;
     const int64_t n = tokens * top_k, e = n < num_experts ? n : num_experts;
     return (n + (granule - 1) * e) / granule * granule;
@@ -213,7 +216,7 @@ gg_status gg_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t num
     gg_status st = check_tokens(tokens, num_experts, top_k);
     if (st != GG_OK)
         return st;
-    if (granule < 1 || granule > 256 || (granule & (granule - 1)))
+    if (!is_granule(granule))
         return fail(GG_ERR_SHAPE, "granule must be a power of two in 1..256 (got %d)", granule);
     if (m_rows < 0 || m_rows > INT32_MAX)
         return fail(GG_ERR_SHAPE, "m_rows must be in 0..2^31-1");

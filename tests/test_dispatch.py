@@ -389,6 +389,13 @@ def test_plan_rejects(kw, status):
     assert B.gg_last_error() != ""
 
 
+def test_plan_max_rows_out_of_range():
+    """0 for a granule that gg_plan refuses."""
+    for g in (0, 3, 6, 100, 255, 257, 512):
+        assert c_plan(g=g) == SHAPE
+        assert max_rows(10, 2, 4, g) == 0
+
+
 def c_permute(**kw):
     a = dict(x=P, dt=0, ld=64, T=16, H=64, row_of=P, k=4, counts=P, ends=P, E=8, m=512, out=P)
     a.update(kw)
