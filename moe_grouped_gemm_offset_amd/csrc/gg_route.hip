@@ -36,6 +36,21 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
 }
 
+// sigmoid(-|x|), at most 1/2, with x's sign.  A sigmoid and its slope come out
+// of it without 1 minus what rounds to 1: sigmoid(x) is the tail t or 1 - t,
+// the slope t (1 - t).  (From the sigmoid itself the slope is off by 6% at x =
+// 16 and 0 from 17 on.)
+__device__ __forceinline__ float signed_tail(float x) {
+    const float e = __expf(-fabsf(x));
+    return __builtin_copysignf(e * __builtin_amdgcn_rcpf(1.0f + e), x);
+}
+__device__ __forceinline__ float tail_sigmoid(float t) {
+    return __builtin_signbitf(t) ? -t : 1.0f - t;
+}
+__device__ __forceinline__ float tail_slope(float t) {
+    return fmaf(-t, t, fabsf(t));
+}
+
 // Order of the choice as unsigned integers: fp32 order with -0 = +0 (bias is
 // never -0).  kNever, a key of -inf, is never chosen; 0: taken.  ODD: the wave
 // has a logit that is +inf or NaN.  An invalid operation of this hardware gives
@@ -576,14 +591,24 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         wave_sync();
 
         float top = 0.0f, inv = 0.0f;
-        row_scores<LPT, EPL>(x, softmax, softmax ? lane_top(x) : 0.0f, top, inv);
+        if constexpr (softmax) {
+            row_scores<LPT, EPL>(x, true, lane_top(x), top, inv);
+        } else {                                     // x become the tails
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                x[i] = signed_tail(x[i]);
+                sum += tail_sigmoid(x[i]);
+            }
+            inv = inverse_sum(group_all<LPT>(sum, OpAddF()), false);
+        }
         float pc = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; i += 4) {
             const f32x4 four = *(const f32x4*)(c + g * kPitch + i);
 #pragma unroll
             for (int h = 0; h < 4; h++)
-                pc = fmaf(x[i + h], four[h], pc);
+                pc = fmaf(softmax ? x[i + h] : tail_sigmoid(x[i + h]), four[h], pc);
         }
         pc = group_all<LPT>(pc, OpAddF()) * inv;
 
@@ -593,7 +618,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         float chosen = 0.0f, qg = 0.0f;
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
-            v[s] = softmax ? __expf(v[s] - top) : sigmoid(v[s]);
+            v[s] = softmax ? __expf(v[s] - top) : tail_sigmoid(signed_tail(v[s]));
             chosen += v[s];
             qg = fmaf(v[s], G[s], qg);
         }
@@ -625,7 +650,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
                     if constexpr (softmax)
                         d = fmaf(v * inv, b[h] - pull, a[h]);
                     else
-                        d = fmaf(b[h] - pc, inv, a[h]) * v * (1.0f - v);
+                        d = fmaf(b[h] - pc, inv, a[h]) * tail_slope(v);
                     x[i + h] = routed ? d : 0.0f;
                 }
             }

@@ -427,6 +427,86 @@ def test_route_bwd_without_balance_and_extremes():
             assert float((d.cpu().double() - want).abs().max()) <= 512 * U * 2
 
 
+def ref_bwd_terms(x, ids, softmax, normalize, scale, g, db):
+    """(gradient, the magnitudes of the terms it is the sum of) by the formulas,
+    in 64 bits and without cancellation in a sigmoid's slope.  Rows with a
+    choice, logits without NaN or +inf."""
+    T, E = x.shape
+    k = ids.shape[1]
+    x = x.double()
+    there, at = ids >= 0, ids.clamp_min(0)
+    any_ = there[:, :1]
+    n = max(int(there[:, 0].sum()), 1)
+    counts = torch.bincount(at[there], minlength=E).double()
+    G = torch.where(there, scale * g.double(), torch.zeros(1).double())
+    a, p = ref_scores(x, softmax)
+    c = (db * E / (k * n * n) * counts).expand(T, E)
+    pc = (p * c).sum(1, keepdim=True)
+
+    def place(v):
+        return torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, at, torch.where(there, v, torch.zeros_like(v)))
+
+    if softmax:
+        if normalize:
+            q = ref_scores(torch.where(there, x.gather(1, at), torch.full_like(x[:, :1], -INF)), True)[0]
+            d = place(q * (G - (q * G).sum(1, keepdim=True)))
+            size = place(q * (G.abs() + (q * G.abs()).sum(1, keepdim=True)))
+        else:
+            d, size = p * (place(G) - (p * place(G)).sum(1, keepdim=True)), \
+                p * (place(G.abs()) + (p * place(G.abs())).sum(1, keepdim=True))
+        d, size = d + p * (c - pc), size + p * (c + pc)
+    else:
+        e = torch.exp(-x.abs())
+        slope = e / (1 + e) ** 2
+        total = a.sum(1, keepdim=True) + TINY
+        d, size = (c - pc) / total, (c + pc) / total
+        if normalize:
+            s = torch.where(there, a.gather(1, at), torch.zeros_like(x[:, :1]))
+            chosen = s.sum(1, keepdim=True) + TINY
+            d = d + place((G - (s * G).sum(1, keepdim=True) / chosen) / chosen)
+            size = size + place((G.abs() + (s * G.abs()).sum(1, keepdim=True) / chosen) / chosen)
+        else:
+            d, size = d + place(G), size + place(G.abs())
+        d, size = d * slope, size * slope
+    zero = torch.zeros_like(d)
+    return torch.where(any_, d, zero), torch.where(any_, size, zero)
+
+
+def check_bwd_terms(x, k, score, normalize, g, db, scale=1.5):
+    """Every element within its own terms' error.  In fp32, with u = 2^-24: an
+    exponential 4 u, and |a| u of its argument a (softmax's x - top is rounded);
+    a row's sum of up to 1024 positive terms 24 u (16 in a row, 6 joins); the
+    quotient 2 u; a probability 30 u; the mean of c or G over them 60 u; the
+    difference and the factor in front 40 u: 130 u, and |a| u, of the terms."""
+    softmax = score == B.GG_SOFTMAX
+    f = ref_route(x.double(), None, k, softmax, normalize, scale)
+    dev = dict(device="cuda")
+    d = run_bwd(x.cuda(), f["ids"].to(torch.int32).cuda(), f["counts"].to(torch.int32).cuda(),
+                torch.tensor([f["routed"]], dtype=torch.int32, **dev), g.cuda(), score, normalize, scale, None,
+                torch.tensor([db], **dev))
+    want, size = ref_bwd_terms(x, f["ids"], softmax, normalize, scale, g, db)
+    arg = (x.double() - x.double().max(1, keepdim=True).values).abs() if softmax else torch.zeros(1).double()
+    arg = torch.where(arg.isfinite(), arg, torch.zeros(1).double())
+    # (fp32 holds nothing below 2^-126 to its full precision)
+    tol = (130 + arg) * U * size + (HALF_ULP[x.dtype] + U) * want.abs() + FLOOR[x.dtype] + 2.0 ** -120
+    err = (d.cpu().double() - want).abs()
+    say(f"  dlogits: worst {float((err / tol).max()):.3f} of the terms' tolerance")
+    assert bool((err <= tol).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("db", [0.0, 0.7])
+def test_route_bwd_saturated_sigmoids(db, sign, normalize):
+    """The slope of a sigmoid far from 0, on either side: not 1 minus what
+    rounds to 1."""
+    say("saturated", db, sign, normalize)
+    gen = torch.Generator().manual_seed(8)
+    x = sign * (8 + 17 * torch.rand(40, 61, generator=gen))
+    check_bwd_terms(x, 5, B.GG_SIGMOID, normalize, torch.randn(40, 5, generator=gen), db)
+
+
 # --------------------------------------------------------------------------
 # refusals, on the host (no GPU)
 # --------------------------------------------------------------------------
