@@ -554,7 +554,9 @@ gg_status gg_route(const void* logits, gg_dtype dtype, int64_t ld, int64_t token
  * The gradient of gg_route's logits:
  *   dlogits = d/dlogits (sum_tj dprob_tj prob_tj + dbalance balance)
  * at the choice `ids` (the choice and the counts have no gradient).  Rows of
- * a token without a choice are 0.
+ * a token without a choice are 0.  A NaN or +inf logit that was not chosen
+ * enters where the formulas have all experts: the balance loss, and GG_SOFTMAX
+ * without GG_FLAG_NORMALIZE.
  *
  * logits, dtype, ld, tokens, num_experts, top_k, score, scale, flags, ids,
  * counts, routed   as given to and made by gg_route.  An id outside

@@ -545,6 +545,11 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         c[e / EPL * kPitch + e % EPL] = e < E ? cb * (float)p.counts[e] : 0.0f;
     __syncthreads();
 
+    // Whether every expert's score has a gradient: the balance loss and plain
+    // softmax weights are over all of them.  Otherwise only the choices have
+    // one, and a NaN elsewhere (an expert that a bias of -inf took out) is not
+    // in any of their terms.
+    const bool every = p.dbalance || (softmax && !p.normalize);
     const int64_t rows = p.row_of ? p.m_rows : p.T * k;
     const int T_ = (int)p.T;                         // at most 2^23
     const int step = (int)gridDim.x * 4 * TPW;
@@ -590,35 +595,38 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
             *(f32x4*)(at + g * kPitch + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         wave_sync();
 
-        float top = 0.0f, inv = 0.0f;
-        if constexpr (softmax) {
-            row_scores<LPT, EPL>(x, true, lane_top(x), top, inv);
-        } else {                                     // x become the tails
-            float sum = 0.0f;
+        float top = 0.0f, inv = 0.0f, pc = 0.0f;
+        if (every) {
+            if constexpr (softmax) {
+                row_scores<LPT, EPL>(x, true, lane_top(x), top, inv);
+            } else {                                 // x become the tails
+                float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < EPL; i++) {
-                x[i] = signed_tail(x[i]);
-                sum += tail_sigmoid(x[i]);
+                for (int i = 0; i < EPL; i++) {
+                    x[i] = signed_tail(x[i]);
+                    sum += tail_sigmoid(x[i]);
+                }
+                inv = inverse_sum(group_all<LPT>(sum, OpAddF()), false);
             }
-            inv = inverse_sum(group_all<LPT>(sum, OpAddF()), false);
-        }
-        float pc = 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPL; i += 4) {
-            const f32x4 four = *(const f32x4*)(c + g * kPitch + i);
+            for (int i = 0; i < EPL; i += 4) {
+                const f32x4 four = *(const f32x4*)(c + g * kPitch + i);
 #pragma unroll
-            for (int h = 0; h < 4; h++)
-                pc = fmaf(softmax ? x[i + h] : tail_sigmoid(x[i + h]), four[h], pc);
+                for (int h = 0; h < 4; h++)
+                    pc = fmaf(softmax ? x[i + h] : tail_sigmoid(x[i + h]), four[h], pc);
+            }
+            pc = group_all<LPT>(pc, OpAddF()) * inv;
         }
-        pc = group_all<LPT>(pc, OpAddF()) * inv;
 
         // weights q (before scale) and their mean gradient sum q G
         if (p.normalize && softmax)
             top = choice_top<LPT, NJ>(v);
-        float chosen = 0.0f, qg = 0.0f;
+        float chosen = 0.0f, qg = 0.0f, slope[NJ];
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
-            v[s] = softmax ? __expf(v[s] - top) : tail_sigmoid(signed_tail(v[s]));
+            const float tail = softmax ? 0.0f : signed_tail(v[s]);
+            slope[s] = every ? 1.0f : tail_slope(tail);
+            v[s] = softmax ? __expf(v[s] - top) : tail_sigmoid(tail);
             chosen += v[s];
             qg = fmaf(v[s], G[s], qg);
         }
@@ -626,13 +634,13 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         qg = group_all<LPT>(qg, OpAddF());
         const float norm = p.normalize ? inverse_sum(chosen, softmax) : softmax ? inv : 1.0f;
         const float mean = qg * norm;
-        // what a choice adds: to dx (softmax), to ds (sigmoid)
+        // what a choice adds: to dx (softmax), to ds (sigmoid; dx if !every)
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
             if (e[s] < 0)
                 continue;
             const float centred = p.normalize ? G[s] - mean : G[s];
-            const float d = softmax ? v[s] * norm * centred : centred * norm;
+            const float d = softmax ? v[s] * norm * centred : centred * norm * slope[s];
             atomicAdd(&at[e[s] / EPL * kPitch + e[s] % EPL], d);
         }
         wave_sync();
@@ -647,7 +655,9 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
                 for (int h = 0; h < 4; h++) {
                     const float v = x[i + h];
                     float d;
-                    if constexpr (softmax)
+                    if (!every)
+                        d = a[h];
+                    else if constexpr (softmax)
                         d = fmaf(v * inv, b[h] - pull, a[h]);
                     else
                         d = fmaf(b[h] - pc, inv, a[h]) * tail_slope(v);

@@ -507,6 +507,38 @@ def test_route_bwd_saturated_sigmoids(db, sign, normalize):
     check_bwd_terms(x, 5, B.GG_SIGMOID, normalize, torch.randn(40, 5, generator=gen), db)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [B.GG_SOFTMAX, B.GG_SIGMOID])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_route_bwd_of_a_masked_nan(bad, normalize, score):
+    """An expert that a bias of -inf took out, with a logit of NaN or +inf.
+    Without the balance loss only the chosen experts' weights have a
+    gradient: the row's is that of a row where the expert is masked, 0 for the
+    expert itself.  Plain softmax weights are over all experts: NaN there."""
+    softmax = score == B.GG_SOFTMAX
+    x = make_logits(6, 61, torch.float32, 17)
+    y = x.clone()
+    x[2, 33] = x[4, 9] = bad
+    y[2, 33] = y[4, 9] = -INF
+    f = ref_route(y.double(), None, 4, softmax, normalize, 1.0)
+    g = torch.randn(6, 4, generator=torch.Generator().manual_seed(18))
+    args = (f["ids"].to(torch.int32).cuda(), f["counts"].to(torch.int32).cuda(),
+            torch.tensor([6], dtype=torch.int32).cuda(), g.cuda(), score, normalize, 1.0)
+    d = run_bwd(x.cuda(), *args).cpu().double()
+    want = ref_bwd(y, f["ids"], 4, softmax, normalize, 1.0, g.double(), 0.0)
+    rows = [0, 1, 3, 5] if softmax and not normalize else list(range(6))
+    assert float((d[rows] - want[rows]).abs().max()) <= 512 * U * 2 * float(g.abs().max())
+    if softmax and not normalize:
+        assert bool(torch.isnan(d[[2, 4]]).all())
+    # the balance loss is over all experts' probabilities: its gradient's rows
+    # are NaN where the formula's are, and no others
+    d = run_bwd(x.cuda(), *args, dbalance=torch.ones(1).cuda()).cpu()
+    assert not bool(torch.isnan(d[[0, 1, 3, 5]]).any())
+    if bad != bad:
+        assert bool(torch.isnan(d[[2, 4]]).all())
+
+
 # --------------------------------------------------------------------------
 # refusals, on the host (no GPU)
 # --------------------------------------------------------------------------
