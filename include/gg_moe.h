@@ -528,8 +528,11 @@ size_t gg_route_workspace_size(int64_t tokens, int32_t num_experts);
  *             over the N tokens, p the softmax, or s / (sum over all experts
  *             of s + 1e-20); 0 if N is 0
  * A NaN or +inf logit makes NaN of what the formulas say it enters.
- * fp32 arithmetic; the loss is summed in an order that depends on the sizes
- * alone, so equal calls give equal bits.
+ * fp32 arithmetic: a weight is good to some 16 units of 2^-24 of itself at
+ * logits of any size (softmax: besides the rounding of x minus the largest).
+ * The loss's probabilities are off by up to |x| units each and added up in
+ * fp32 within a block, in fp64 over the blocks, in an order that depends on
+ * the sizes alone, so equal calls give equal bits.
  *
  * logits     (tokens, num_experts), dtype GG_BF16, GG_F16 or GG_F32, element
  *            (t, e) at logits[t*ld + e], ld >= num_experts; aligned to its
@@ -567,7 +570,9 @@ gg_status gg_route(const void* logits, gg_dtype dtype, int64_t ld, int64_t token
  *            is outside 0 .. m_rows-1 (a dropped choice).
  * dbalance   float[1] in device memory, or NULL for no balance loss.
  * dlogits    output (tokens, num_experts), dtype, contiguous, not
- *            overlapping logits; aligned to its element; rounded once.
+ *            overlapping logits; aligned to its element; fp32 arithmetic,
+ *            rounded once (exponentials as in gg_route's weights for GG_F32,
+ *            as in its loss for the 16-bit types).
  */
 gg_status gg_route_bwd(const void* logits, gg_dtype dtype, int64_t ld, int64_t tokens,
                        int32_t num_experts, int32_t top_k, gg_score score, float scale,

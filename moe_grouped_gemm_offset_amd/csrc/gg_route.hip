@@ -32,17 +32,39 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr float kTiny = 1e-20f;          // added to sums of sigmoids, which can underflow
 
-__device__ __forceinline__ float sigmoid(float x) {
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+// Exponentials.  The hardware's, of a log2(e) rounded to fp32, is off by up to
+// |a| 2^-24 of itself: FULL brings back what that rounding left out, as a - t
+// ln(2) with ln(2) in two parts, and is good to 2 units of 2^-24.  It is used
+// where a caller sees the exponential itself, the weights and fp32 gradients
+// (weights at logits of -25 to -45: off by 5 units at most for 44).  Without it are
+// the sums over all experts, whose large terms have small arguments, the loss,
+// which is a mean over them, and gradients that are rounded to 16 bits: there
+// it would cost route_kernel 20.1 -> 24.6 us and route_bwd_kernel 19.0 -> 20.1
+// (65536 x 256 bf16).
+
+// exp(a) of a <= 0: 0 far below the normal numbers, a NaN kept.
+template <bool FULL>
+__device__ __forceinline__ float exp_below(float a) {
+    if constexpr (!FULL)
+        return __expf(a);
+    a = __builtin_elementwise_maximum(a, -110.0f);
+    const float t = a * 1.44269504f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float rest = fmaf(t, 1.90465421e-9f, fmaf(t, -0.693147182f, a));
+    return fmaf(e, rest, e);
 }
 
 // sigmoid(-|x|), at most 1/2, with x's sign.  A sigmoid and its slope come out
 // of it without 1 minus what rounds to 1: sigmoid(x) is the tail t or 1 - t,
 // the slope t (1 - t).  (From the sigmoid itself the slope is off by 6% at x =
 // 16 and 0 from 17 on.)
+template <bool FULL>
 __device__ __forceinline__ float signed_tail(float x) {
-    const float e = __expf(-fabsf(x));
-    return __builtin_copysignf(e * __builtin_amdgcn_rcpf(1.0f + e), x);
+    const float e = exp_below<FULL>(-fabsf(x)), d = 1.0f + e;
+    float r = __builtin_amdgcn_rcpf(d);              // to 1 ulp; a step of Newton's makes it half
+    if constexpr (FULL)
+        r = fmaf(fmaf(-d, r, 1.0f), r, r);
+    return __builtin_copysignf(e * r, x);
 }
 __device__ __forceinline__ float tail_sigmoid(float t) {
     return __builtin_signbitf(t) ? -t : 1.0f - t;
@@ -163,7 +185,7 @@ __device__ __forceinline__ float inverse_sum(float sum, bool softmax) {
 // turns them into the balance probabilities (softmax: x are exp(x - top), so
 // that p = x inv is the softmax as well; a row of -inf gives all zeros, one
 // with a NaN all NaN).  m is the lane's lane_top.
-template <int LPT, int EPL>
+template <int LPT, int EPL, bool FULL>
 __device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float m, float& top, float& inv) {
     float sum = 0.0f;
     if (softmax) {
@@ -171,7 +193,7 @@ __device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float 
         top = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            x[i] = __expf(x[i] - top);
+            x[i] = exp_below<FULL>(x[i] - top);
             sum += x[i];
         }
         sum = group_all<LPT>(sum, OpAddF());
@@ -180,7 +202,7 @@ __device__ __forceinline__ void row_scores(float (&x)[EPL], bool softmax, float 
         top = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            x[i] = sigmoid(x[i]);
+            x[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
             sum += x[i];
         }
         sum = group_all<LPT>(sum, OpAddF());
@@ -300,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         uint32_t most = group_all<LPT>(best, OpMaxU());
         float top = 0.0f, inv = 0.0f;
         if (stats || (softmax && !p.normalize)) {
-            row_scores<LPT, EPL>(x, softmax, m, top, inv);
+            row_scores<LPT, EPL, false>(x, softmax, m, top, inv);
             if (stats) {
                 // no choice: no part in the loss, though a bias of -inf may
                 // have taken out a NaN, which 0 times does not
@@ -352,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         float sum = 0.0f;
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
-            v[s] = softmax ? __expf(v[s] - top) : sigmoid(v[s]);
+            v[s] = softmax ? exp_below<true>(v[s] - top) : tail_sigmoid(signed_tail<true>(v[s]));
             sum += v[s];
         }
         if (p.normalize) {
@@ -526,6 +548,7 @@ __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(RouteArgs p, i
 template <int DT, int LPT, int EPL, int KIND, int SCORE>
 __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
     constexpr bool softmax = SCORE == GG_SOFTMAX;
+    constexpr bool kFull = DT == GG_F32;
     constexpr int TPW = 64 / LPT;
     constexpr int NJ = LPT >= 32 ? 1 : 32 / LPT;
     constexpr int kCap = LPT * EPL, kPitch = lane_pitch<EPL>();
@@ -597,24 +620,25 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
 
         float top = 0.0f, inv = 0.0f, pc = 0.0f;
         if (every) {
-            if constexpr (softmax) {
-                row_scores<LPT, EPL>(x, true, lane_top(x), top, inv);
-            } else {                                 // x become the tails
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < EPL; i++) {
-                    x[i] = signed_tail(x[i]);
-                    sum += tail_sigmoid(x[i]);
-                }
-                inv = inverse_sum(group_all<LPT>(sum, OpAddF()), false);
-            }
+            if constexpr (softmax)
+                row_scores<LPT, EPL, kFull>(x, true, lane_top(x), top, inv);
+            float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; i += 4) {
                 const f32x4 four = *(const f32x4*)(c + g * kPitch + i);
 #pragma unroll
-                for (int h = 0; h < 4; h++)
-                    pc = fmaf(softmax ? x[i + h] : tail_sigmoid(x[i + h]), four[h], pc);
+                for (int h = 0; h < 4; h++) {
+                    float score = x[i + h];
+                    if constexpr (!softmax) {        // x become the tails
+                        x[i + h] = signed_tail<kFull>(score);
+                        score = tail_sigmoid(x[i + h]);
+                        sum += score;
+                    }
+                    pc = fmaf(score, four[h], pc);
+                }
             }
+            if constexpr (!softmax)
+                inv = inverse_sum(group_all<LPT>(sum, OpAddF()), false);
             pc = group_all<LPT>(pc, OpAddF()) * inv;
         }
 
@@ -624,9 +648,9 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         float chosen = 0.0f, qg = 0.0f, slope[NJ];
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
-            const float tail = softmax ? 0.0f : signed_tail(v[s]);
+            const float tail = softmax ? 0.0f : signed_tail<kFull>(v[s]);
             slope[s] = every ? 1.0f : tail_slope(tail);
-            v[s] = softmax ? __expf(v[s] - top) : tail_sigmoid(tail);
+            v[s] = softmax ? exp_below<kFull>(v[s] - top) : tail_sigmoid(tail);
             chosen += v[s];
             qg = fmaf(v[s], G[s], qg);
         }
@@ -647,23 +671,22 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         const bool routed = group_first<LPT>(any, lane) >= 0;
         const float pull = pc + (softmax && !p.normalize ? mean : 0.0f);
         if (live) {
-            // a row without a choice has no gradient
+            auto gradients = [&](auto of) {
 #pragma unroll
-            for (int i = 0; i < EPL; i += 4) {
-                const f32x4 a = *(const f32x4*)(at + g * kPitch + i), b = *(const f32x4*)(c + g * kPitch + i);
+                for (int i = 0; i < EPL; i += 4) {
+                    const f32x4 a = *(const f32x4*)(at + g * kPitch + i), b = *(const f32x4*)(c + g * kPitch + i);
 #pragma unroll
-                for (int h = 0; h < 4; h++) {
-                    const float v = x[i + h];
-                    float d;
-                    if (!every)
-                        d = a[h];
-                    else if constexpr (softmax)
-                        d = fmaf(v * inv, b[h] - pull, a[h]);
-                    else
-                        d = fmaf(b[h] - pc, inv, a[h]) * tail_slope(v);
-                    x[i + h] = routed ? d : 0.0f;
+                    for (int h = 0; h < 4; h++)
+                        x[i + h] = routed ? of(x[i + h], a[h], b[h]) : 0.0f;
                 }
-            }
+            };
+            // a row without a choice has no gradient
+            if (!every)
+                gradients([&](float, float a, float) { return a; });
+            else if constexpr (softmax)
+                gradients([&](float v, float a, float b) { return fmaf(v * inv, b - pull, a); });
+            else
+                gradients([&](float v, float a, float b) { return fmaf(b - pc, inv, a) * tail_slope(v); });
             store_row<DT, EPL, KIND>((T*)p.dlogits + (int64_t)t * E, first, E, x);
         }
         wave_sync();

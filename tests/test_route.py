@@ -539,6 +539,43 @@ def test_route_bwd_of_a_masked_nan(bad, normalize, score):
         assert bool(torch.isnan(d[[2, 4]]).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [B.GG_SOFTMAX, B.GG_SIGMOID])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_route_weights_to_their_own_size(normalize, score):
+    """Every weight to fp32's precision of its own, far from 0 as well.  In u =
+    2^-24, for logits in steps of 1/8 (x - top is exact): an exponential 4, a
+    sigmoid's sum and quotient 2, the sum of six chosen ones 3 more, the last
+    quotient and products 3: 18 of the weight itself."""
+    softmax = score == B.GG_SOFTMAX
+    gen = torch.Generator().manual_seed(55)
+    x = -(25 * 8 + torch.randint(0, 20 * 8, (4000, 8), generator=gen)).float() / 8
+    if softmax:
+        x[:, 0] = -1.0
+    r = ref_route(x.double(), None, 6, softmax, normalize, 2.0)
+    o = run_route(x.cuda(), 6, None, score, normalize, 2.0)
+    assert torch.equal(o["ids"].cpu().long(), r["ids"])
+    err = (o["prob"].cpu().double() - r["prob"]).abs() / r["prob"]
+    say(f"  weights: rms {float(err.square().mean().sqrt()) / U:.2f} u, worst {float(err.max()) / U:.2f} u")
+    assert float(err.max()) <= 18 * U
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [B.GG_SOFTMAX, B.GG_SIGMOID])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("db", [0.0, 0.7])
+def test_route_bwd_to_its_terms(db, normalize, score):
+    """Every element of the gradient within its own terms' error, the balance
+    loss's alone (dprob 0) too."""
+    for i, (T, E, k) in enumerate(SHAPES):
+        gen = torch.Generator().manual_seed(300 + i)
+        g = torch.randn(T, k, generator=gen) * (i % 2 if db else 1)
+        say("bwd terms", T, E, k, normalize, score, db)
+        for dtype in (torch.float32, torch.bfloat16):
+            check_bwd_terms(make_logits(T, E, dtype, 310 + i, masked=0.3 if i % 3 == 0 else 0.0, spread=4.0), k,
+                            score, normalize, g, db)
+
+
 # --------------------------------------------------------------------------
 # refusals, on the host (no GPU)
 # --------------------------------------------------------------------------
