@@ -361,6 +361,115 @@ def test_combine_is_the_gradient_of_permute():
 
 
 # --------------------------------------------------------------------------
+# rows that pass the cache by: more than 256 MB of expert rows
+# --------------------------------------------------------------------------
+
+def big_case(T, k, E, H, dtype, seed):
+    """(row_of, counts, ends, x, weights, rows in use) on the GPU, groups padded
+    to 16; some choices without a row."""
+    counts, ends, row_of, m, _ = rows_case(T, k, E, H, dtype, 16, seed)
+    size = torch.empty(0, dtype=dtype).element_size()
+    assert T * k * H * size > 256 << 20
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randint(-99, 100, (T, H), generator=g, device="cuda", dtype=torch.int32)
+    x = (x.abs() if dtype == torch.uint8 else x.float() / 64).to(dtype)
+    w = torch.randn(T, k, generator=g, device="cuda")
+    return row_of.cuda(), counts.cuda(), ends.cuda(), x, w, m
+
+
+BIG = [(9001, 4, 8191, torch.uint8), (9001, 4, 4096, torch.bfloat16), (5003, 7, 4097, torch.float16),
+       (17_003, 2, 2050, torch.float32)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,dtype", BIG)
+def test_permute_past_the_cache(T, k, H, dtype):
+    say("permute past the cache", T, k, H, dtype)
+    row_of, counts, ends, x, _, m = big_case(T, k, 12, H, dtype, T)
+    out = torch.full((m, H), 7, dtype=dtype, device="cuda")
+    B.gg_permute(x, row_of, counts, ends, out)
+    torch.cuda.synchronize()
+    want = torch.full((m, H), 7, dtype=dtype, device="cuda")
+    want[: int(ends[-1])] = 0
+    ok = row_of >= 0
+    t = torch.arange(T, device="cuda")[:, None].expand(T, k)
+    want[row_of[ok].long()] = x[t[ok]]
+    assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,dtype", BIG[1:])
+def test_combine_past_the_cache(T, k, H, dtype):
+    say("combine past the cache", T, k, H, dtype)
+    row_of, counts, ends, x, w, m = big_case(T, k, 12, H, dtype, T)
+    y = torch.randn(m, H, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dtype)
+    out = torch.full((T, H), 9.0, dtype=dtype, device="cuda")
+    B.gg_combine(y, row_of, out, weights=w)
+    torch.cuda.synchronize()
+    want = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for j in range(k):
+        term = torch.where(row_of[:, j:j + 1] >= 0, y[row_of[:, j].clamp_min(0).long()].double() *
+                           w[:, j:j + 1].double(), 0.0)
+        want += term
+        size += term.abs()
+    tol = (k + 1) * U * size + HALF_ULP[dtype] * (1 + 2 ** -7) * want.abs() + FLOOR[dtype]
+    assert bool(((out.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,dtype", BIG[1:])
+def test_combine_bwd_past_the_cache(T, k, H, dtype):
+    say("combine_bwd past the cache", T, k, H, dtype)
+    row_of, counts, ends, d, w, m = big_case(T, k, 12, H, dtype, T)
+    y = torch.randn(m, H, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(dtype)
+    dy = torch.full((m, H), 7.0, dtype=dtype, device="cuda")
+    dw = torch.full((T, k), float("nan"), device="cuda")
+    B.gg_combine_bwd(d, y, row_of, w, counts, ends, dy, dw)
+    torch.cuda.synchronize()
+    end = int(ends[-1])
+    assert bool((dy[end:] == 7.0).all())
+    padding = torch.ones(end, dtype=torch.bool, device="cuda")
+    padding[row_of[row_of >= 0].long()] = False
+    assert bool((dy[:end][padding] == 0).all())
+    for j in range(k):
+        ok = row_of[:, j] >= 0
+        r = row_of[ok, j].long()
+        want = w[ok, j:j + 1].double() * d[ok].double()
+        tol = (HALF_ULP[dtype] * (1 + 2 ** -7) + U) * want.abs() + FLOOR[dtype]
+        assert bool(((dy[r].double() - want).abs() <= tol).all())
+        terms = y[r].double() * d[ok].double()
+        tol = (H / 256 + 32) * U * terms.abs().sum(1)
+        assert bool(((dw[ok, j].double() - terms.sum(1)).abs() <= tol).all())
+        assert bool((dw[~ok, j] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [1, 2, 3, 5, 6, 7, 9, 17])
+def test_combine_bwd_every_count_of_choices(k):
+    """Choices that fill a block's rows in flight in part, or in several turns."""
+    T, E, H = 50, 40, 515
+    say("combine_bwd choices", k)
+    counts, ends, row_of, m, g = rows_case(T, k, E, H, torch.float32, 8, k)
+    y, d, w = torch.randn(m, H, generator=g), torch.randn(T, H, generator=g), torch.randn(T, k, generator=g)
+    y[0] = float("nan")                                # not to be taken by a choice without a row
+    nan = row_of == 0
+    dy, dw = torch.full((m, H), 7.0, device="cuda"), torch.full((T, k), float("nan"), device="cuda")
+    B.gg_combine_bwd(d.cuda(), y.cuda(), row_of.cuda(), w.cuda(), counts.cuda(), ends.cuda(), dy, dw)
+    torch.cuda.synchronize()
+    ok = row_of >= 0
+    yy = torch.where(ok[:, :, None], y.double()[row_of.clamp_min(0).long()], torch.zeros(1).double())
+    terms = yy * d.double()[:, None, :]
+    near = (dw.cpu().double() - terms.sum(2)).abs() <= (H / 256 + 32) * U * terms.abs().sum(2)
+    assert bool(near[~nan].all()) and bool(torch.isnan(dw.cpu()[nan]).all()) and int(nan.sum()) == 1
+    want = torch.full((m, H), 7.0, dtype=torch.float64)
+    want[: int(ends[-1])] = 0
+    t = torch.arange(T)[:, None].expand(T, k)
+    want[row_of[ok].long()] = w[ok].double()[:, None] * d.double()[t[ok]]
+    assert bool(((dy.cpu().double() - want).abs() <= U * want.abs()).all())
+
+
+# --------------------------------------------------------------------------
 # refusals, on the host (no GPU)
 # --------------------------------------------------------------------------
 

@@ -173,6 +173,61 @@ def test_error_word_is_each_calls_own(T):
             assert B.gg_device_error(ws) == 0
 
 
+def test_the_most_tokens():
+    """2^23 tokens: the largest grids and the largest indices of a token."""
+    T, E, H = 1 << 23, 8, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.randn(T, E, generator=g, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, row_of = torch.empty(T, 1, **i32), torch.empty(T, 1, **i32)
+    counts, kept, ends, routed = (torch.empty(n, **i32) for n in (E, E, E, 1))
+    prob, balance = torch.empty(T, 1, device="cuda"), torch.empty(1, device="cuda")
+    say("most tokens: route")
+    B.gg_route(logits, ids, prob, counts, routed, balance)
+    torch.cuda.synchronize()
+    p = torch.softmax(logits.double(), 1)
+    first = logits.float().sort(dim=1, descending=True, stable=True).indices[:, :1]
+    assert torch.equal(ids.long(), first)
+    want = torch.bincount(first.flatten(), minlength=E)
+    assert torch.equal(counts.long(), want) and int(routed) == T
+    assert bool(((prob.double() - p.gather(1, first)).abs() <= 128 * 2.0 ** -24).all())
+    # (a group of lanes sums T / (768 * 64) = 171 tokens in fp32)
+    loss = float(E * (want / T * (p.sum(0) / T)).sum())
+    assert abs(float(balance) - loss) <= (128 + 171) * 2.0 ** -24 * loss
+    say("most tokens: plan")
+    m = B.gg_plan_max_rows(T, 1, E)
+    B.gg_plan(ids, kept, ends, row_of, m)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, counts)
+    flat = ids.flatten().long()
+    begin = ends.long() - (want + 255) // 256 * 256
+    order = flat.argsort(stable=True)
+    rows = torch.empty_like(flat)
+    rows[order] = begin[flat[order]] + torch.arange(T, device="cuda") - (want.cumsum(0) - want)[flat[order]]
+    assert torch.equal(row_of.flatten().long(), rows)
+    say("most tokens: rows")
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    x_rows = torch.full((m, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.gg_permute(x, row_of, kept, ends, x_rows)
+    out, dw = torch.empty_like(x), torch.empty(T, 1, device="cuda")
+    dy = torch.full((m, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.gg_combine(x_rows, row_of, out)
+    B.gg_combine_bwd(x, x_rows, row_of, torch.ones_like(prob), kept, ends, dy, dw)
+    torch.cuda.synchronize()
+    assert torch.equal(x_rows[rows], x) and torch.equal(out, x)
+    assert torch.equal(dy, x_rows) and bool((x_rows[int(ends[-1]):] == 7.0).all())
+    norm = x.double().square().sum(1, keepdim=True)
+    assert bool(((dw.double() - norm).abs() <= 32 * 2.0 ** -24 * norm).all())
+    say("most tokens: route_bwd")
+    d = torch.empty_like(logits)
+    B.gg_route_bwd(logits, ids, counts, routed, prob, d)
+    torch.cuda.synchronize()
+    w = p.gather(1, first) * prob.double()
+    want = torch.zeros_like(p).scatter_(1, first, w) - p * w
+    size = torch.zeros_like(p).scatter_(1, first, w) + p * w
+    assert bool(((d.double() - want).abs() <= 160 * 2.0 ** -24 * size + 2.0 ** -8 * 1.01 * want.abs()).all())
+
+
 def test_rows_past_32_bits():
     """Expert rows past 2^32 bytes from the first, and past 2^31 elements."""
     H, T, k = 8192, 6, 2

@@ -577,6 +577,68 @@ def test_route_bwd_to_its_terms(db, normalize, score):
 
 
 # --------------------------------------------------------------------------
+# many tokens: several blocks joined, several passes of a block
+# --------------------------------------------------------------------------
+
+def check_route_many(T, E, k, dtype, score, masked=0.02):
+    """check_route with a choice by a stable sort (finite or -inf logits)."""
+    x = make_logits(T, E, dtype, T, masked=masked)
+    key = x.float().sort(dim=1, descending=True, stable=True)
+    ids = torch.where(key.values[:, :k] > -INF, key.indices[:, :k], -1)
+    o = run_route(x.cuda(), k, None, score, True, 2.5)
+    r = ref_route(x.double(), None, k, score == B.GG_SOFTMAX, True, 2.5, ids=ids)
+    assert torch.equal(o["ids"].cpu().long(), ids)
+    assert torch.equal(o["counts"].cpu().long(), r["counts"])
+    assert int(o["routed"]) == r["routed"]
+    assert float((o["prob"].cpu().double() - r["prob"]).abs().max()) <= 128 * U * 2.5
+    loss = float(r["balance"])
+    say(f"  balance {float(o['balance']):.7f} ref {loss:.7f}")
+    # (the tokens that a group of lanes sums in fp32: T over 768 blocks of 8)
+    assert abs(float(o["balance"]) - loss) <= (128 + T / 6144) * U * loss
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1537, 3100, 4700, 6144, 6145, 7000, 13000])
+def test_route_joins_every_block(T):
+    """8 tokens a block at 1024 experts: 193 to 768 blocks, one to four
+    quarters of the join, then a second and a third pass of the blocks."""
+    say("route many", T)
+    check_route_many(T, 1024, 4, torch.float32, B.GG_SOFTMAX)
+    check_route_many(T, 1001, 6, torch.bfloat16, B.GG_SIGMOID)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(100_000, 64, 2), (49_500, 61, 8), (26_000, 256, 8), (13_001, 300, 4)])
+def test_route_passes(T, E, k):
+    """Several passes of the blocks in the other layouts."""
+    say("route passes", T, E, k)
+    check_route_many(T, E, k, torch.float16, B.GG_SOFTMAX)
+    check_route_many(T, E, k, torch.float32, B.GG_SIGMOID)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(9000, 1024, 4), (17_001, 500, 3), (33_000, 256, 8), (33_000, 97, 2),
+                                   (66_000, 61, 2)])
+def test_route_bwd_passes(T, E, k):
+    """More tokens than 2048 blocks take in one pass."""
+    for score in (B.GG_SOFTMAX, B.GG_SIGMOID):
+        say("route_bwd passes", T, E, k, score)
+        for normalize, db in ((True, 0.7 * T), (False, 0.0)):
+            x = make_logits(T, E, torch.float32, T)
+            key = x.sort(dim=1, descending=True, stable=True)
+            ids = key.indices[:, :k]
+            counts = torch.bincount(ids.flatten(), minlength=E)
+            g = torch.randn(T, k, generator=torch.Generator().manual_seed(T))
+            d = run_bwd(x.cuda(), ids.to(torch.int32).cuda(), counts.to(torch.int32).cuda(),
+                        torch.tensor([T], dtype=torch.int32).cuda(), g.cuda(), score, normalize, 1.5, None,
+                        torch.tensor([db]).cuda())
+            want, size = ref_bwd_terms(x, ids, score == B.GG_SOFTMAX, normalize, 1.5, g, db)
+            # (the terms' error of check_bwd_terms, arguments below 30)
+            tol = 160 * U * size + 2.0 ** -120
+            assert bool(((d.cpu().double() - want).abs() <= tol).all())
+
+
+# --------------------------------------------------------------------------
 # refusals, on the host (no GPU)
 # --------------------------------------------------------------------------
 
