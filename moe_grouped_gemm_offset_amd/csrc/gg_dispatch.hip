@@ -284,7 +284,7 @@ __device__ __forceinline__ int wave_token(int tx) {
 // and written k times.
 template <int SIZE, bool NT>
 __global__ void __launch_bounds__(kRowThreads) permute_kernel(RowsArgs p, int tx, int pads) {
-    typedef typename Raw<16>::T V;
+    typedef Raw16 V;
     const int col = threadIdx.x % tx + (int)blockIdx.y * tx;
     const int64_t bytes = (int64_t)p.width * SIZE;
     if ((int64_t)col * 16 >= bytes)

@@ -42,25 +42,16 @@ __device__ __forceinline__ typename Elem<DT>::T from_f32(float f) {
 }
 
 // ---- vectors ---------------------------------------------------------------
-// N elements in one access of up to 16 bytes that needs no more than the
-// element's own alignment: rows of an odd width start anywhere, and global
-// memory takes unaligned vectors.
+// 16 bytes of elements in one access that needs no more than the element's own
+// alignment: rows of an odd width start anywhere, and global memory takes
+// unaligned vectors.
 
-template <int BYTES>
-struct Raw;
-template <>
-struct Raw<16> {
-    typedef uint32_t T __attribute__((ext_vector_type(4), aligned(1)));
-};
-template <>
-struct Raw<8> {
-    typedef uint32_t T __attribute__((ext_vector_type(2), aligned(1)));
-};
+typedef uint32_t Raw16 __attribute__((ext_vector_type(4), aligned(1)));
 
 template <int DT, int N>
 struct Vec {
-    static constexpr int kBytes = N * (int)sizeof(typename Elem<DT>::T);
-    typedef typename Raw<kBytes>::T T;
+    static_assert(N * (int)sizeof(typename Elem<DT>::T) == 16, "16 bytes");
+    typedef Raw16 T;
     T raw;
 
     // NT: values that are not used again soon pass the caches by
@@ -82,30 +73,20 @@ struct Vec {
             return to_f32<DT>((uint16_t)(raw[i >> 1] >> (16 * (i & 1))));
     }
     // Moves element d + i to i (0 <= d < N; what comes in at the top is
-    // unspecified).
+    // unspecified).  (Words by name: of an array of them the compiler may make
+    // memory in LDS, indexed by d.)
     __device__ __forceinline__ void drop(int d) {
-        constexpr int W = kBytes / 4;
         const int words = DT == GG_F32 ? d : d >> 1;
-        uint32_t r[W];
-#pragma unroll
-        for (int i = 0; i < W; i++)
-            r[i] = raw[i];
-        if constexpr (W == 4) {
-            r[0] = words & 2 ? raw[2] : raw[0];
-            r[1] = words & 2 ? raw[3] : raw[1];
-        }
-#pragma unroll
-        for (int i = 0; i + 1 < W; i++)
-            r[i] = words & 1 ? r[i + 1] : r[i];
-        if constexpr (DT != GG_F32) {
+        const bool two = words & 2, one = words & 1;
+        const uint32_t a = two ? raw[2] : raw[0], b = two ? raw[3] : raw[1], c = raw[2], e = raw[3];
+        const uint32_t w0 = one ? b : a, w1 = one ? c : b, w2 = one ? e : c;
+        if constexpr (DT == GG_F32) {
+            raw = T{w0, w1, w2, e};
+        } else {
             const uint32_t sh = 16 * (d & 1);
-#pragma unroll
-            for (int i = 0; i < W; i++)
-                r[i] = __builtin_amdgcn_alignbit(r[i + 1 < W ? i + 1 : i], r[i], sh);
+            raw = T{__builtin_amdgcn_alignbit(w1, w0, sh), __builtin_amdgcn_alignbit(w2, w1, sh),
+                    __builtin_amdgcn_alignbit(e, w2, sh), __builtin_amdgcn_alignbit(e, e, sh)};
         }
-#pragma unroll
-        for (int i = 0; i < W; i++)
-            raw[i] = r[i];
     }
     __device__ __forceinline__ void set(const float (&f)[N]) {
         if constexpr (DT == GG_F32) {

@@ -101,9 +101,9 @@ constexpr int lane_pitch() {
 // not but hold one, kShortRows are shorter than one.
 enum RowKind { kWholeRows = 0, kOddRows = 1, kShortRows = 2 };
 
-template <int DT, int EPL>
+template <int DT>
 constexpr int row_vector() {
-    return EPL * (int)sizeof(typename Elem<DT>::T) >= 16 ? 16 / (int)sizeof(typename Elem<DT>::T) : EPL;
+    return 16 / (int)sizeof(typename Elem<DT>::T);
 }
 
 // The EPL experts of a lane, -inf past the row's end and where !live.  The
@@ -112,7 +112,7 @@ constexpr int row_vector() {
 template <int DT, int EPL, int KIND>
 __device__ __forceinline__ void load_row(const typename Elem<DT>::T* row, int first, int E, bool live,
                                          float (&x)[EPL]) {
-    constexpr int N = row_vector<DT, EPL>();
+    constexpr int N = row_vector<DT>();
     // `first` as a value of its own in every pass over this: compares with it
     // would otherwise be kept from pass to pass, a register pair each
     asm volatile("" : "+v"(first));
@@ -146,7 +146,7 @@ __device__ __forceinline__ void load_row(const typename Elem<DT>::T* row, int fi
 template <int DT, int EPL, int KIND>
 __device__ __forceinline__ void store_row(typename Elem<DT>::T* row, int first, int E,
                                           const float (&x)[EPL]) {
-    constexpr int N = row_vector<DT, EPL>();
+    constexpr int N = row_vector<DT>();
 #pragma unroll
     for (int c = 0; c < EPL; c += N) {
         if (first + c + N <= E) {
@@ -719,7 +719,7 @@ size_t route_workspace(int64_t T, int E) {
 // to 128 experts: see the measurements above), how the rows load.
 template <int DT, class F>
 static hipError_t by_experts(int E, F f) {
-    constexpr int N = row_vector<DT, 8>();
+    constexpr int N = row_vector<DT>();
 #define GG_KIND(LPT, EPL)                                                     \
     (E % N == 0 ? f(std::integral_constant<int, LPT>(), std::integral_constant<int, EPL>(),    \
                     std::integral_constant<int, kWholeRows>())                                     \

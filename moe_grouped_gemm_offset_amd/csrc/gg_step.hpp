@@ -80,10 +80,12 @@ struct GradArgs {
     int32_t* ws;
 };
 
-// Launchers (return the HIP status of the launch); Bytes of workspace a route / plan call of this size uses
+// Bytes of workspace that a route, plan or norm call uses.
 size_t route_workspace(int64_t T, int E);
 size_t plan_workspace(int64_t T, int E);
 size_t grad_workspace();
+// Launchers: the HIP status of the launch; *info, where given, says what was
+// launched.
 hipError_t launch_route(const RouteArgs& p, int dtype, hipStream_t s, LaunchInfo* info);
 hipError_t launch_route_bwd(const RouteBwdArgs& p, int dtype, hipStream_t s, LaunchInfo* info);
 hipError_t launch_plan(const PlanArgs& p, hipStream_t s, LaunchInfo* info);
