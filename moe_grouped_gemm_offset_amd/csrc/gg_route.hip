@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         float sum = 0.0f;
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
+            if (s * LPT >= k)                        // no lane's: the wave skips it
+                continue;
             v[s] = softmax ? exp_below<true>(v[s] - top) : tail_sigmoid(signed_tail<true>(v[s]));
             sum += v[s];
         }
@@ -645,9 +647,11 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs p) {
         // weights q (before scale) and their mean gradient sum q G
         if (p.normalize && softmax)
             top = choice_top<LPT, NJ>(v);
-        float chosen = 0.0f, qg = 0.0f, slope[NJ];
+        float chosen = 0.0f, qg = 0.0f, slope[NJ] = {};
 #pragma unroll
         for (int s = 0; s < NJ; s++) {
+            if (s * LPT >= k)                        // no lane's: the wave skips it
+                continue;
             const float tail = softmax ? 0.0f : signed_tail<kFull>(v[s]);
             slope[s] = every ? 1.0f : tail_slope(tail);
             v[s] = softmax ? exp_below<kFull>(v[s] - top) : tail_sigmoid(tail);
