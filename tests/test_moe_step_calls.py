@@ -228,6 +228,28 @@ def test_the_most_tokens():
     assert bool(((d.double() - want).abs() <= 160 * 2.0 ** -24 * size + 2.0 ** -8 * 1.01 * want.abs()).all())
 
 
+def test_logits_past_32_bits():
+    """Rows of logits at a pitch that takes the last ones past 2^32 bytes and
+    2^31 elements: the same bits as of the rows put together."""
+    T, E, k = 300_000, 40, 3
+    wide = torch.empty(T, 8192, dtype=torch.bfloat16, device="cuda")
+    x = wide[:, 17:17 + E]
+    x.copy_(torch.randn(T, E, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda"))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    got = []
+    for logits in (x, x.contiguous()):
+        o = [torch.full((T, k), -7, **i32), torch.zeros(T, k, device="cuda"), torch.zeros(E, **i32),
+             torch.zeros(1, **i32), torch.zeros(1, device="cuda"), torch.zeros(T, E, dtype=x.dtype, device="cuda")]
+        say("logits past 32 bits", logits.stride())
+        B.gg_route(logits, *o[:5])
+        B.gg_route_bwd(logits, o[0], o[2], o[3], o[1], o[5], dbalance=torch.ones(1, device="cuda"))
+        torch.cuda.synchronize()
+        got.append(o)
+    assert same(*got) and int(got[0][3]) == T
+    top = x[-1].float().sort(descending=True, stable=True).indices[:k]
+    assert torch.equal(got[0][0][-1].long(), top)
+
+
 def test_rows_past_32_bits():
     """Expert rows past 2^32 bytes from the first, and past 2^31 elements."""
     H, T, k = 8192, 6, 2
