@@ -185,7 +185,9 @@ enum {
                                    in its token                                */
 };
 
-/* ABI version of the loaded library (GG_ABI_VERSION of its build). */
+/* ABI version of the loaded library (GG_ABI_VERSION of its build).  It changes
+ * when a call or a structure that was there does; a call that has come since
+ * is found by its name. */
 int gg_abi_version(void);
 
 /* Message for the last non-GG_OK status returned on this thread ("" if
@@ -512,7 +514,10 @@ size_t gg_route_workspace_size(int64_t tokens, int32_t num_experts);
 /*
  * The choice of experts, their weights, tokens per expert and the balance
  * loss.  Per token t, with x its logits:
- *   key_e   = x_e + bias_e                     (one fp32 addition)
+ *   key_e   = x_e + bias_e                     (one fp32 addition; with
+ *             GG_SIGMOID too the bias is on the logit, not on the score:
+ *             sigmoid(x_e) + bias_e is another order, which this call does
+ *             not have)
  *   ids     = the top_k experts of the largest keys, largest first, ties to
  *             the lower index.  -0 and +0 are equal; a NaN of either sign is
  *             above +inf.  A logit, bias or key of -inf is never chosen:

@@ -1,8 +1,9 @@
 """ctypes binding of libgg_moe (include/gg_moe.h) -- argument marshalling only.
 
-Each function takes torch tensors (device memory allocated by PyTorch) or
-raw integers for pointers, converts them to the C arguments, calls the C
-entry point of the same name and raises GGError on a non-GG_OK status.
+Each function takes torch tensors (device memory allocated by PyTorch) or, for
+the grouped GEMMs, raw integers for pointers, converts them to the C
+arguments, calls the C entry point of the same name and raises GGError on a
+non-GG_OK status.
 Every step of the computation runs in the library's HIP kernels; if the
 library has not been built, loading it raises.
 """

@@ -2,20 +2,25 @@
 //
 // The tensors are one range of elements, cut at `ends` (cumulative element
 // counts).  Blocks take equal pieces of the range and find, by a search over
-// `ends`, the tensors that a piece covers, so that a thousand small tensors
-// and a few large ones make the same kind of work, with no table to build on
-// the host.  Squares are summed in 64 bits: no overflow or underflow of a
-// square for any fp32 value, and no error of the sum's length.
+// `ends`, the tensors that a piece covers: equal work by elements, with no
+// table to build on the host.  Within a piece a block takes its tensors one
+// after another, each a chain of dependent loads (end, type and address,
+// values), so that what costs there is the number of tensors, not their sizes:
+// 256 tensors of 16 elements are one piece, 115 us for the norm and 158 for
+// the scaling; 1000 of 128 elements 17, 4 and 23 us.  Squares are summed in 64
+// bits: no overflow or underflow of a square for any fp32 value, and no error
+// of the sum's length.
 //
-// Memory bound.  What sets the rate is how the blocks are cut: the norm, which
-// only reads, runs at 6.9 TB/s with 2048 blocks of non-temporal loads (5.2
-// without the hint and one load in flight); the scaling writes as much as it
-// reads and wants many short blocks -- pieces of 8192 elements 6.5 TB/s, of
-// 32768 5.8, of 4096 4.9 (64 tensors of 4096 x 2048 bf16: 156 and 332 us).
-// Walking the pieces backwards, or loads that stay in the cache, change
-// nothing at 64 MB to 1 GB: the scaling finds nothing of the norm's pass.  96
-// small tensors of mixed types (10 MB): 5.3, 2 and 7.4 us, the latency of the
-// search, the addresses and the values behind one another.
+// Memory bound where the tensors are large: 64 of 4096 x 2048 bf16, out of
+// place, 162 and 338 us (medians), 6.6 and 6.4 TB/s.  What sets the rate is how
+// the blocks are cut.  Each at its fastest: the norm, which only reads, 6.9
+// TB/s with 2048 blocks of non-temporal loads, 5.2 without the hint and with
+// one load in flight; the scaling, which writes as much as it reads, wants many
+// short blocks: pieces of 8192 elements 6.5, of 32768 5.8, of 4096 4.9.  Walking the pieces backwards,
+// or loads that stay in the cache, change nothing at 64 MB to 1 GB: the scaling
+// finds nothing of the norm's pass.  96 tensors of mixed types, 40000 elements
+// on average (10 MB): 5.1, 4.7 and 7.4 us, the latency of the search, the
+// addresses and the values behind one another.
 #include "gg_lane.hpp"
 #include "gg_step.hpp"
 
@@ -30,7 +35,8 @@ constexpr int kNormPiece = 32768, kClipPiece = 8192, kClipBlocks = 1 << 20;
 // Elements of a piece: about kMaxBlocks pieces, of 4096 elements at least and
 // `most` at most.  (A block's start is what a small piece costs: with 2048 and
 // twice the blocks, 3.8 M elements in 96 tensors take 7.0 and 8.1 us for 5.3
-// and 7.4; with 8192 as long as with 4096.)
+// and 7.4; with 8192 as long as with 4096.  Tensors of a few elements are the
+// other way round: twice as many of them follow one another in a block.)
 int64_t piece_size(int64_t total, int64_t most) {
     int64_t c = (total / kMaxBlocks + 2047) / 2048 * 2048;
     return c < 4096 ? 4096 : c > most ? most : c;

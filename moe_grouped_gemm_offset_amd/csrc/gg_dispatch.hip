@@ -256,14 +256,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_assign_kernel(PlanArgs p, i
 //
 // Bound by memory: every token row is read or written once, every expert row
 // once.  Measured, bf16 (a copy kernel's best on the same card is 6.6 TB/s):
-// - permute, 8192 tokens x 8 rows of 4096 (604 MB, and 67 MB of zeros): 109 us,
+// - permute, 8192 tokens x 8 rows of 4096 (604 MB, and 67 MB of zeros): 111 us,
 //   6.1 TB/s.  Scattering, so that a token row is read once.
 // - combine, the same sizes: 99 us, 6.1 TB/s.  A row at a time per thread:
 //   with 2, 4 or 8 rows' loads at once 102 us, and 252 for 231 at two rows of
 //   7168 a token; enough waves are in flight.
-// - combine_bwd, 32768 tokens x 2 rows of 7168 (2.35 GB): 415 us, 5.7 TB/s.
+// - combine_bwd, 32768 tokens x 2 rows of 7168 (2.35 GB): 421 us, 5.6 TB/s.
 //   Here a block keeps a token (its sums end in one place), so 8 vectors of
-//   rows at once are needed: one at a time 516 us.
+//   rows at once are needed: one at a time 516 us.  A slot without a row (past
+//   k, or a dropped choice) loads row 0, which the cache holds: 65536 rows of
+//   4096 in 1, 2, 3, 4, 5, 6, 7, 8 and 9 choices a token run at 5.1, 5.5, 5.5,
+//   5.3, 5.2, 5.2, 4.9, 4.8 and 4.3 TB/s, nothing at 3, 5 and 6, 10% at 9,
+//   whose second turn has one row in eight slots.
 
 constexpr int kRowThreads = 256;
 constexpr int kPadParts = 8;                         // blocks that share an expert's padding rows

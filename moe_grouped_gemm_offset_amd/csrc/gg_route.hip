@@ -5,16 +5,19 @@
 // consecutive experts, so that one pass over the logits holds a token's row
 // in registers.  Statistics, weights and gradients are in fp32.
 //
-// Measured at 65536 tokens x 256 experts, bf16, 8 choices (34 MB of logits):
-// - route_kernel 19.7 us and route_join_kernel 5 us.  Bound by the vector ALU:
-//   a wave spends some 450 vector instructions and 33 transcendental ones on
-//   four tokens, 43% of them in the 8 steps of the choice; 80% of its cycles
-//   issue one.  Occupancies of 4, 6 and 8 waves a SIMD give the same time.
-//   Twice the experts a lane (8 lanes x 32) halves what the reductions cost
-//   a token but leaves half the passes to hide latency: 21.8 us.
-// - route_bwd_kernel 18.5 us, 73 MB read and written once and half a million
-//   scattered 4-byte reads of dprob: latency of the chain ids -> rows -> dprob.
-//   8 lanes a token 26.9 us, 32 lanes 21.6.
+// Measured at 65536 tokens x 256 experts, bf16, 8 choices (34 MB of logits;
+// medians):
+// - route_kernel 20.2 us (sigmoid) and route_join_kernel 5.0 us.  Bound by the
+//   vector ALU: a wave spends some 500 vector instructions, 35 of them
+//   transcendental, on four tokens, two fifths in the 8 steps of the choice;
+//   79% of its cycles issue one.  Occupancies of 4, 6 and 8 waves a SIMD give
+//   the same time.  Twice the experts a lane (8 lanes x 32) halves what the
+//   reductions cost a token but leaves half the passes to hide latency: 2.2 us
+//   more.
+// - route_bwd_kernel 18.4 us (softmax) and 21.1 (sigmoid, whose slope takes a
+//   second value an expert).  88 MB from and to memory by the counters, 13 us
+//   at a copy's rate: the latency of the chain ids -> rows -> dprob is the
+//   rest.  8 lanes a token take 8 us more, 32 lanes 3.
 // A few tokens (5 x 256): 5 us, the launch and four dependent loads.
 #include <cfloat>
 #include <type_traits>
@@ -283,6 +286,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         const float b = p.bias && e < E ? p.bias[e] : 0.0f;
         bias[e / EPL * kPitch + e % EPL] = b <= FLT_MAX ? b + 0.0f : FLT_MAX;
     }
+    // (fp32: a group adds T / (blocks x groups) probabilities here, 171 at 2^23
+    // tokens of 8 experts; the blocks' sums are joined in fp64)
     float psum[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; i++)
@@ -719,8 +724,11 @@ size_t route_workspace(int64_t T, int E) {
 }
 
 // Calls f with the kernels' parameters for E experts of a type: lanes a token,
-// experts a lane (the fewest lanes that leave a lane 16 experts at most, 8 up
-// to 128 experts: see the measurements above), how the rows load.
+// experts a lane, how the rows load.  A lane has 16 experts at most, 8 up to 128
+// of them.  One table for both kernels, which agree from 65 experts on (the
+// measurements above); up to 64 they do not, at 65536 x 64 fp32 the choice
+// takes 9.8 us with 8 lanes x 8 and 11.5 with 4 x 16, the gradient 11.6 with 8
+// x 8 and 10.2 with 16 x 4.
 template <int DT, class F>
 static hipError_t by_experts(int E, F f) {
     constexpr int N = row_vector<DT>();
