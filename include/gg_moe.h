@@ -34,6 +34,13 @@
  *   gg_grad_norm, gg_grad_clip   the 2-norm over many gradients, and
  *              clipping by it.
  *
+ * and the forward pass of the experts, with weights in 4 bits:
+ *
+ *   gg_mx4_quant, gg_mx4_dequant   rows to MXFP4 and back.
+ *   gg_glu     the gated activation whose backward gg_dglu computes.
+ *   gg_gemm_mx4   the grouped product of MXFP4 rows and weights.
+ *   gg_moe_few   a whole layer for up to 64 tokens, bf16 or MXFP4 weights.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Pointers are device pointers unless marked [host].  Every buffer is
@@ -90,7 +97,9 @@ typedef enum {
     GG_F16 = 1,
     GG_F32 = 2,
     GG_F8E4M3 = 3,           /* OCP E4M3 ("float8_e4m3fn"): max 448, no inf     */
-    GG_F8E5M2 = 4            /* OCP E5M2 ("float8_e5m2"): max 57344, inf / NaN  */
+    GG_F8E5M2 = 4,           /* OCP E5M2 ("float8_e5m2"): max 57344, inf / NaN  */
+    GG_MXFP4 = 5             /* OCP E2M1 codes, two a byte, with E8M0 scales: the
+                                weights of gg_moe_few                           */
 } gg_dtype;
 
 typedef enum {
@@ -719,6 +728,158 @@ gg_status gg_grad_norm(const int64_t* ptrs, const int64_t* ends, const int32_t* 
 gg_status gg_grad_clip(const int64_t* ptrs, const int64_t* ends, const int32_t* dtypes, int32_t n,
                        int64_t total, const double* sumsq, float max_norm, float eps, float* norm,
                        const int64_t* out_ptrs, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* MXFP4: quantisation                                                       */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * MXFP4 (OCP Microscaling): blocks of 32 consecutive values of a row, one E2M1
+ * code of 4 bits a value -- sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6 for 0 .. 7 --
+ * and one E8M0 scale byte s a block: value = code * 2^(s - 127), s = 255: the
+ * block is NaN.
+ * codes      (rows, width/2): value 2j of a row in the low half of its byte j,
+ *            value 2j + 1 in the high half.
+ * scales     (rows, width/32).
+ *
+ * gg_mx4_quant: s - 127 = e is the smallest e >= -127 with max|x| of the block
+ * <= 6 * 2^e (-127 for a block of zeros), so that no value is clamped; each
+ * code is x / 2^e rounded to the nearest, ties to the even code, keeping the
+ * sign of zeros.  A block with a NaN or an infinity has scale 255 and codes 0.
+ * (The values' gradient, taken straight through, is the gradient of x.)
+ *
+ * x          (rows, width), GG_BF16, GG_F16 or GG_F32, element (r, c) at
+ *            x[r*ldx + c], ldx >= width; aligned to its element.
+ * rows       0 .. 2^30.  width: a multiple of 32, at most 2^20.
+ * codes, scales  outputs, contiguous, of any alignment (gg_gemm_mx4 and
+ *            gg_moe_few read codes at 16-byte alignment).
+ * end        int32[1] in device memory, or NULL: rows at or past *end are
+ *            neither read nor written (padded_offsets + E - 1 for a dispatched
+ *            batch).
+ */
+gg_status gg_mx4_quant(const void* x, gg_dtype dtype, int64_t ldx, int64_t rows, int32_t width,
+                       uint8_t* codes, uint8_t* scales, const int32_t* end, void* stream);
+
+/*
+ * out = the values that codes and scales stand for, rounded once to dtype
+ * (bf16 and fp32 hold every one but those past their largest, which become
+ * infinities).
+ *
+ * out        (rows, width), GG_BF16, GG_F16 or GG_F32, element (r, c) at
+ *            out[r*ldo + c], ldo >= width; aligned to its element.
+ * rows, width, codes, scales, end  as for gg_mx4_quant.
+ */
+gg_status gg_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t width,
+                         void* out, gg_dtype dtype, int64_t ldo, const int32_t* end, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The gated activation                                                      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The forward pass of what gg_dglu and gg_dglu_mx differentiate (at beta 1):
+ * compact column n of a row lies in block pair p = n/32 at j = n%32, its input
+ * u in column 64p + j of c and its gate g in 64p + 32 + j (GG_FLAG_GATE_FIRST
+ * swaps them).
+ *   GG_DSWIGLU   y = prob g sigmoid(g) u
+ *   GG_DGEGLU    y = prob gc sigmoid(geglu_alpha gc) (uc + linear_offset),
+ *                gc = min(g, clamp_max), uc = clamp(u, clamp_min, clamp_max)
+ *   GG_DSITUGLU  y = prob b1 tanh(g/b1) sigmoid(g) b2 tanh(u/b2)
+ * fp32 arithmetic, rounded once.  A NaN gate or input gives NaN.
+ *
+ * c          (rows, 2n), GG_BF16, GG_F16 or GG_F32, row pitch ldc >= 2n.
+ * prob       float[rows], or NULL for 1.
+ * rows       0 .. 2^30.  n: a multiple of 32, at most 2^20.
+ * y          output (rows, n), GG_BF16, GG_F16 or GG_F32, row pitch ldy >= n.
+ * c and y aligned to their elements.
+ * act and its constants  as for gg_dglu_mx.
+ * flags      0 or GG_FLAG_GATE_FIRST.
+ * end        as for gg_mx4_quant.
+ */
+gg_status gg_glu(const void* c, gg_dtype c_dtype, int64_t ldc, const float* prob, int64_t rows,
+                 int32_t n, void* y, gg_dtype y_dtype, int64_t ldy, gg_act act, float geglu_alpha,
+                 float clamp_min, float clamp_max, float linear_offset, float situ_beta1,
+                 float situ_beta2, uint32_t flags, const int32_t* end, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The grouped product of MXFP4 rows and weights                             */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace gg_gemm_mx4 needs. */
+size_t gg_gemm_mx4_workspace_size(void);
+
+/*
+ * For the rows m of group g (offsets[g-1] <= m < offsets[g], offsets[-1] = 0):
+ *   d[m, n] = alpha_g * sum_k deq(a[m, k]) deq(b_g[n, k]) + bias[g, n]
+ * with MXFP4 operands (above), fp32 accumulation, rounded once to d_dtype.
+ *
+ * a_fp4, sfa  codes (m_rows, k/2) and scales (m_rows, k/32).
+ * k          a multiple of 128, at most 2^21.  n: a multiple of 32, at most
+ *            2^21 (GG_ERR_UNSUPPORTED beyond either limit).
+ * b_fp4, sfb  dense weights: codes (L, n, k/2), scales (L, n, k/32);
+ * b_ptrs, sfb_ptrs  or: int64[L] device arrays of the experts' codes (n, k/2)
+ *            and scales (n, k/32).  Exactly one of the two pairs is given.
+ * offsets    int32[L] cumulative group ends, non-decreasing, at most m_rows;
+ *            groups of any size, empty ones among them (gg_plan's
+ *            padded_offsets at any granule).  An end below an earlier one or 0
+ *            makes an empty group and sets GG_DEVERR_DECREASING, one past
+ *            m_rows is cut off and sets GG_DEVERR_LAST.  L in 1..1024.
+ * m_rows     0 .. 2^31-1.  Rows of d at or past the last end are not written.
+ * alpha      float[L], or NULL for 1.  bias: float (L, n), or NULL.
+ * d          output (m_rows, n) contiguous, GG_BF16, GG_F16 or GG_F32.
+ * Codes and d 16-byte, scales, alpha and bias 4-byte aligned.
+ * flags      0.
+ * workspace  >= gg_gemm_mx4_workspace_size() bytes, 256-B aligned: the error
+ *            word, read with gg_device_error.
+ */
+gg_status gg_gemm_mx4(const uint8_t* a_fp4, const uint8_t* sfa, int64_t m_rows, int32_t k,
+                      const uint8_t* b_fp4, const uint8_t* sfb, const int64_t* b_ptrs,
+                      const int64_t* sfb_ptrs, int32_t n, const int32_t* offsets, int32_t L,
+                      const float* alpha, const float* bias, void* d, gg_dtype d_dtype,
+                      uint32_t flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* A whole layer for a few tokens                                            */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace gg_moe_few needs (0 for arguments out of its ranges). */
+size_t gg_moe_few_workspace_size(int32_t tokens, int32_t top_k, int32_t hidden, int32_t inner);
+
+/*
+ * For up to 64 tokens, e = ids[t, j]:
+ *   h    = prob[t, j] * act(w1_e x[t] + bias1_e)
+ *   y[t] = sum_j (w2_e h + prob[t, j] * bias2_e)
+ * act as for gg_glu, on rows of w1 in 32-wide blocks of inputs and gates.  An
+ * id outside 0 .. num_experts-1 is no choice (its prob is not used); a token
+ * without any gives 0; an expert may be chosen twice by a token.  Products with
+ * fp32 accumulation; h is held as the sum of two bf16 values (16 bits) and the
+ * choices are added up in fp32 in the order of j, so equal calls give equal
+ * bits.  Only the chosen experts' weights are read.
+ *
+ * x          (tokens, hidden) bf16, row pitch ldx >= hidden, a multiple of 8.
+ * tokens     0 .. 64.  hidden, inner: multiples of 32, at most 2^16.
+ *            num_experts 1..1024, top_k 1..32.
+ * ids, prob  (tokens, top_k) int32 / float, as made by gg_route.
+ * w_dtype    GG_BF16: w1 (num_experts, 2 inner, hidden) and w2 (num_experts,
+ *            hidden, inner) row-major, sf1 and sf2 NULL; or GG_MXFP4: codes
+ *            (num_experts, 2 inner, hidden/2), (num_experts, hidden, inner/2)
+ *            and scales sf1 (num_experts, 2 inner, hidden/32), sf2 (num_experts,
+ *            hidden, inner/32).  A value past bf16's largest is an infinity.
+ * bias1      float (num_experts, 2 inner), or NULL;  bias2: float
+ *            (num_experts, hidden), or NULL.
+ * y          output (tokens, hidden), GG_BF16, GG_F16 or GG_F32, row pitch
+ *            ldy >= hidden; aligned to its element.
+ * x, w1, w2 16-byte, every other array 4-byte aligned (scales: any).
+ * act and its constants  as for gg_dglu_mx.  flags: 0 or GG_FLAG_GATE_FIRST.
+ * workspace  >= gg_moe_few_workspace_size(...) bytes, 256-B aligned.
+ */
+gg_status gg_moe_few(const void* x, int64_t ldx, int32_t tokens, int32_t hidden, const int32_t* ids,
+                     const float* prob, int32_t top_k, int32_t num_experts, const void* w1,
+                     const uint8_t* sf1, const float* bias1, const void* w2, const uint8_t* sf2,
+                     const float* bias2, gg_dtype w_dtype, int32_t inner, void* y, gg_dtype y_dtype,
+                     int64_t ldy, gg_act act, float geglu_alpha, float clamp_min, float clamp_max,
+                     float linear_offset, float situ_beta1, float situ_beta2, uint32_t flags,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgg_moe.so")
 
 # enums of gg_moe.h
-GG_BF16, GG_F16, GG_F32, GG_F8E4M3, GG_F8E5M2 = 0, 1, 2, 3, 4
+GG_BF16, GG_F16, GG_F32, GG_F8E4M3, GG_F8E5M2, GG_MXFP4 = 0, 1, 2, 3, 4, 5
 GG_MAJOR_K, GG_MAJOR_M, GG_MAJOR_N = 0, 1, 2
 GG_DSWIGLU, GG_DGEGLU, GG_DSITUGLU = 0, 1, 2
 GG_FLAG_GATE_FIRST, GG_FLAG_GEGLU_MASK_FILTER, GG_FLAG_VALIDATE_OFFSETS = 1, 2, 4
@@ -32,7 +32,9 @@ EXPORTS = ["gg_abi_version", "gg_last_error", "gg_device_error", "gg_wgrad_works
            "gg_wgrad", "gg_wgrad_noalloc", "gg_wgrad_mx", "gg_dglu_workspace_size", "gg_dglu", "gg_dglu_mx",
            "gg_dsrelu_workspace_size", "gg_dsrelu", "gg_route_workspace_size", "gg_route",
            "gg_route_bwd", "gg_plan_workspace_size", "gg_plan_max_rows", "gg_plan", "gg_permute",
-           "gg_combine", "gg_combine_bwd", "gg_grad_workspace_size", "gg_grad_norm", "gg_grad_clip"]
+           "gg_combine", "gg_combine_bwd", "gg_grad_workspace_size", "gg_grad_norm", "gg_grad_clip",
+           "gg_mx4_quant", "gg_mx4_dequant", "gg_glu", "gg_gemm_mx4_workspace_size", "gg_gemm_mx4",
+           "gg_moe_few_workspace_size", "gg_moe_few"]
 
 _TORCH_DTYPE = {torch.bfloat16: GG_BF16, torch.float16: GG_F16, torch.float32: GG_F32,
                 torch.float8_e4m3fn: GG_F8E4M3, torch.float8_e5m2: GG_F8E5M2}
@@ -110,6 +112,21 @@ def load_library(path=LIB_PATH):
     L.gg_grad_norm.argtypes = [P, P, P, I32, I64, P, I32, P, SZ, P]
     L.gg_grad_clip.restype = ctypes.c_int
     L.gg_grad_clip.argtypes = [P, P, P, I32, I64, P, F, F, P, P, P]
+    L.gg_mx4_quant.restype = ctypes.c_int
+    L.gg_mx4_quant.argtypes = [P, I32, I64, I64, I32, P, P, P, P]
+    L.gg_mx4_dequant.restype = ctypes.c_int
+    L.gg_mx4_dequant.argtypes = [P, P, I64, I32, P, I32, I64, P, P]
+    L.gg_glu.restype = ctypes.c_int
+    L.gg_glu.argtypes = [P, I32, I64, P, I64, I32, P, I32, I64, I32, F, F, F, F, F, F, U32, P, P]
+    L.gg_gemm_mx4_workspace_size.restype = SZ
+    L.gg_gemm_mx4_workspace_size.argtypes = []
+    L.gg_gemm_mx4.restype = ctypes.c_int
+    L.gg_gemm_mx4.argtypes = [P, P, I64, I32, P, P, P, P, I32, P, I32, P, P, P, I32, U32, P, SZ, P]
+    L.gg_moe_few_workspace_size.restype = SZ
+    L.gg_moe_few_workspace_size.argtypes = [I32, I32, I32, I32]
+    L.gg_moe_few.restype = ctypes.c_int
+    L.gg_moe_few.argtypes = [P, I64, I32, I32, P, P, I32, I32, P, P, P, P, P, P, I32, I32, P, I32, I64,
+                             I32, F, F, F, F, F, F, U32, P, SZ, P]
     _lib = L
     return L
 
@@ -583,3 +600,142 @@ def gg_grad_clip(ptrs, ends, dtypes, total, sumsq, max_norm, norm, eps=1e-6, out
     p_out = None if out_ptrs is None else _need(out_ptrs, "out_ptrs", (n,), torch.int64, dev)
     _check(L.gg_grad_clip(p_ptrs, p_ends, p_dt, n, total, p_sum, max_norm, eps, p_norm, p_out,
                           _raw_stream(stream, dev)))
+
+
+# --------------------------------------------------------------------------
+# the experts' forward pass: MXFP4, the gated activation, a few tokens' layer
+# --------------------------------------------------------------------------
+
+_CODES = (torch.uint8, torch.float4_e2m1fn_x2)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _need_one(t, what, shape, dtypes, dev):
+    """As _need, for any of the types."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse(t, what, shape, dtypes, dev, False)
+
+
+def _need_end(end, dev):
+    return None if end is None else _need(end, "end", (1,), _I32, dev)
+
+
+def gg_mx4_quant(x, codes, scales, end=None, stream=None):
+    """Rows to MXFP4 (gg_mx4_quant of gg_moe.h): x (rows, width) at any row
+    pitch; codes (rows, width / 2) and scales (rows, width / 32) are written,
+    uint8 (or float4_e2m1fn_x2 and float8_e8m0fnu).  end: int32 (1,), the rows
+    in use."""
+    L = load_library()
+    px, n, width, ld, dev = _need_rows(x, "x", _FLOATS)
+    p_codes = _need_one(codes, "codes", (n, width // 2), _CODES, dev)
+    p_scales = _need_one(scales, "scales", (n, width // 32), _SCALES, dev)
+    _check(L.gg_mx4_quant(px, _TORCH_DTYPE[x.dtype], ld, n, width, p_codes, p_scales, _need_end(end, dev),
+                          _raw_stream(stream, dev)))
+
+
+def gg_mx4_dequant(codes, scales, out, end=None, stream=None):
+    """The values of MXFP4 rows (gg_mx4_dequant of gg_moe.h): out (rows,
+    width) at any row pitch, arguments as for gg_mx4_quant."""
+    L = load_library()
+    po, n, width, ld, dev = _need_rows(out, "out", _FLOATS)
+    p_codes = _need_one(codes, "codes", (n, width // 2), _CODES, dev)
+    p_scales = _need_one(scales, "scales", (n, width // 32), _SCALES, dev)
+    _check(L.gg_mx4_dequant(p_codes, p_scales, n, width, po, _TORCH_DTYPE[out.dtype], ld, _need_end(end, dev),
+                            _raw_stream(stream, dev)))
+
+
+def gg_glu(c, y, prob=None, act=GG_DSWIGLU, geglu_alpha=1.702, clamp_min=-7.0, clamp_max=7.0,
+           linear_offset=1.0, situ_beta1=4.0, situ_beta2=25.0, flags=0, end=None, stream=None):
+    """The gated activation (gg_glu of gg_moe.h): c (rows, 2n) in 32-wide
+    blocks of inputs and gates to y (rows, n), both at any row pitch, times
+    prob (rows,) if given."""
+    L = load_library()
+    pc, rows, two_n, ldc, dev = _need_rows(c, "c", _FLOATS)
+    py, n, width, ldy, ydev = _need_rows(y, "y", _FLOATS)
+    if n != rows or 2 * width != two_n:
+        raise GGError(2, f"y has shape {tuple(y.shape)}, not {(rows, two_n // 2)}")
+    if ydev != dev:
+        _refuse(y, "y", y.shape, y.dtype, dev, True)
+    p_prob = None if prob is None else _need(prob, "prob", (rows,), _F32, dev)
+    _check(L.gg_glu(pc, _TORCH_DTYPE[c.dtype], ldc, p_prob, rows, width, py, _TORCH_DTYPE[y.dtype], ldy, act,
+                    geglu_alpha, clamp_min, clamp_max, linear_offset, situ_beta1, situ_beta2, flags,
+                    _need_end(end, dev), _raw_stream(stream, dev)))
+
+
+def gg_gemm_mx4_workspace_size():
+    return load_library().gg_gemm_mx4_workspace_size()
+
+
+def gg_gemm_mx4(a, sfa, b, sfb, offsets, d, alpha=None, bias=None, b_ptrs=None, sfb_ptrs=None, flags=0,
+                workspace=None, stream=None):
+    """The grouped product of MXFP4 rows and weights (gg_gemm_mx4 of
+    gg_moe.h): a (m_rows, k / 2) codes, sfa (m_rows, k / 32) scales; b (L, n,
+    k / 2), sfb (L, n, k / 32), or b = sfb = None and int64 (L,) addresses of
+    each expert's in b_ptrs, sfb_ptrs; offsets int32 (L,) group ends; d
+    (m_rows, n).  alpha float32 (L,), bias float32 (L, n).  Returns the
+    workspace used (gg_device_error reads its error word)."""
+    L = load_library()
+    pd, m, n, ld, dev = _need_rows(d, "d", _FLOATS)
+    if ld != n:
+        _refuse(d, "d", d.shape, d.dtype, dev, False)
+    k, E = 2 * _last(a), _extent(offsets, "offsets")
+    p_a = _need_one(a, "a", (m, k // 2), _CODES, dev)
+    p_sfa = _need_one(sfa, "sfa", (m, k // 32), _SCALES, dev)
+    p_b = None if b is None else _need_one(b, "b", (E, n, k // 2), _CODES, dev)
+    p_sfb = None if sfb is None else _need_one(sfb, "sfb", (E, n, k // 32), _SCALES, dev)
+    p_bp = None if b_ptrs is None else _need(b_ptrs, "b_ptrs", (E,), torch.int64, dev)
+    p_sp = None if sfb_ptrs is None else _need(sfb_ptrs, "sfb_ptrs", (E,), torch.int64, dev)
+    p_off = _need(offsets, "offsets", (E,), _I32, dev)
+    p_alpha = None if alpha is None else _need(alpha, "alpha", (E,), _F32, dev)
+    p_bias = None if bias is None else _need(bias, "bias", (E, n), _F32, dev)
+    p_ws, nbytes, ws = _scratch(workspace, L.gg_gemm_mx4_workspace_size, stream, dev)
+    _check(L.gg_gemm_mx4(p_a, p_sfa, m, k, p_b, p_sfb, p_bp, p_sp, n, p_off, E, p_alpha, p_bias, pd,
+                         _TORCH_DTYPE[d.dtype], flags, p_ws, nbytes, _raw_stream(stream, dev)))
+    return ws
+
+
+def gg_moe_few_workspace_size(tokens, top_k, hidden, inner):
+    return load_library().gg_moe_few_workspace_size(tokens, top_k, hidden, inner)
+
+
+def gg_moe_few(x, ids, prob, w1, w2, y, sf1=None, sf2=None, bias1=None, bias2=None, act=GG_DSWIGLU,
+               geglu_alpha=1.702, clamp_min=-7.0, clamp_max=7.0, linear_offset=1.0, situ_beta1=4.0,
+               situ_beta2=25.0, flags=0, workspace=None, stream=None):
+    """A whole layer for up to 64 tokens (gg_moe_few of gg_moe.h): x (T, H)
+    bf16 at any row pitch that is a multiple of 8; ids int32 and prob float32
+    (T, top_k); w1 (E, 2I, H) and w2 (E, H, I) bf16, or their MXFP4 codes
+    (E, 2I, H / 2), (E, H, I / 2) with scales sf1 (E, 2I, H / 32), sf2 (E, H,
+    I / 32); bias1 float32 (E, 2I), bias2 (E, H); y (T, H) at any row pitch.
+    Returns the workspace used."""
+    L = load_library()
+    px, T, H, ldx, dev = _need_rows(x, "x", (torch.bfloat16,))
+    py, Ty, Hy, ldy, ydev = _need_rows(y, "y", _FLOATS)
+    if (Ty, Hy) != (T, H):
+        raise GGError(2, f"y has shape {tuple(y.shape)}, not {(T, H)}")
+    if ydev != dev:
+        _refuse(y, "y", y.shape, y.dtype, dev, True)
+    if w1.dim() != 3:
+        raise GGError(2, f"w1 has shape {tuple(w1.shape)}, not three dimensions")
+    k, E, I = _last(ids), w1.shape[0], w1.shape[1] // 2
+    mx4 = w1.dtype is not torch.bfloat16
+    per, types = (2, _CODES) if mx4 else (1, (torch.bfloat16,))
+    p_ids = _need(ids, "ids", (T, k), _I32, dev)
+    p_prob = _need(prob, "prob", (T, k), _F32, dev)
+    p_w1 = _need_one(w1, "w1", (E, 2 * I, H // per), types, dev)
+    p_w2 = _need_one(w2, "w2", (E, H, I // per), types, dev)
+    p_sf1 = None if sf1 is None else _need_one(sf1, "sf1", (E, 2 * I, H // 32), _SCALES, dev)
+    p_sf2 = None if sf2 is None else _need_one(sf2, "sf2", (E, H, I // 32), _SCALES, dev)
+    p_b1 = None if bias1 is None else _need(bias1, "bias1", (E, 2 * I), _F32, dev)
+    p_b2 = None if bias2 is None else _need(bias2, "bias2", (E, H), _F32, dev)
+    p_ws, nbytes, ws = _scratch(workspace, _few_bytes, stream, dev, T, k, H, I)
+    _check(L.gg_moe_few(px, ldx, T, H, p_ids, p_prob, k, E, p_w1, p_sf1, p_b1, p_w2, p_sf2, p_b2,
+                        GG_MXFP4 if mx4 else GG_BF16, I, py, _TORCH_DTYPE[y.dtype], ldy, act, geglu_alpha,
+                        clamp_min, clamp_max, linear_offset, situ_beta1, situ_beta2, flags, p_ws, nbytes,
+                        _raw_stream(stream, dev)))
+    return ws
+
+
+def _few_bytes(*of):
+    # (at least the header, so that the call itself refuses what is out of range)
+    return max(256, gg_moe_few_workspace_size(*of))

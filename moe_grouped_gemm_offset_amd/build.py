@@ -22,7 +22,8 @@ PEAK_SOURCE = ("gg_peak.hip", "gg_peak", [])
 SOURCES = [(f, os.path.splitext(f)[0], []) for f in
            ("gg_api.cpp", "gg_prologue.hip", "gg_wgrad.hip", "gg_wgrad_mx.hip", "gg_dglu.hip",
             "gg_dglu_mx.hip", "gg_dsrelu.hip", "gg_api_moe.cpp", "gg_route.hip", "gg_dispatch.hip",
-            "gg_clip.hip")]
+            "gg_clip.hip", "gg_api_forward.cpp", "gg_mx4.hip", "gg_glu.hip", "gg_gemm_mx4.hip",
+            "gg_moe_few.hip")]
 SOURCES += [("gg_dglu_mx_inst.hip", f"gg_dglu_mx_a{act}{'k' if bk else 'n'}",
              [f"-DGG_ACT={act}", f"-DGG_BK={bk}"]) for act in range(3) for bk in (1, 0)]
 SOURCES += [("gg_dsrelu_inst.hip", f"gg_dsrelu_{'k' if bk else 'n'}", [f"-DGG_BK={bk}"])

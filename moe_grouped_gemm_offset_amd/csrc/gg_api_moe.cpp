@@ -19,12 +19,8 @@ constexpr int64_t kMaxTokens = 1 << 23;
 constexpr int32_t kMaxTopK = 32;
 constexpr int32_t kMaxWidth = 1 << 20;
 
-size_t size_of(gg_dtype d) { return d == GG_F32 ? 4 : d == GG_BF16 || d == GG_F16 ? 2 : 1; }
-
 // Rows that a plan's groups are padded to.
 bool is_granule(int32_t g) { return g >= 1 && g <= 256 && (g & (g - 1)) == 0; }
-
-bool off(const void* p, size_t align) { return ((uintptr_t)p & (align - 1)) != 0; }
 
 gg_status check_tokens(int64_t tokens, int32_t num_experts, int32_t top_k) {
     if (num_experts < 1 || num_experts > 1024)
@@ -33,16 +29,6 @@ gg_status check_tokens(int64_t tokens, int32_t num_experts, int32_t top_k) {
         return fail(GG_ERR_SHAPE, "tokens must be >= 0 and top_k >= 1");
     if (tokens > kMaxTokens || top_k > kMaxTopK)
         return fail(GG_ERR_UNSUPPORTED, "tokens is limited to 2^23 and top_k to 32");
-    return GG_OK;
-}
-
-gg_status check_workspace(const void* workspace, size_t bytes, size_t need) {
-    if (!workspace)
-        return fail(GG_ERR_NULL, "workspace must be non-NULL");
-    if (off(workspace, 256))
-        return fail(GG_ERR_ALIGN, "workspace must be 256-byte aligned");
-    if (bytes < need)
-        return fail(GG_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", bytes, need);
     return GG_OK;
 }
 
@@ -83,29 +69,6 @@ gg_status check_rows(int64_t tokens, int32_t width, int32_t top_k, int64_t m_row
     if (ld < width || ld > INT32_MAX)
         return fail(GG_ERR_LAYOUT, "%s must be in width .. 2^31-1 (got %lld)", pitch, (long long)ld);
     return GG_OK;
-}
-
-void report(const char* op, const LaunchInfo& info, int64_t rows, int64_t cols) {
-    char shape[96];
-    snprintf(shape, sizeof shape, "(%lld x %lld)", (long long)rows, (long long)cols);
-    if (info.grid > 0)
-        log_launch(op, info, shape);
-}
-
-// What every entry does last: the device check, the launch, the report.
-template <class Launch>
-gg_status go(const char* op, int64_t rows, int64_t cols, Launch launch) {
-    gg_status st = check_device();
-    if (st != GG_OK)
-        return st;
-    LaunchInfo info{};
-    LaunchInfo* li = log_enabled() ? &info : nullptr;
-    const hipError_t e = launch(li);
-    if (e != hipSuccess)
-        return hip_fail(e, op);
-    if (li)
-        report(op, info, rows, cols);
-    return ok();
 }
 
 }  // namespace

@@ -1,0 +1,83 @@
+// gg_glu.hip -- the gated activation over rows of 32-wide input and gate blocks
+// (gg_glu): y = prob act(g, u).
+//
+// Bound by memory: three elements moved for some 15 vector instructions an
+// output (SwiGLU).
+#include <type_traits>
+
+#include "gg_act.hpp"
+
+namespace gg {
+
+namespace {
+
+template <int CDT, int YDT, int ACT>
+__global__ void __launch_bounds__(kRowThreads) glu_kernel(GluArgs p, Eights e) {
+    typedef typename Elem<CDT>::T C;
+    typedef typename Elem<YDT>::T Y;
+    const C* const c = (const C*)p.c;
+    Y* const y = (Y*)p.y;
+    const int gate = p.act.gate_first ? 0 : 32, input = 32 - gate;
+    for_eights(e, p.end, [&](const int64_t (&row)[kUnroll], const uint32_t (&col)[kUnroll],
+                             const int64_t (&v)[kUnroll], const bool (&live)[kUnroll]) {
+        Eight<CDT> u[kUnroll], g[kUnroll];
+        float w[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; i++) {
+            const C* const at = c + row[i] * p.ldc + ((col[i] & ~31u) * 2 + (col[i] & 31u));
+            u[i].load(at + input);
+            g[i].load(at + gate);
+            w[i] = p.prob ? p.prob[row[i]] : 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; i++) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                f[j] = act_forward<ACT>(g[i].get(j), u[i].get(j), p.act) * w[i];
+            Eight<YDT> o;
+            o.set(f);
+            if (live[i])
+                o.store(y + row[i] * p.ldy + col[i]);
+        }
+    });
+}
+
+template <class F>
+void for_float(int dtype, F f) {
+    if (dtype == GG_BF16)
+        f(std::integral_constant<int, GG_BF16>());
+    else if (dtype == GG_F16)
+        f(std::integral_constant<int, GG_F16>());
+    else
+        f(std::integral_constant<int, GG_F32>());
+}
+
+}  // namespace
+
+hipError_t launch_glu(const GluArgs& p, int c_dtype, int y_dtype, hipStream_t s, LaunchInfo* info) {
+    const Eights e = eights_of(p.rows, p.n);
+    const unsigned grid = eights_grid(e);
+    if (grid == 0)
+        return hipSuccess;
+    if (info) {
+        static const char* const kActs[] = {"SwiGLU", "GeGLU", "SiTU-GLU"};
+        snprintf(info->kernel, sizeof info->kernel, "glu_kernel<%s, C %s, Y %s>", kActs[p.act.act],
+                 dtype_name(c_dtype), dtype_name(y_dtype));
+        info->tm = kRowStep;
+        info->tn = 8;
+        info->waves = kRowThreads / 64;
+        info->grid = grid;
+    }
+    for_float(c_dtype, [&](auto CDT) {
+        for_float(y_dtype, [&](auto YDT) {
+            for_act(p.act.act, [&](auto ACT) {
+                hipLaunchKernelGGL((glu_kernel<decltype(CDT)::value, decltype(YDT)::value, decltype(ACT)::value>),
+                                   dim3(grid), dim3(kRowThreads), 0, s, p, e);
+            });
+        });
+    });
+    return hipGetLastError();
+}
+
+}  // namespace gg

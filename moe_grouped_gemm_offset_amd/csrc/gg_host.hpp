@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <cstdio>
+
 #include "gg_internal.hpp"
 #include "gg_moe.h"
 
@@ -26,5 +28,40 @@ inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline bool is_out_dtype(gg_dtype d) { return d == GG_BF16 || d == GG_F16 || d == GG_F32; }
 inline bool is_fp8(gg_dtype d) { return d == GG_F8E4M3 || d == GG_F8E5M2; }
+inline size_t size_of(gg_dtype d) { return d == GG_F32 ? 4 : d == GG_BF16 || d == GG_F16 ? 2 : 1; }
+inline bool off(const void* p, size_t align) { return ((uintptr_t)p & (align - 1)) != 0; }
+
+inline gg_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (!workspace)
+        return fail(GG_ERR_NULL, "workspace must be non-NULL");
+    if (off(workspace, 256))
+        return fail(GG_ERR_ALIGN, "workspace must be 256-byte aligned");
+    if (bytes < need)
+        return fail(GG_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", bytes, need);
+    return GG_OK;
+}
+
+inline void report(const char* op, const LaunchInfo& info, int64_t rows, int64_t cols) {
+    char shape[96];
+    snprintf(shape, sizeof shape, "(%lld x %lld)", (long long)rows, (long long)cols);
+    if (info.grid > 0)
+        log_launch(op, info, shape);
+}
+
+// What every entry does last: the device check, the launch, the report.
+template <class Launch>
+gg_status go(const char* op, int64_t rows, int64_t cols, Launch launch) {
+    gg_status st = check_device();
+    if (st != GG_OK)
+        return st;
+    LaunchInfo info{};
+    LaunchInfo* li = log_enabled() ? &info : nullptr;
+    const hipError_t e = launch(li);
+    if (e != hipSuccess)
+        return hip_fail(e, op);
+    if (li)
+        report(op, info, rows, cols);
+    return ok();
+}
 
 }  // namespace gg

@@ -132,8 +132,8 @@ struct DsreluArgs {
 // Launchers (return the HIP status of the launch).
 // Name of a gg_dtype code, for diagnostics.
 inline const char* dtype_name(int d) {
-    static const char* const kNames[] = {"bf16", "fp16", "fp32", "e4m3", "e5m2"};
-    return d >= 0 && d < 5 ? kNames[d] : "?";
+    static const char* const kNames[] = {"bf16", "fp16", "fp32", "e4m3", "e5m2", "mxfp4"};
+    return d >= 0 && d < 6 ? kNames[d] : "?";
 }
 
 // What a launcher chose (reported when GG_LOG is set): the kernel and its

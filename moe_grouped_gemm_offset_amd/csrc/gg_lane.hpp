@@ -101,6 +101,23 @@ struct Vec {
     }
 };
 
+// ---- exponentials ----------------------------------------------------------
+// The hardware's, of a log2(e) rounded to fp32, is off by up to |a| 2^-24 of
+// itself: FULL brings back what that rounding left out, as a - t ln(2) with
+// ln(2) in two parts, and is good to 2 units of 2^-24.
+
+// exp(a) of a <= 0: 0 far below the normal numbers, a NaN kept.
+template <bool FULL>
+__device__ __forceinline__ float exp_below(float a) {
+    if constexpr (!FULL)
+        return __expf(a);
+    a = __builtin_elementwise_maximum(a, -110.0f);
+    const float t = a * 1.44269504f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float rest = fmaf(t, 1.90465421e-9f, fmaf(t, -0.693147182f, a));
+    return fmaf(e, rest, e);
+}
+
 // ---- lanes -----------------------------------------------------------------
 
 template <int CTRL>

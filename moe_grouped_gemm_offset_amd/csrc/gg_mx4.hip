@@ -1,0 +1,122 @@
+// gg_mx4.hip -- rows to MXFP4 and back (gg_mx4_quant, gg_mx4_dequant).
+//
+// Four lanes hold a block of 32 values, eight each.  The largest magnitude is
+// found on the bit patterns (ordered like the magnitudes, with infinities and
+// NaNs on top), so the scale is exact: with the largest = (1 + f) 2^E and
+// 6 = 1.5 * 2^2, the smallest e with 6 * 2^e >= largest is E - 2, or E - 1
+// where f > 1/2.  The conversion instruction divides by 2^e, rounds to nearest
+// even and packs; the division is exact, so this is the only rounding.
+#include <type_traits>
+
+#include "gg_act.hpp"
+
+namespace gg {
+
+namespace {
+
+typedef uint32_t Word __attribute__((aligned(1)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) quant_kernel(QuantArgs p, Eights e) {
+    typedef typename Elem<DT>::T T;
+    const T* const x = (const T*)p.x;
+    for_eights(e, p.end, [&](const int64_t (&row)[kUnroll], const uint32_t (&col)[kUnroll],
+                             const int64_t (&v)[kUnroll], const bool (&live)[kUnroll]) {
+        Eight<DT> in[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++)
+            in[u].load(x + row[u] * p.ld + col[u]);
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint32_t a = __builtin_bit_cast(uint32_t, in[u].get(i)) & 0x7FFFFFFFu;
+                top = a > top ? a : top;
+            }
+            top = group_all<4>(top, OpMaxU());
+            const bool odd = top >= 0x7F800000u;         // an infinity or a NaN
+            // the exponent field, one more where f > 1/2, less 2
+            const uint32_t up = (top + 0x3FFFFFu) >> 23;
+            const uint32_t s = odd ? 255u : (up > 2u ? up - 2u : 0u);
+            const float scale = __builtin_bit_cast(float, s << 23);
+            uint32_t c = 0;
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(0), in[u].get(1), scale, 0);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(2), in[u].get(3), scale, 1);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(4), in[u].get(5), scale, 2);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(6), in[u].get(7), scale, 3);
+            if (live[u]) {
+                *(Word*)(p.codes + v[u] * 4) = odd ? 0u : c;
+                if ((threadIdx.x & 3) == 0)
+                    p.scales[v[u] >> 2] = (uint8_t)s;
+            }
+        }
+    });
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) dequant_kernel(QuantArgs p, Eights e) {
+    typedef typename Elem<DT>::T T;
+    T* const out = (T*)p.x;
+    for_eights(e, p.end, [&](const int64_t (&row)[kUnroll], const uint32_t (&col)[kUnroll],
+                             const int64_t (&v)[kUnroll], const bool (&live)[kUnroll]) {
+        uint32_t c[kUnroll], s[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+            c[u] = *(const Word*)(p.codes + v[u] * 4);
+            s[u] = p.scales[v[u] >> 2];
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+            const float scale = __builtin_bit_cast(float, s[u] << 23);
+            const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], scale, 0);
+            const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], scale, 1);
+            const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], scale, 2);
+            const f32x2 g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], scale, 3);
+            const float f[8] = {a[0], a[1], b[0], b[1], d[0], d[1], g[0], g[1]};
+            Eight<DT> o;
+            o.set(f);
+            if (live[u])
+                o.store(out + row[u] * p.ld + col[u]);
+        }
+    });
+}
+
+template <class Launch>
+hipError_t by_dtype(const char* name, const QuantArgs& p, int dtype, LaunchInfo* info, Launch launch) {
+    const Eights e = eights_of(p.rows, p.width);
+    const unsigned grid = eights_grid(e);
+    if (grid == 0)
+        return hipSuccess;
+    if (info) {
+        snprintf(info->kernel, sizeof info->kernel, "%s<%s>", name, dtype_name(dtype));
+        info->tm = kRowStep;
+        info->tn = 8;
+        info->waves = kRowThreads / 64;
+        info->grid = grid;
+    }
+    if (dtype == GG_BF16)
+        launch(std::integral_constant<int, GG_BF16>(), e, grid);
+    else if (dtype == GG_F16)
+        launch(std::integral_constant<int, GG_F16>(), e, grid);
+    else
+        launch(std::integral_constant<int, GG_F32>(), e, grid);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
+    return by_dtype("quant_kernel", p, dtype, info, [&](auto DT, const Eights& e, unsigned grid) {
+        hipLaunchKernelGGL((quant_kernel<decltype(DT)::value>), dim3(grid), dim3(kRowThreads), 0, s, p, e);
+    });
+}
+
+hipError_t launch_dequant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
+    return by_dtype("dequant_kernel", p, dtype, info, [&](auto DT, const Eights& e, unsigned grid) {
+        hipLaunchKernelGGL((dequant_kernel<decltype(DT)::value>), dim3(grid), dim3(kRowThreads), 0, s, p, e);
+    });
+}
+
+}  // namespace gg

@@ -35,27 +35,13 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr float kTiny = 1e-20f;          // added to sums of sigmoids, which can underflow
 
-// Exponentials.  The hardware's, of a log2(e) rounded to fp32, is off by up to
-// |a| 2^-24 of itself: FULL brings back what that rounding left out, as a - t
-// ln(2) with ln(2) in two parts, and is good to 2 units of 2^-24.  It is used
-// where a caller sees the exponential itself, the weights and fp32 gradients
+// exp_below<FULL> is used where a caller sees the exponential itself, the weights
+// and fp32 gradients
 // (weights at logits of -25 to -45: off by 5 units at most for 44).  Without it are
 // the sums over all experts, whose large terms have small arguments, the loss,
 // which is a mean over them, and gradients that are rounded to 16 bits: there
 // it would cost route_kernel 20.1 -> 24.6 us and route_bwd_kernel 19.0 -> 20.1
 // (65536 x 256 bf16).
-
-// exp(a) of a <= 0: 0 far below the normal numbers, a NaN kept.
-template <bool FULL>
-__device__ __forceinline__ float exp_below(float a) {
-    if constexpr (!FULL)
-        return __expf(a);
-    a = __builtin_elementwise_maximum(a, -110.0f);
-    const float t = a * 1.44269504f;
-    const float e = __builtin_amdgcn_exp2f(t);
-    const float rest = fmaf(t, 1.90465421e-9f, fmaf(t, -0.693147182f, a));
-    return fmaf(e, rest, e);
-}
 
 // sigmoid(-|x|), at most 1/2, with x's sign.  A sigmoid and its slope come out
 // of it without 1 minus what rounds to 1: sigmoid(x) is the tail t or 1 - t,

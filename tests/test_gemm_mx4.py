@@ -1,0 +1,217 @@
+"""gg_gemm_mx4 against the product in 64 bits (GPU), and its refusals (CPU).
+
+Most cases are exact: codes are multiples of 1/2 up to 6 and scales 2^-1 .. 2^1,
+so a product is a multiple of 2^-4 up to 144, and any partial sum of at most
+4096 of them has 20 + 4 = 24 bits: fp32 holds it whatever the order.  With alpha
+a power of two and the bias a multiple of 2^-4 below 2^10 times it, the result is
+exact too, and only rounded to its type."""
+import pytest
+import torch
+
+from moe_grouped_gemm_offset_amd import binding as B
+from tests import mx4_util as mx
+from tests.parity_util import say
+
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+P = 1 << 20
+
+
+def case(sizes, K, N, seed=0, tail=0, bias=False, lo=126, hi=128):
+    g = torch.Generator().manual_seed(seed)
+    L, m = len(sizes), sum(sizes) + tail
+    s = dict(K=K, N=N, sizes=sizes, m=m)
+    s["a"], s["sfa"] = mx.random_mx4(g, (m, K), lo, hi)
+    s["b"], s["sfb"] = mx.random_mx4(g, (L, N, K), lo, hi)
+    s["ends"] = torch.tensor(sizes, dtype=torch.int64).cumsum(0).to(torch.int32)
+    s["alpha"] = torch.exp2(torch.randint(-2, 3, (L,), generator=g).float())
+    s["bias"] = torch.randint(-4000, 4000, (L, N), generator=g).float() / 16 * s["alpha"][:, None] if bias else None
+    return s
+
+
+def want(s, ends=None):
+    """(float64 result, float64 sum of magnitudes), 0 behind the last group."""
+    d, mag = torch.zeros(s["m"], s["N"], dtype=torch.float64), torch.zeros(s["m"], s["N"], dtype=torch.float64)
+    a, at = mx.values(s["a"], s["sfa"]), 0
+    for e, end in enumerate((s["ends"] if ends is None else ends).tolist()):
+        end = max(at, min(end, s["m"]))
+        if end > at:
+            b = mx.values(s["b"][e], s["sfb"][e])
+            al = 1.0 if s["alpha"] is None else float(s["alpha"][e])
+            d[at:end] = al * (a[at:end] @ b.T) + (0 if s["bias"] is None else s["bias"][e].double())
+            mag[at:end] = al * (a[at:end].abs() @ b.abs().T) + (0 if s["bias"] is None else s["bias"][e].abs().double())
+        at = end
+    return d, mag, at
+
+
+def run(s, dtype=torch.float32, ends=None, ptrs=False, fill=77.0, **kw):
+    dev = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in s.items()}
+    d = torch.full((s["m"], s["N"]), fill, dtype=dtype, device="cuda")
+    kw.setdefault("workspace", torch.full((256,), 255, dtype=torch.uint8, device="cuda"))
+    b, sfb = dev["b"], dev["sfb"]
+    if ptrs:
+        parts = [(x.clone(), y.clone()) for x, y in zip(b, sfb)]
+        kw["b_ptrs"] = torch.tensor([x.data_ptr() for x, _ in parts], dtype=torch.int64, device="cuda")
+        kw["sfb_ptrs"] = torch.tensor([y.data_ptr() for _, y in parts], dtype=torch.int64, device="cuda")
+        b = sfb = None
+    ws = B.gg_gemm_mx4(dev["a"], dev["sfa"], b, sfb, dev["ends"] if ends is None else ends.cuda(), d, alpha=dev["alpha"],
+                       bias=dev["bias"], **kw)
+    err = B.gg_device_error(ws)
+    return d.cpu(), err
+
+
+def check_exact(s, d, dtype, ends=None, fill=77.0):
+    w, _, last = want(s, ends)
+    assert torch.equal(d[:last].double(), w[:last].float().to(dtype).double())
+    assert (d[last:] == fill).all()
+
+
+# few rows a group (16 or 64 to a tile) and many, K of one stage to several
+# groups of scales with an odd number of stages among them, N off the tiles
+SHAPES = [([1], 128, 32), ([5], 256, 64), ([0, 3, 0], 384, 96), ([16, 1, 17, 0, 2], 640, 160),
+          ([33, 64, 65, 1], 1152, 224), ([0, 0], 128, 64), ([40] * 5, 2176, 320), ([1] * 200, 256, 64),
+          ([300], 128, 32), ([257, 0, 255], 256, 288), ([130, 513, 90], 384, 256), ([600], 640, 544),
+          ([256, 256], 1024, 512), ([1000, 1, 0, 250], 1920, 288), ([700], 4096, 256)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes,K,N", SHAPES, ids=lambda v: str(v)[:24].replace(" ", ""))
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_exact(sizes, K, N, dtype):
+    i = SHAPES.index((sizes, K, N))
+    say("gemm_mx4", sizes[:6], K, N, dtype)
+    s = case(sizes, K, N, seed=i, tail=(0, 3, 40)[i % 3], bias=i % 2 == 0)
+    if i % 4 == 3:
+        s["alpha"] = None
+    if dtype == torch.float16:                               # (within fp16's range)
+        s["sfb"] = s["sfb"] - 6
+        if s["bias"] is not None:
+            s["bias"] = s["bias"] / 64
+    d, err = run(s, dtype, ptrs=i % 3 == 1)
+    assert err == 0
+    check_exact(s, d, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,rows", [(65, 3), (700, 5), (1024, 1), (130, 100)])
+def test_many_groups(L, rows):
+    """More groups than lanes, some empty; thin and tiled."""
+    sizes = [(i * 7 % 5) * rows for i in range(L)]
+    s = case(sizes, 128, 32, seed=L, tail=9)
+    d, err = run(s)
+    assert err == 0
+    check_exact(s, d, torch.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("per", [4, 40, 300])
+def test_random_scales(per):
+    """Scales of any size, fp32: off by at most a rounding of each of K + 2
+    additions, (K + 2) 2^-24 of the sum of the magnitudes."""
+    K = 1408
+    s = case([per, 2 * per, 0, per // 2], K, 288, seed=per, bias=True, lo=97, hi=157)
+    d, err = run(s)
+    w, mag, last = want(s)
+    tol = (K + 2) * 2.0 ** -24 * mag[:last]
+    assert err == 0 and ((d[:last].double() - w[:last]).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("per,K", [(4, 384), (40, 384), (300, 384), (300, 512), (4, 128)])
+def test_nan_scales_stay_in_their_rows(per, K):
+    """A scale of 255 makes NaN of its row of d (A) or column (B), of nothing
+    else; also in the first scale of the row behind an odd number of stages."""
+    s = case([per, per], K, 96, seed=1)
+    s["sfa"][1::3, 0] = 255
+    s["sfa"][2::6, -1] = 255
+    s["sfb"][1, 5::8, 0] = 255
+    d, _ = run(s)
+    w, _, last = want(s)
+    assert torch.equal(torch.isnan(d), torch.isnan(w))
+    ok = ~torch.isnan(w)
+    assert torch.equal(d[ok].double(), w[ok])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("per", [6, 40, 300])
+def test_malformed_ends(per):
+    """Ends that fall, are negative or lie past m_rows: flagged, groups by the
+    running maximum, nothing written outside them."""
+    s = case([per, per, per, per], 256, 96, seed=2, tail=5)
+    for ends, flag in [([per, per // 2, 2 * per, 3 * per], 1), ([-4, per, per, 2 * per], 1),
+                       ([per, 2 * per, 4 * per + 6, 4 * per + 6], 4), ([2 ** 31 - 1, -2 ** 31, 0, 5], 5)]:
+        ends = torch.tensor(ends, dtype=torch.int32)
+        d, err = run(s, ends=ends)
+        assert err == flag
+        top = torch.cummax(ends.clamp(0, s["m"]), 0).values
+        check_exact(s, d, torch.float32, ends=top)
+    d, err = run(s)                                          # the word is cleared
+    assert err == 0
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    s = case([0, 0, 0], 128, 32)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    d, err = run(s, workspace=ws)
+    assert err == 0 and d.numel() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [70000, 140])
+def test_past_4_gib(rows):
+    """d past 2^32 bytes (tiled), weights past them (thin)."""
+    if rows == 70000:
+        N, L, K = 32768, 1, 128
+    else:
+        N, L, K = 32768, 68, 4096
+    g = torch.Generator().manual_seed(0)
+    a, sfa = mx.random_mx4(g, (rows, K))
+    b = torch.zeros(L, N, K // 2, dtype=torch.uint8, device="cuda")
+    sfb = torch.full((L, N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    bc, bs = mx.random_mx4(g, (N, K))
+    b[-1], sfb[-1] = bc.cuda(), bs.cuda()
+    ends = torch.zeros(L, dtype=torch.int32)
+    ends[-1] = rows
+    d = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    B.gg_gemm_mx4(a.cuda(), sfa.cuda(), b, sfb, ends.cuda(), d)
+    pick = torch.tensor([0, rows // 2, rows - 2, rows - 1])
+    w = mx.values(a[pick], sfa[pick]) @ mx.values(bc, bs).T
+    assert torch.equal(d[pick.cuda()].cpu().double(), w.float().bfloat16().double())
+
+
+# --------------------------------------------------------------------------
+# refusals (CPU)
+# --------------------------------------------------------------------------
+
+def c_gemm(**kw):
+    a = dict(a=P, sfa=P, m=64, k=256, b=P, sfb=P, bp=None, sp=None, n=64, off=P, L=2, alpha=None, bias=None, d=P,
+             dt=B.GG_BF16, flags=0, ws=P, nb=256)
+    a.update(kw)
+    return B.load_library().gg_gemm_mx4(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dt=B.GG_F8E4M3), 3), (dict(L=0), 2), (dict(L=1025), 2), (dict(m=-1), 2), (dict(m=1 << 31), 2), (dict(k=64), 2),
+    (dict(k=192), 2), (dict(n=48), 2), (dict(n=0), 2), (dict(k=(1 << 21) + 128), 8), (dict(n=(1 << 21) + 32), 8),
+    (dict(bp=P, sp=P), 6), (dict(b=None, sfb=None), 6), (dict(sfb=None), 1), (dict(b=None, sfb=None, bp=P), 1),
+    (dict(off=None), 1), (dict(a=None), 1), (dict(sfa=None), 1), (dict(d=None), 1), (dict(a=P + 8), 5), (dict(b=P + 8), 5),
+    (dict(d=P + 8), 5), (dict(sfa=P + 2), 5), (dict(sfb=P + 1), 5), (dict(off=P + 2), 5), (dict(alpha=P + 2), 5),
+    (dict(bias=P + 1), 5), (dict(b=None, sfb=None, bp=P + 4, sp=P), 5), (dict(flags=4), 6), (dict(ws=None), 1),
+    (dict(ws=P + 128), 5), (dict(nb=255), 7), (dict(m=(1 << 31) - 1, n=1 << 21), 8)])
+def test_refused(kw, status):
+    assert c_gemm(**kw) == status
+    assert B.gg_last_error()
+
+
+def test_binding_refuses():
+    u8 = dict(dtype=torch.uint8)
+    good = dict(a=torch.zeros(4, 64, **u8), sfa=torch.zeros(4, 4, **u8), b=torch.zeros(2, 32, 64, **u8),
+                sfb=torch.zeros(2, 32, 4, **u8), offsets=torch.zeros(2, dtype=torch.int32), d=torch.zeros(4, 32))
+    for bad in [dict(a=good["a"].float()), dict(sfa=good["sfa"][:3]), dict(b=good["b"][:1]), dict(b=good["b"][0]),
+                dict(sfb=good["sfb"].transpose(1, 2)), dict(offsets=good["offsets"].long()),
+                dict(offsets=good["offsets"][None]), dict(d=torch.zeros(4, 40)[:, :32]), dict(d=torch.zeros(3, 32)),
+                dict(alpha=torch.ones(3)), dict(bias=torch.zeros(2, 31)), dict(b_ptrs=torch.zeros(2)), {}]:
+        a = dict(good)
+        a.update(bad)
+        with pytest.raises(B.GGError):
+            B.gg_gemm_mx4(**a)
