@@ -205,8 +205,8 @@ gg_status gg_moe_few(const void* x, int64_t ldx, int32_t tokens, int32_t hidden,
         return fail(GG_ERR_SHAPE, "hidden and inner must be positive multiples of 32 (got %d, %d)", hidden, inner);
     if (tokens > kFewTokens || top_k > kFewTopK || hidden > kFewWidth || inner > kFewWidth)
         return fail(GG_ERR_UNSUPPORTED, "tokens is limited to 64, top_k to 32, hidden and inner to 2^16");
-    if (ldx < hidden || ldx % 8 != 0 || ldx > (1 << 24) || ldy < hidden || ldy > INT32_MAX)
-        return fail(GG_ERR_LAYOUT, "ldx must be a multiple of 8 in hidden .. 2^24, ldy in hidden .. 2^31-1");
+    if (ldx < hidden || ldx % 8 != 0 || ldx > (1 << 23) || ldy < hidden || ldy > INT32_MAX)
+        return fail(GG_ERR_LAYOUT, "ldx must be a multiple of 8 in hidden .. 2^23, ldy in hidden .. 2^31-1");
     const bool mx4 = w_dtype == GG_MXFP4;
     if (((!x || !ids || !prob || !y) && tokens > 0) || !w1 || !w2 || (mx4 && (!sf1 || !sf2)))
         return fail(GG_ERR_NULL, "x, ids, prob, w1, w2, y (and the scales of MXFP4) must be non-NULL");

@@ -65,6 +65,8 @@ struct FewArgs {
     const float* bias2;       // (E, H) or null
     void* y;                  // (T, H), row pitch ldy
     int y_dtype, mx4;
+    int parts;                // bf16 values that hold an h
+    uint32_t k_magic;         // i * k_magic >> 16 = i / k
     ActArgs act;
     char* ws;
 };
