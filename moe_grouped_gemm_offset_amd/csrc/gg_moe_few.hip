@@ -58,27 +58,33 @@ struct Choices {
     // choice of an expert has them all; with more it stands for expert a.
     static __device__ __forceinline__ bool by_pair(const FewArgs& p) { return p.T * p.k <= p.E; }
 
-    static constexpr int kAtOnce = 8;
-    __device__ __forceinline__ void load(const FewArgs& p, int at, int (&id)[kAtOnce]) const {
-#pragma unroll
-        for (int c = 0; c < kAtOnce; c++)
-            if (at + 64 * c < p.T * p.k)
-                id[c] = p.ids[min(at + 64 * c + (int)(threadIdx.x & 63), p.T * p.k - 1)];
+    __device__ __forceinline__ void add(const FewArgs& p, int at, int id, int e) {
+        const int i = at + (int)(threadIdx.x & 63);
+        const bool hit = i < p.T * p.k && id == e;
+        const uint64_t m = __ballot(hit);
+        if (hit)                                       // (i / k by a reciprocal, exact below 2^11)
+            list[n + __popcll(m & ((1ull << (threadIdx.x & 63)) - 1))] = (uint32_t)i * p.k_magic >> 16 << 16 | i;
+        if (first < 0 && m)
+            first = at + __ffsll((unsigned long long)m) - 1;
+        n += __popcll(m);
     }
-    __device__ __forceinline__ void add(const FewArgs& p, int at, const int (&id)[kAtOnce], int e) {
-        const int lane = threadIdx.x & 63, pairs = p.T * p.k;
+    __device__ __forceinline__ void collect(const FewArgs& p, int e) {
+        constexpr int kAtOnce = 8;
+        const int pairs = p.T * p.k, lane = threadIdx.x & 63;
+        if (pairs <= 64) {
+            add(p, 0, p.ids[min(lane, pairs - 1)], e);
+        } else {
+            for (int at = 0; at < pairs; at += 64 * kAtOnce) {
+                int id[kAtOnce];
 #pragma unroll
-        for (int c = 0; c < kAtOnce; c++)
-            if (at + 64 * c < pairs) {
-                const int i = at + 64 * c + lane;
-                const bool hit = i < pairs && id[c] == e;
-                const uint64_t m = __ballot(hit);
-                if (hit)                               // (i / k by a reciprocal, exact below 2^11)
-                    list[n + __popcll(m & ((1ull << lane) - 1))] = (uint32_t)i * p.k_magic >> 16 << 16 | i;
-                if (first < 0 && m)
-                    first = at + 64 * c + __ffsll((unsigned long long)m) - 1;
-                n += __popcll(m);
+                for (int c = 0; c < kAtOnce; c++)
+                    id[c] = p.ids[min(at + 64 * c + lane, pairs - 1)];
+#pragma unroll
+                for (int c = 0; c < kAtOnce; c++)
+                    add(p, at + 64 * c, id[c], e);
             }
+        }
+        wave_sync();
     }
 };
 
@@ -125,9 +131,9 @@ struct Few {
     static constexpr bool MX4 = MX4_;
     static constexpr int NW = NW_, WK = WK_, NB = NB_, WR = NW / WK, kThreads = 64 * NW;
     static constexpr int XC = 16 * NB / WK;
-    // a piece: 4 lines of every row, and as many values of the columns
-    static constexpr int kBytes = 512, kValues = MX4 ? 2 * kBytes : kBytes / 2;
-    static constexpr int kHalf = kValues / 8, F = MX4 ? 4 : 1;   // operands of 16 bytes
+    // a piece: 2 or 4 lines of every row, and as many values of the columns
+    static constexpr int kLines = MX4 ? 2 : 4, kBytes = 128 * kLines, kValues = MX4 ? 2 * kBytes : kBytes / 2;
+    static constexpr int kHalf = MX4 ? 128 : 32, F = MX4 ? 4 : 1;   // operands of 16 bytes
     static constexpr int kPitch = 2 * kValues + 16;              // of a column in LDS
     static constexpr int kX = 16 * NB * kPitch;
     static constexpr int kPer = 2 * kValues / 16;                // 16-byte pieces of a column
@@ -155,8 +161,10 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
     if ((uint32_t)e >= (uint32_t)p.E)
         return;
     Choices choices{list, 0, -1};
-    int id[Choices::kAtOnce];
-    choices.load(p, 0, id);
+    choices.collect(p, e);
+    const int n = uniform(choices.n);
+    if (n == 0 || (by_pair && uniform(choices.first) != (int)blockIdx.y))
+        return;
     const int R = FIRST ? 2 * p.I : p.H, K = FIRST ? p.H : p.I;
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wr = wave / WK, wk = wave % WK;
@@ -169,14 +177,16 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
     const __amdgpu_buffer_rsrc_t rw =
         make_rsrc(uniform_ptr((const char*)(FIRST ? p.w1 : p.w2) + first * pitch), (second + 16) * pitch);
     const uint8_t* const sf = (FIRST ? p.sf1 : p.sf2) + first * KB;
-    // Load i of a row block: rows 8 i + r % 8, piece q (lanes 0 .. 7) or 4 + q.
-    const uint32_t piece = 16 * (q + 4 * (r >> 3));
+    // Load i of a row block's line: bf16, rows 8 i + r % 8, piece q (lanes 0 .. 7)
+    // or 4 + q; 4-bit, row r, half i, piece q.
+    const uint32_t piece = 16 * (MX4 ? q : q + 4 * (r >> 3));
     uint32_t row_at[2][2];
 #pragma unroll
     for (int rb = 0; rb < 2; rb++)
 #pragma unroll
         for (int i = 0; i < 2; i++)
-            row_at[rb][i] = (uint32_t)(rb * second + 8 * i + (r & 7)) * pitch + piece;
+            row_at[rb][i] = (MX4 ? (uint32_t)(rb * second + r) * pitch + 64 * i
+                                 : (uint32_t)(rb * second + 8 * i + (r & 7)) * pitch) + piece;
     const int pieces = (int)((pitch + C::kBytes - 1) / C::kBytes), steps = (pieces + WK - 1) / WK;
     // Blocks start at different pieces: at the same one they would all read the
     // same few of the memory's channels (rows are powers of two apart: 441 us for
@@ -184,68 +194,54 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
     const int start = (blockIdx.x + blockIdx.y) % steps;
     auto turn = [&](int t) { return t >= steps ? steps : (t + start >= steps ? t + start - steps : t + start); };
 
-    u32x4 w[4][2][2];
-    uint64_t sc[2], next_sc[2];
-    // line j of the wave's piece of step t (zeros past the row's end)
+    constexpr int kLines = C::kLines;
+    u32x4 w[kLines][2][2];
+    uint32_t sc[2], next_sc[2];
+    // Line j of the wave's piece of step t.  Past the row's end: zeros (bf16), or
+    // whatever the next row has there (4-bit: finite, at scales of 2^-127 against
+    // columns of zeros).
     auto load_line = [&](int t, int j) {
-        const uint32_t at = (uint32_t)(t * WK + wk) * C::kBytes + 128 * j;
-        const bool in = at + piece < pitch;
+        const uint32_t at = (uint32_t)(t * WK + wk) * C::kBytes;
+        const bool in = MX4 || at + 128 * j + piece < pitch;
 #pragma unroll
         for (int rb = 0; rb < 2; rb++)
 #pragma unroll
             for (int i = 0; i < 2; i++)
-                w[j][rb][i] = buf16(rw, in ? row_at[rb][i] + at : kInvalid);
+                w[j][rb][i] = buf16(rw, in ? row_at[rb][i] + at + 128 * j : kInvalid);
     };
-    // The scales of line q of step t, of row r: 8 bytes, 0 past the row's end.
-    // (Loaded at the array's last 8 bytes where they would pass its end.)
-    const int64_t sf_left = ((int64_t)p.E * R - first) * KB - 8;
+    // The scales of half line q of step t, of row r: 4 bytes, 0 past the row's end.
+    // (Loaded at the array's last 4 bytes where they would pass its end.)
+    const int64_t sf_left = ((int64_t)p.E * R - first) * KB - 4;
     const uint32_t sf_last = sf_left < INT32_MAX ? (uint32_t)sf_left : INT32_MAX;
-    auto load_scales = [&](int t, uint64_t (&v)[2]) {
+    auto load_scales = [&](int t, uint32_t (&v)[2]) {
         if constexpr (MX4) {
-            typedef uint64_t Eight __attribute__((aligned(1)));
+            typedef uint32_t Four __attribute__((aligned(1)));
 #pragma unroll
             for (int rb = 0; rb < 2; rb++) {
-                const uint32_t at = (uint32_t)(rb * second + r) * KB + (uint32_t)(t * WK + wk) * 32 + 8 * q;
-                v[rb] = *(const Eight*)(sf + min(at, sf_last));
+                const uint32_t at = (uint32_t)(rb * second + r) * KB + (uint32_t)(t * WK + wk) * 16 + 4 * q;
+                v[rb] = *(const Four*)(sf + min(at, sf_last));
             }
         }
     };
-    auto row_scales = [&](int t, const uint64_t (&v)[2], uint32_t (&out)[2][2][4]) {
+    auto row_scales = [&](int t, const uint32_t (&v)[2], uint32_t (&out)[2][4]) {
 #pragma unroll
         for (int rb = 0; rb < 2; rb++) {
-            const uint32_t in_row = (uint32_t)(t * WK + wk) * 32 + 8 * q;
+            const uint32_t in_row = (uint32_t)(t * WK + wk) * 16 + 4 * q;
             const uint32_t at = (uint32_t)(rb * second + r) * KB + in_row;
             const uint32_t past = at > sf_last ? at - sf_last : 0;
-            uint64_t x = v[rb] >> (8 * (past & 7));
-            if (in_row + 8 > KB)
-                x = in_row < KB ? x & ((1ull << (8 * (KB - in_row))) - 1) : 0;
-            spread4((uint32_t)x, out[rb][0]);
-            spread4((uint32_t)(x >> 32), out[rb][1]);
+            uint32_t x = v[rb] >> (8 * (past & 3));
+            if (in_row + 4 > KB)
+                x = in_row < KB ? x & ((1u << (8 * (KB - in_row))) - 1) : 0;
+            spread4(x, out[rb]);
         }
     };
 
     auto load_weights = [&](int t) {
         load_scales(t, sc);
 #pragma unroll
-        for (int j = 0; j < 4; j++)
+        for (int j = 0; j < kLines; j++)
             load_line(t, j);
     };
-    // The weights need no more than the expert: where that is known, they are on
-    // their way while the choices are listed.
-    if (by_pair)
-        load_weights(turn(0));
-    choices.add(p, 0, id, e);
-    for (int at = 64 * Choices::kAtOnce; at < pairs; at += 64 * Choices::kAtOnce) {
-        choices.load(p, at, id);
-        choices.add(p, at, id, e);
-    }
-    wave_sync();
-    const int n = uniform(choices.n);
-    if (n == 0 || (by_pair && uniform(choices.first) != (int)blockIdx.y))
-        return;
-    if (!by_pair)
-        load_weights(turn(0));
-
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(FIRST ? p.x : hbuf);
     for (int c0 = 0; c0 < n; c0 += kPass) {
         const int here = min(kPass, n - c0);
@@ -321,10 +317,12 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
             col_at[b] = (wk * XC + (16 * b + r < kPass * PARTS && (16 * b + r) % kPass < here ? 16 * b + r : 0)) *
                             C::kPitch + q * (2 * C::kHalf / 4);
 
+        // The columns of every wave before any wave's weights: a CU's vector loads
+        // return in the order they were issued.
         load_x(turn(0));
+        unit_barrier();
+        load_weights(turn(0));
         const Extra early = extra(item(threadIdx.x));
-        if (c0)
-            load_weights(turn(0));
         store_x(0);
         lds_wait();
         unit_barrier();
@@ -332,17 +330,22 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
             const int next = turn(t + 1);
             load_x(next);
             load_scales(next, next_sc);
-            uint32_t scale[2][2][4];
+            uint32_t scale[2][4];
             if constexpr (MX4)
                 row_scales(turn(t), sc, scale);
             const char* const xb = smem + (t & 1) * C::kX;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
+            for (int j = 0; j < kLines; j++) {
                 u32x4 wv[2][2];
 #pragma unroll
-                for (int rb = 0; rb < 2; rb++)
-                    own_rows(r < 8, w[j][rb][0], w[j][rb][1], wv[rb]);
-                load_line(next, j);
+                for (int rb = 0; rb < 2; rb++) {
+                    if constexpr (MX4)
+                        wv[rb][0] = w[j][rb][0], wv[rb][1] = w[j][rb][1];
+                    else
+                        own_rows(r < 8, w[j][rb][0], w[j][rb][1], wv[rb]);
+                }
+                if constexpr (!MX4)
+                    load_line(next, j);
 #pragma unroll
                 for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
                         for (int rb = 0; rb < 2; rb++) {
                             if constexpr (MX4)
                                 wf[rb] = widen(wv[rb][h][f], __builtin_bit_cast(float, __builtin_amdgcn_ubfe(
-                                                                 scale[rb][h][j], 8 * q, 8) << 23));
+                                                                 scale[rb][(2 * j + h) & 3], 8 * q, 8) << 23));
                             else
                                 wf[rb] = __builtin_bit_cast(bf16x8, wv[rb][h]);
                         }
@@ -365,6 +368,10 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
                                 acc[rb][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[rb], xf, acc[rb][b], 0, 0, 0);
                         }
                     }
+                // (once the line is used up: the loads go into its registers)
+                if constexpr (MX4)
+                    load_line(next, j);
+                __builtin_amdgcn_sched_barrier(0);
             }
             store_x(t + 1);
             sc[0] = next_sc[0], sc[1] = next_sc[1];
@@ -469,17 +476,19 @@ __global__ void __launch_bounds__(256) few_sum_kernel(FewArgs p) {
 
 // Calls f(Few<...>()) with a block's shape for `rows` rows of `active` experts
 // (at most) and about `cols` columns of each: parts of the reduction axis until
-// two blocks a CU have work (their columns then share the LDS of 16), else room
+// three quarters of the CUs have a block, as far as the columns then fit (3
+// tokens over 8 experts of 2048 x 1024 in bf16, first and second pass: 18.4 + 10.2
+// us undivided, 12.4 + 6.6 in two, 13.2 + 8.0 in four; one token over 64 of 4096 x
+// 2048 in MXFP4, 256 blocks undivided: 17.5 + 11.1, 18.7 + 11.4, 20.2 + 14.0); room
 // for 32 columns where 16 are too few.
 template <bool MX4, class F>
 void for_shape(int rows, int active, int cols, F f) {
-    const int64_t blocks = (int64_t)(rows / 32) * active / 4, want = 2 * cu_count();
-    if (blocks * 2 > want || cols > 8) {
-        if (cols > 16)
-            f(Few<MX4, 8, 1, 2>());
-        else
-            f(Few<MX4, 4, 1, 1>());
-    } else if (blocks * 4 > want || cols > 4)
+    const int64_t blocks = (int64_t)(rows / 32) * active / 4, enough = cu_count() * 3 / 4;
+    if (cols > 16)
+        f(Few<MX4, 8, 1, 2>());
+    else if (blocks >= enough || cols > 8)
+        f(Few<MX4, 4, 1, 1>());
+    else if (blocks * 2 >= enough || cols > 4)
         f(Few<MX4, 4, 2, 1>());
     else
         f(Few<MX4, 4, 4, 1>());
