@@ -16,14 +16,11 @@
 
 #include "gg_forward.hpp"
 #include "gg_lane.hpp"
-#include "gg_tile.hpp"
+#include "gg_stream.hpp"
 
 namespace gg {
 
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
 
 // ---- tiles of ragged groups --------------------------------------------------
 
@@ -32,6 +29,23 @@ struct TileAt {
     int m0, rows;             // first row and rows of the tile (at most TM)
     int nt;                   // tile of columns
 };
+
+// v of the lane D before within 16 (first 15: 0), of lane 15 of the 16 lanes
+// before, of lane 31: the steps of a scan over the wave in the vector ALU.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int step_from(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+// Inclusive scan over the lanes of a wave, of values that 0 leaves as they are.
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+    v = op(v, step_from<0x111, 0xF>(v));
+    v = op(v, step_from<0x112, 0xF>(v));
+    v = op(v, step_from<0x114, 0xF>(v));
+    v = op(v, step_from<0x118, 0xF>(v));
+    v = op(v, step_from<0x142, 0xA>(v));               // row_bcast:15
+    return op(v, step_from<0x143, 0xC>(v));            // row_bcast:31
+}
 
 // Tile of block `q` where groups are cut into tiles of TM rows and tiles_n
 // columns.  Ends are taken as a running maximum within 0 .. m_rows, so ranges
@@ -46,26 +60,21 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* ends, int L, int m_rows
     for (int i = 0; i < per; i++)
         if (g0 + i < L)
             top = max(top, end_of(g0 + i));
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int below = __shfl_up(top, d);
-        top = lane >= d ? max(top, below) : top;
-    }
+    top = wave_scan(top, [](int a, int b) { return max(a, b); });
     int start = __shfl_up(top, 1);                     // where the lane's first group begins
     start = lane ? start : 0;
-    int tiles = 0, at = start;
-    for (int i = 0; i < per; i++)
-        if (g0 + i < L) {
-            const int end = max(at, end_of(g0 + i));
-            tiles += (end - at + TM - 1) / TM;
-            at = end;
-        }
-    int upto = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int below = __shfl_up(upto, d);
-        upto += lane >= d ? below : 0;
+    int tiles = 0;
+    if (per == 1) {
+        tiles = (top - start + TM - 1) / TM;
+    } else {
+        for (int i = 0, at = start; i < per; i++)
+            if (g0 + i < L) {
+                const int end = max(at, end_of(g0 + i));
+                tiles += (end - at + TM - 1) / TM;
+                at = end;
+            }
     }
+    const int upto = wave_scan(tiles, [](int a, int b) { return a + b; });
     TileAt t;
     t.g = -1;
     const int64_t P = (int64_t)__builtin_amdgcn_readlane(upto, 63) * tiles_n;
@@ -76,16 +85,17 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* ends, int L, int m_rows
     int mt = j / tiles_n;
     const int owner = __ffsll((unsigned long long)__ballot(upto > mt)) - 1;
     int before = __builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(tiles, owner);
-    int begin = __builtin_amdgcn_readlane(start, owner), end = begin, n = 0;
-    int g = owner * per;
-    for (; g < L; g++) {
-        end = max(begin, uniform(end_of(g)));
-        n = (end - begin + TM - 1) / TM;
-        if (mt < before + n)
-            break;
-        before += n;
-        begin = end;
-    }
+    int begin = __builtin_amdgcn_readlane(start, owner), end = __builtin_amdgcn_readlane(top, owner);
+    int n = (end - begin + TM - 1) / TM, g = owner * per;
+    if (per > 1)
+        for (end = begin; g < L; g++) {
+            end = max(begin, uniform(end_of(g)));
+            n = (end - begin + TM - 1) / TM;
+            if (mt < before + n)
+                break;
+            before += n;
+            begin = end;
+        }
     j -= before * tiles_n;
     const int band = j / (4 * tiles_n), high = min(4, n - 4 * band);
     j -= band * 4 * tiles_n;
@@ -155,8 +165,10 @@ __device__ __forceinline__ i32x8 low4(u32x4 v) {
     return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }
 
-// acc += deq(a) deq(b)^T over K values of rows whose codes are K / 2 bytes
-// apart (scales K / 32); rows past rows_valid / cols_valid count as zeros.
+// acc[i][j] += the transpose of the wave's (32 i, 32 j) block of deq(a) deq(b)^T
+// (a lane then owns a row of the block and four consecutive columns a register
+// group) over K values of rows whose codes are K / 2 bytes apart (scales K / 32);
+// rows past rows_valid / cols_valid count as zeros.
 // ODD: K is an odd number of stages of 128.
 template <class C, bool ODD>
 __device__ __forceinline__ void mx4_mainloop(char* smem, const char* a, const char* sfa, const char* b,
@@ -227,10 +239,10 @@ __device__ __forceinline__ void mx4_mainloop(char* smem, const char* a, const ch
             const int sa = (int)(f.sa[i] >> sh), sb = (int)(f.sb[j] >> sh);
             if (m < MB * NB)
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    low4(f.a[0][i]), low4(f.b[0][j]), acc[i][j], 4, 4, 0, sa, 0, sb);
+                    low4(f.b[0][j]), low4(f.a[0][i]), acc[i][j], 4, 4, 0, sb, 0, sa);
             else
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    low4(f.a[1][i]), low4(f.b[1][j]), acc[i][j], 4, 4, 2, sa, 2, sb);
+                    low4(f.b[1][j]), low4(f.a[1][i]), acc[i][j], 4, 4, 2, sb, 2, sa);
         }
     };
     if (ODD && threadIdx.x == 0)
@@ -264,179 +276,292 @@ __global__ void __launch_bounds__(GemmCfg::kThreads, 1) gemm_kernel(GemmMx4Args 
     mx4_mainloop<C, ODD>(smem, (const char*)p.a + m0 * (p.K / 2), (const char*)p.sfa + m0 * (p.K / 32),
                          weights_at(p, g, n0), scales_at(p, g, n0), p.K, rows, cols, am0, bn0, acc);
     const float alpha = p.alpha ? p.alpha[g] : 1.0f;
-    struct Bias {
-        float v[BIAS ? 8 : 1];
-    };
-    auto load = [&](int, int, int c) {
-        Bias b = {};
-        if constexpr (BIAS) {
-            const int col = n0 + bn0 + c;
-            const float* from = p.bias + (int64_t)g * p.N + (col < p.N ? col : 0);
+    // Rounded, then through the wave's own region of LDS, a row of the wave's 128
+    // (for fp32 half of one) behind the other, so that a store has whole lines: 16
+    // lanes the 256 bytes of a row.  Rows and columns off the tile are masked by
+    // the descriptor.  (Against staging fp32 and rounding behind it, a third of the
+    // LDS instructions: 4k clocks a tile for 15k.)
+    constexpr int kSize = DT == GG_F32 ? 4 : 2, kPasses = kSize / 2, kJ = NB / kPasses;
+    constexpr int kPitch = 32 * kJ * kSize + 16, kRows = TM / C::WM, kWave = kRows * kPitch;
+    static_assert(kPitch == 272 && C::kWaves * kWave <= Scales4<C>::kSmem, "rows of 256 bytes");
+    char* const lds = smem + w * kWave;
+    const int lane = threadIdx.x & 63, lr = lane & 31, lq = lane >> 5;
+    const uint32_t pitch = (uint32_t)p.N * kSize;
+    const int left = rows - am0 < 0 ? 0 : (rows - am0 < kRows ? rows - am0 : kRows);
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(uniform_ptr((char*)p.d + (m0 + am0) * pitch),
+                                                (uint32_t)uniform((int)(left * pitch)));
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-                b.v[k] = from[k];
-        }
-        return b;
-    };
-    auto store = [&](int, int r, int c, float (&v)[8], const Bias& b) {
-        const int row = am0 + r, col = n0 + bn0 + c;
-        if (row < rows && col < p.N) {
+    for (int pass = 0; pass < kPasses; pass++) {
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-                v[k] = BIAS ? fmaf(alpha, v[k], b.v[k]) : alpha * v[k];
-            store8(p.d, DT, (m0 + row) * p.N + col, v);
+        for (int jj = 0; jj < kJ; jj++) {
+            const int j = pass * kJ + jj, col = n0 + bn0 + 32 * j + 4 * lq;
+            f32x4 bias[4];
+#pragma unroll
+            for (int g4 = 0; g4 < 4; g4++)
+                if constexpr (BIAS) {
+                    const float* const from = p.bias + (int64_t)g * p.N + (col < p.N ? col + 8 * g4 : 0);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        bias[g4][k] = from[k];
+                }
+#pragma unroll
+            for (int i = 0; i < MB; i++)
+#pragma unroll
+                for (int g4 = 0; g4 < 4; g4++) {
+                    float v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        v[k] = BIAS ? fmaf(alpha, acc[i][j][4 * g4 + k], bias[g4][k]) : alpha * acc[i][j][4 * g4 + k];
+                    char* const at = lds + (32 * i + lr) * kPitch + (32 * jj + 8 * g4 + 4 * lq) * kSize;
+                    if constexpr (DT == GG_F32)
+                        *(f32x4*)at = f32x4{v[0], v[1], v[2], v[3]};
+                    else if constexpr (DT == GG_BF16)
+                        *(u32x2*)at = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    else
+                        *(u32x2*)at = u32x2{(uint32_t)f32_to_f16(v[0]) | (uint32_t)f32_to_f16(v[1]) << 16,
+                                            (uint32_t)f32_to_f16(v[2]) | (uint32_t)f32_to_f16(v[3]) << 16};
+                }
         }
-    };
-    for_each_row8<C, BIAS ? 4 : 1, 64, 0, -1, true>(acc, (float*)(smem + w * kEpiWaveBytes), load, store);
+        wave_sync();
+        const int col = n0 + bn0 + 32 * kJ * pass + 16 / kSize * (lane & 15);
+        const uint32_t at = (lane >> 4) * pitch + (uint32_t)col * kSize;
+#pragma unroll
+        for (int t4 = 0; t4 < kRows / 4; t4++) {
+            typedef int i32x4 __attribute__((ext_vector_type(4)));
+            const i32x4 v = *(const i32x4*)(lds + (4 * t4 + (lane >> 4)) * kPitch + 16 * (lane & 15));
+            __builtin_amdgcn_raw_buffer_store_b128(v, rd, col < p.N ? at + 4 * t4 * pitch : kInvalid, 0, 2);
+        }
+        wave_sync();                                   // the region is free again
+    }
 }
 
 // ---- the thin kernel ---------------------------------------------------------
 
-constexpr int kThinWaves = 8, kThinThreads = 64 * kThinWaves, kThinCols = 64, kRB = kThinCols / 16;
+constexpr int kThinWaves = 4, kThinThreads = 64 * kThinWaves;
 
-// NB: blocks of 16 rows of d in a tile.
-template <int NB>
-__global__ void __launch_bounds__(kThinThreads, NB == 1 ? 4 : 2) thin_kernel(GemmMx4Args p) {
-    __shared__ __attribute__((aligned(16))) f32x4 sum[kThinWaves][kRB][64];
+// A wave takes 32 rows of the weights and NB blocks of 16 rows of a, piece after
+// piece of 2 lines (512 values) of each row; the next piece's loads go into the
+// registers that a line leaves.  WK waves share the rows of the weights and have
+// a part of the reduction axis each, added up in LDS: for calls with too few rows
+// of weights to fill the device.
+//
+// What a CU's load path takes is lines, so every load is one of whole lines: codes
+// 8 rows x 128 bytes (own_rows brings each lane its own row's), scales as 8 rows x
+// 128 bytes for 8 pieces, through a region of LDS of the wave's own.
+template <int WK, int NB>
+__global__ void __launch_bounds__(kThinThreads, 2) thin_kernel(GemmMx4Args p) {
+    constexpr int WR = kThinWaves / WK, kCols = 32 * WR, kBlocks = 2 + NB;   // (two blocks of b, NB of a)
+    constexpr int kAhead = 8, kPitch = 16 * kAhead + 16;                     // pieces of scales; a row of them in LDS
+    constexpr int kScales = 16 * kBlocks * kPitch, kSum = WK > 1 ? 2 * NB * 1024 : 0;
+    __shared__ __attribute__((aligned(16))) char smem[kThinWaves][kScales > kSum ? kScales : kSum];
     check_ends(p);
-    const TileAt t = tile_at<16 * NB>(p.ends, p.L, (int)p.m_rows, (p.N + kThinCols - 1) / kThinCols, blockIdx.x);
+    const TileAt t = tile_at<16 * NB>(p.ends, p.L, (int)p.m_rows, (p.N + kCols - 1) / kCols, blockIdx.x);
     if (t.g < 0)
         return;
-    const int g = uniform(t.g), rows = uniform(t.rows), n0 = uniform(t.nt) * kThinCols;
+    const int g = uniform(t.g), rows = uniform(t.rows);
     const int64_t m0 = uniform(t.m0);
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int cols = min(kThinCols, p.N - n0), nb = (rows + 15) >> 4;
-    const uint32_t pitch = p.K / 2, spitch = p.K / 32;
-    const char* const w = (const char*)uniform_ptr(weights_at(p, g, n0));
-    const char* const sw = (const char*)uniform_ptr(scales_at(p, g, n0));
-    const char* const x = (const char*)p.a + m0 * pitch;
-    const char* const sx = (const char*)p.sfa + m0 * spitch;
-    uint32_t wr[kRB], xr[NB];
+    const int wr = wave / WK, wk = wave % WK;
+    const int n0 = uniform(t.nt) * kCols + 32 * wr;
+    const bool live = n0 < p.N;                        // (of the last block's waves some may have none)
+    const uint32_t pitch = p.K / 2, KB = p.K / 32;
+    const int nw = live ? n0 : 0;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(uniform_ptr(weights_at(p, g, nw)), 32 * pitch);
+    const __amdgpu_buffer_rsrc_t rsw = make_rsrc(uniform_ptr(scales_at(p, g, nw)), 32 * KB);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(uniform_ptr((const char*)p.a + m0 * pitch), rows * pitch);
+    const __amdgpu_buffer_rsrc_t rsx = make_rsrc(uniform_ptr((const char*)p.sfa + m0 * KB), rows * KB);
+    const int pieces = (p.K + 511) / 512, steps = (pieces + WK - 1) / WK;
+    const int first = wk * steps;                      // the wave's pieces: first .. first + steps - 1
+    // block c: rows 16 c .. of the weights, then of a
+    auto rsrc = [&](int c) { return c < 2 ? rw : rx; };
+    auto scale_rsrc = [&](int c) { return c < 2 ? rsw : rsx; };
+    auto row_of = [&](int c, int row) { return (uint32_t)(c < 2 ? 16 * c + row : 16 * (c - 2) + row); };
+
+    u32x4 v[2][kBlocks][2], sv[kBlocks][2];
+    // Line j of piece i: rows 8 h + r % 8, 16 bytes at 16 (q + 4 (r / 8)).  (Past the
+    // rows of a: zeros.  Past the row's end, where no step uses it, whatever the
+    // next row has there.)
+    const uint32_t lane_at = (r & 7) * pitch + 16 * (q + 4 * (r >> 3));
+    auto load_line = [&](int i, int j) {
+        const uint32_t at = lane_at + (uint32_t)i * 256 + 128 * j;
 #pragma unroll
-    for (int rb = 0; rb < kRB; rb++)
-        wr[rb] = min(16 * rb + r, cols - 1);
+        for (int c = 0; c < kBlocks; c++)
 #pragma unroll
-    for (int b = 0; b < NB; b++)
-        xr[b] = min(16 * b + r, rows - 1);
-    f32x4 acc[kRB][NB];
+            for (int h = 0; h < 2; h++)
+                v[j][c][h] = buf16(rsrc(c), row_of(c, 8 * h) * pitch + at);
+    };
+    // The scales of pieces i .. i + 7: rows 8 h + lane / 8, those of piece i + lane % 8.
+    auto load_scales = [&](int i) {
+        const uint32_t at = (lane >> 3) * KB + (uint32_t)(i + (lane & 7)) * 16;
 #pragma unroll
-    for (int rb = 0; rb < kRB; rb++)
+        for (int c = 0; c < kBlocks; c++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                sv[c][h] = buf16(scale_rsrc(c), row_of(c, 8 * h) * KB + at);
+    };
+    auto store_scales = [&] {
+#pragma unroll
+        for (int c = 0; c < kBlocks; c++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                *(u32x4*)(smem[wave] + (16 * c + 8 * h + (lane >> 3)) * kPitch + 16 * (lane & 7)) = sv[c][h];
+        wave_sync();
+    };
+    f32x4 acc[2][NB];
+#pragma unroll
+    for (int rb = 0; rb < 2; rb++)
 #pragma unroll
         for (int b = 0; b < NB; b++)
             acc[rb][b] = f32x4{0};
-    // H halves of 128 values from k0 on; a scale word has the bytes of its four
-    // blocks, a lane's is byte q
-    auto chunk = [&](int k0, auto Hc) {
-        constexpr int H = decltype(Hc)::value;
-        u32x4 wv[H][kRB], xv[H][NB];
-        uint32_t ws[H][kRB], xs[H][NB];
+    load_scales(first);
+    load_line(first, 0);
+    load_line(first, 1);
+    for (int i0 = first; i0 < first + steps; i0 += kAhead) {
+        store_scales();
+        load_scales(i0 + kAhead);
+        const int end = min(i0 + kAhead, first + steps);
+        for (int i = i0; i < end; i++) {
+            u32x4 sc[kBlocks];
 #pragma unroll
-        for (int h = 0; h < H; h++)
+            for (int c = 0; c < kBlocks; c++)
+                sc[c] = *(const u32x4*)(smem[wave] + (16 * c + r) * kPitch + 16 * (i - i0));
+            // Halves of the piece within the row (its end is a multiple of one); past
+            // them scales of 2^-127 on both sides, which leave nothing of any codes.
+            const int halves = (int)(KB - (uint32_t)i * 16) / 4;
 #pragma unroll
-            for (int rb = 0; rb < kRB; rb++)
-                wv[h][rb] = *(const u32x4*)(w + wr[rb] * pitch + (uint32_t)(k0 / 2 + 64 * h + 16 * q));
+            for (int c = 0; c < kBlocks; c++)
 #pragma unroll
-        for (int h = 0; h < H; h++)
+                for (int h = 0; h < 4; h++)
+                    sc[c][h] = h < halves ? sc[c][h] >> (8 * q) : 0;
 #pragma unroll
-            for (int rb = 0; rb < kRB; rb++)
-                ws[h][rb] = *(const uint32_t*)(sw + wr[rb] * spitch + (uint32_t)(k0 / 32 + 4 * h));
+            for (int j = 0; j < 2; j++) {
+                u32x4 own[kBlocks][2];
 #pragma unroll
-        for (int b = 0; b < NB; b++)
-            if (b < nb) {
+                for (int c = 0; c < kBlocks; c++)
+                    own_rows(r < 8, v[j][c][0], v[j][c][1], own[c]);
+                load_line(i + 1, j);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int h = 0; h < H; h++) {
-                    xv[h][b] = *(const u32x4*)(x + xr[b] * pitch + (uint32_t)(k0 / 2 + 64 * h + 16 * q));
-                    xs[h][b] = *(const uint32_t*)(sx + xr[b] * spitch + (uint32_t)(k0 / 32 + 4 * h));
-                }
+                for (int h = 0; h < 2; h++)
+#pragma unroll
+                    for (int b = 0; b < NB; b++)
+#pragma unroll
+                        for (int rb = 0; rb < 2; rb++)
+                            acc[rb][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                low4(own[rb][h]), low4(own[2 + b][h]), acc[rb][b], 4, 4, 0,
+                                (int)sc[rb][2 * j + h], 0, (int)sc[2 + b][2 * j + h]);
             }
+        }
+    }
+    const float alpha = p.alpha ? p.alpha[g] : 1.0f;
+    // register i of a lane: weight row 16 rb + 4 q + i, row 16 b + r of a
+    auto store = [&](int rb, int b, f32x4 v) {
+        const int row = 16 * b + r, col = n0 + 16 * rb + 4 * q;
+        if (!live || row >= rows)
+            return;
+        const float* const bias = p.bias ? p.bias + (int64_t)g * p.N + col : nullptr;
 #pragma unroll
-        for (int h = 0; h < H; h++)
+        for (int i = 0; i < 4; i++)
+            v[i] = bias ? fmaf(alpha, v[i], bias[i]) : alpha * v[i];
+        const int64_t at = (m0 + row) * p.N + col;
+        if (p.d_dtype == GG_F32) {
+            *(f32x4*)((float*)p.d + at) = v;
+        } else {
+            auto two = [&](float a, float b) {
+                return p.d_dtype == GG_BF16 ? pack_bf16x2(a, b)
+                                            : (uint32_t)f32_to_f16(a) | (uint32_t)f32_to_f16(b) << 16;
+            };
+            *(u32x2*)((uint16_t*)p.d + at) = u32x2{two(v[0], v[1]), two(v[2], v[3])};
+        }
+    };
+    if constexpr (WK == 1) {
+#pragma unroll
+        for (int rb = 0; rb < 2; rb++)
 #pragma unroll
             for (int b = 0; b < NB; b++)
-                if (b < nb) {
+                store(rb, b, acc[rb][b]);
+    } else {
+        auto sum = [&](int w, int rb, int b) { return (f32x4*)smem[w] + (rb * NB + b) * 64 + lane; };
 #pragma unroll
-                    for (int rb = 0; rb < kRB; rb++)
-                        acc[rb][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            low4(wv[h][rb]), low4(xv[h][b]), acc[rb][b], 4, 4, 0, (int)(ws[h][rb] >> (8 * q)),
-                            0, (int)(xs[h][b] >> (8 * q)));
-                }
-    };
-    int k0 = wave * 256;
-    for (; k0 + 256 <= p.K; k0 += kThinWaves * 256)
-        chunk(k0, std::integral_constant<int, 2>());
-    if (k0 < p.K)
-        chunk(k0, std::integral_constant<int, 1>());
-    const float alpha = p.alpha ? p.alpha[g] : 1.0f;
+        for (int rb = 0; rb < 2; rb++)
 #pragma unroll
-    for (int b = 0; b < NB; b++) {
-        if (b >= nb)
-            break;
-        if (b)
-            __syncthreads();                           // sum may still be read
-#pragma unroll
-        for (int rb = 0; rb < kRB; rb++)
-            sum[wave][rb][lane] = acc[rb][b];
+            for (int b = 0; b < NB; b++)
+                *sum(wave, rb, b) = acc[rb][b];
         __syncthreads();
-        if (wave < kRB) {
-            f32x4 v = sum[0][wave][lane];
+        // block (rb, b) of a row of waves by the wave rb NB + b of them
+        for (int j = wk; j < 2 * NB; j += WK) {
+            const int rb = j / NB, b = j % NB;
+            f32x4 v = *sum(wr * WK, rb, b);
 #pragma unroll
-            for (int j = 1; j < kThinWaves; j++)
-                v += sum[j][wave][lane];
-            // register i of a lane is weight row 4 q + i, row r of d
-            const int row = 16 * b + r, col = 16 * wave + 4 * q;
-            if (row < rows && col < cols) {
-                const float* const bias = p.bias ? p.bias + (int64_t)g * p.N + n0 + col : nullptr;
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    v[i] = bias ? fmaf(alpha, v[i], bias[i]) : alpha * v[i];
-                const int64_t at = (m0 + row) * p.N + n0 + col;
-                if (p.d_dtype == GG_F32)
-                    *(f32x4*)((float*)p.d + at) = v;
-                else {
-                    uint32_t lo, hi;
-                    if (p.d_dtype == GG_BF16) {
-                        lo = pack_bf16x2(v[0], v[1]);
-                        hi = pack_bf16x2(v[2], v[3]);
-                    } else {
-                        lo = (uint32_t)f32_to_f16(v[0]) | (uint32_t)f32_to_f16(v[1]) << 16;
-                        hi = (uint32_t)f32_to_f16(v[2]) | (uint32_t)f32_to_f16(v[3]) << 16;
-                    }
-                    *(u32x2*)((uint16_t*)p.d + at) = u32x2{lo, hi};
-                }
-            }
+            for (int k = 1; k < WK; k++)
+                v += *sum(wr * WK + k, rb, b);
+            store(rb, b, v);
         }
     }
 }
 
-}  // namespace
+// How a call's rows are cut: blocks of 16 rows a tile and the waves that share
+// rows of the weights; nb 0: the tiled kernel.
+struct Shape {
+    int nb, wk;
+    int tm() const { return nb ? 16 * nb : GemmCfg::TM; }
+    int tn() const { return nb ? 32 * kThinWaves / wk : GemmCfg::TN; }
+};
 
-// Blocks of 16 rows of the thin kernel's tiles, 0: the tiled kernel.
-static int thin_blocks(const GemmMx4Args& p) {
+// Thin up to 32 rows a group, where the weights are what costs (64 groups of 4096 x
+// 4096, thin and tiled: 8 rows 109 and 159 us, 32 rows 151 and 151, 48 rows 268 and
+// 160), and where there are too few tiles for the device, up to 2^20 elements of d
+// (8 groups of 64 rows, 2048 x 2048: 14 and 21 us; of 128: 24 and 21).  Parts of
+// the reduction axis where blocks would leave half the CUs without one (one group
+// of 16 rows, 4096 x 4096: 8 us for 17; 16 groups of 7168 x 2048, 256 blocks: 30
+// for 26).
+Shape shape_of(const GemmMx4Args& p) {
     const int64_t each = p.m_rows / p.L;               // rows of a group, on average
-    return each <= 16 ? 1 : each <= 64 ? 4 : 0;
+    const int64_t groups = p.m_rows < p.L ? p.m_rows : p.L;
+    if (each > 32 && p.m_rows * p.N > (1 << 20))
+        return Shape{0, 1};
+    Shape s = {each <= 16 ? 1 : 2, 1};
+    const int64_t tiles = p.m_rows / s.tm() > groups ? p.m_rows / s.tm() : groups;
+    if (tiles * ((p.N + s.tn() - 1) / s.tn()) <= cu_count() / 2)
+        s.wk = 4;
+    return s;
 }
 
+template <class F>
+void for_thin(const Shape& s, F f) {
+    using std::integral_constant;
+    if (s.nb == 1)
+        s.wk == 1 ? f(integral_constant<int, 1>(), integral_constant<int, 1>())
+                  : f(integral_constant<int, 4>(), integral_constant<int, 1>());
+    else
+        s.wk == 1 ? f(integral_constant<int, 1>(), integral_constant<int, 2>())
+                  : f(integral_constant<int, 4>(), integral_constant<int, 2>());
+}
+
+}  // namespace
+
 int64_t gemm_mx4_blocks(const GemmMx4Args& p) {
-    const int nb = thin_blocks(p);
-    const int64_t tiles = nb ? tile_bound(p, 16 * nb, kThinCols) : tile_bound(p, GemmCfg::TM, GemmCfg::TN);
+    const Shape c = shape_of(p);
+    const int64_t tiles = tile_bound(p, c.tm(), c.tn());
     return tiles > 1 ? tiles : 1;                      // (one block writes the error word)
 }
 
 hipError_t launch_gemm_mx4(const GemmMx4Args& p, hipStream_t s, LaunchInfo* info) {
-    const int nb = thin_blocks(p);
+    const Shape c = shape_of(p);
     const dim3 grid((unsigned)gemm_mx4_blocks(p));
     if (info) {
-        snprintf(info->kernel, sizeof info->kernel, "%s<D %s>", nb ? "thin_kernel" : "gemm_kernel",
+        snprintf(info->kernel, sizeof info->kernel, "%s<D %s>", c.nb ? "thin_kernel" : "gemm_kernel",
                  dtype_name(p.d_dtype));
-        info->tm = nb ? 16 * nb : GemmCfg::TM;
-        info->tn = nb ? kThinCols : GemmCfg::TN;
-        info->waves = nb ? kThinWaves : GemmCfg::kWaves;
+        info->tm = c.tm();
+        info->tn = c.tn();
+        info->waves = c.nb ? kThinWaves : GemmCfg::kWaves;
         info->grid = grid.x;
     }
-    if (nb == 1)
-        hipLaunchKernelGGL((thin_kernel<1>), grid, dim3(kThinThreads), 0, s, p);
-    else if (nb)
-        hipLaunchKernelGGL((thin_kernel<4>), grid, dim3(kThinThreads), 0, s, p);
+    if (c.nb)
+        for_thin(c, [&](auto WK, auto NB) {
+            hipLaunchKernelGGL((thin_kernel<decltype(WK)::value, decltype(NB)::value>), grid, dim3(kThinThreads), 0, s,
+                               p);
+        });
     else {
         const dim3 block(GemmCfg::kThreads);
         auto by_shape = [&](auto DTc) {
