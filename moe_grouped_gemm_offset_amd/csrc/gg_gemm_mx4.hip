@@ -141,18 +141,18 @@ __device__ __forceinline__ const char* scales_at(const GemmMx4Args& p, int g, in
 
 using GemmCfg = Cfg<256, 256, 2, 2>;
 
-// Scales of 4 stages (16 bytes of every tile row, 2 load units) at a time, in
-// two alternating buffers behind the unit buffers: row r of A in slot r, of B
-// in slot TM + r.  A wave's load moves the 16 bytes of 64 rows; units 2g + 1
-// and 2g + 2 carry the A and the B half of group g + 1.  Then 16 bytes of
-// zeros, the scales of the stage past an odd number of them (the next row's
-// bytes, which the loads bring there, may be the scale of NaN).
+// Scales of 8 stages (32 bytes of every tile row, 4 load units) at a time, in two
+// alternating buffers behind the unit buffers: row r of A in slot r, of B in slot
+// TM + r.  A wave's load moves the 32 bytes of 32 rows, two lanes a row; units
+// 4g + 1 .. 4g + 4 carry 64 rows of A and of B each of group g + 1.  (16 bytes of 64 rows a
+// load, as many loads, cost the load path twice the lines: a third of all that a
+// unit takes.)  The two halves of a slot change places in every second 8 rows, so
+// that the words of 32 rows are read with 2-way bank conflicts.
 template <class C>
 struct Scales4 {
-    static constexpr int kBuf = (C::TM + C::TN) * 16;
-    static constexpr int kBase = 2 * C::kUnit, kZero = kBase + 2 * kBuf;
-    static constexpr int kSmem = kZero + 16 > C::kLds ? kZero + 16 : C::kLds;
-    static_assert(C::TM == 256 && C::TN == 256 && C::kWaves == 4, "a wave's load is 64 rows");
+    static constexpr int kBuf = (C::TM + C::TN) * 32, kBase = 2 * C::kUnit;
+    static constexpr int kSmem = kBase + 2 * kBuf > C::kLds ? kBase + 2 * kBuf : C::kLds;
+    static_assert(C::TM == 256 && C::TN == 256 && C::kWaves == 4, "a wave's load is 32 rows");
 };
 
 template <class C>
@@ -181,14 +181,15 @@ __device__ __forceinline__ void mx4_mainloop(char* smem, const char* a, const ch
     const int64_t ld = K / 2;
     const uint32_t KB = K / 32;
     const int nk = K / 128;
-    // waves 0 and 1 load A's scales, 2 and 3 B's
+    // Slice s of a group: rows 64 s + 32 (w & 1) + l / 2 of A (waves 0 and 1) and of
+    // B (2 and 3).  (What is past a row's end belongs to no stage.)
     const bool of_a = wu < 2;
     const int valid = of_a ? (rows_valid < TM ? rows_valid : TM) : (cols_valid < TN ? cols_valid : TN);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(uniform_ptr(of_a ? sfa : sfb), (uint32_t)uniform(valid * (int)KB));
-    const uint32_t sc_lds = lds_addr(smem) + S::kBase + (of_a ? 0 : TM * 16) + (wu & 1) * 1024;
-    const uint32_t sc_off = (uint32_t)(64 * (wu & 1) + l) * KB;
-    auto scale_load = [&](int grp, int half) {
-        dma16(rs, sc_lds + (grp & 1) * S::kBuf + half * 2048, sc_off + half * 128 * KB + 16 * grp);
+    const uint32_t sc_lds = lds_addr(smem) + S::kBase + (of_a ? 0 : TM * 32) + (wu & 1) * 1024;
+    const uint32_t sc_off = (uint32_t)(32 * (wu & 1) + (l >> 1)) * KB + 16 * ((l ^ l >> 4) & 1);
+    auto scale_load = [&](int grp, int s) {
+        dma16(rs, sc_lds + (grp & 1) * S::kBuf + s * 2048, sc_off + s * 64 * KB + 32 * grp);
     };
     LoadK<C, TM> la;
     LoadK<C, TN> lb;
@@ -202,22 +203,26 @@ __device__ __forceinline__ void mx4_mainloop(char* smem, const char* a, const ch
         else if (i < kLA + kLB)
             lb.template issue<ODD>(st + TM * kRowBytes, b + kb, ld - kb, i - kLA);
         else                                           // (unit 0: group 0's again)
-            scale_load(u > 0 ? (u - 1) / 2 + 1 : 0, u > 0 ? (u - 1) & 1 : 0);
+            scale_load(u > 0 ? (u - 1) / 4 + 1 : 0, u > 0 ? (u - 1) & 3 : 0);
     };
     const uint32_t sh = 8 * lq;
+    const int sc_a = (am0 + lr) * 32, sc_b = (TM + bn0 + lr) * 32, sc_half = lr << 1 & 16;
     auto read = [&](const char* st, int kt, FragMx4<C>& f, int g) {
         const bool is_a = g < MB;
         const int r = is_a ? am0 + 32 * g + lr : bn0 + 32 * (g - MB) + lr;
         const char* s = is_a ? st : st + TM * kRowBytes;
         const u32x4 x0 = ld_lds16(s, lds_off(r, 4 * (kt & 1) + lq));
         const u32x4 x1 = ld_lds16(s, lds_off(r, 4 * (kt & 1) + 2 + lq));
-        int base = S::kBase + ((kt >> 2) & 1) * S::kBuf + 4 * (kt & 3), at = (is_a ? r : TM + r) * 16;
+        // (word w of a slot is in its half (w / 4) ^ (row / 8 % 2))
+        const char* base = smem + S::kBase + ((kt >> 3) & 1) * S::kBuf + 4 * (kt & 3);
+        int at = (is_a ? sc_a + 1024 * g : sc_b + 1024 * (g - MB)) + ((kt << 2 & 16) ^ sc_half);
         if constexpr (ODD) {
-            const int keep = kt < nk ? -1 : 0;
-            base = kt < nk ? base : S::kZero;
-            at &= keep;
+            // past an odd number of stages: a word of the codes, which are zeros
+            // there (the next row's scales, which the loads bring, may be NaN's)
+            base = kt < nk ? base : st + lds_off(0, 4);
+            at = kt < nk ? at : 0;
         }
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(smem + base + at);
+        const uint32_t word = *reinterpret_cast<const uint32_t*>(base + at);
         if (is_a) {
             f.a[0][g] = x0;
             f.a[1][g] = x1;
@@ -245,11 +250,11 @@ __device__ __forceinline__ void mx4_mainloop(char* smem, const char* a, const ch
                     low4(f.b[1][j]), low4(f.a[1][i]), acc[i][j], 4, 4, 2, sb, 2, sa);
         }
     };
-    if (ODD && threadIdx.x == 0)
-        *reinterpret_cast<u32x4*>(smem + S::kZero) = u32x4{0};
     FragMx4<C> frag[2];
     scale_load(0, 0);
     scale_load(0, 1);
+    scale_load(0, 2);
+    scale_load(0, 3);
     pipeline<C, kLA + kLB + 1, 2 * MB * NB, MB + NB>(smem, nk, frag, issue, read, mma);
 }
 
