@@ -43,12 +43,13 @@ void for_act(int act, F f) {
 
 // ---- rows as a run of eights -------------------------------------------------
 // Kernels over (rows, width) elements take eight elements of a row a lane (width
-// is a multiple of 8), kUnroll of them at a time, the block's threads side by
+// is a multiple of 8), kUnroll of them at a time (65536 rows of 4096 in bf16, one, two,
+// four at a time: see the kernels), the block's threads side by
 // side: eight v of the matrix is row v / per_row.  The division goes by the
 // block's first eight (a 64-bit reciprocal, exact for v * per_row < 2^64) and
 // by the distance from it within the row.
 constexpr int kRowThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 constexpr int kRowStep = kRowThreads * kUnroll;
 
 struct Eights {
@@ -74,11 +75,19 @@ inline unsigned eights_grid(const Eights& e) {
     return (unsigned)(n < (1 << 22) ? n : 1 << 22);
 }
 
-// Calls f(rows, cols, live, base, n) for every run of the block: the row and
-// first column of each of the thread's eights (clamped to the matrix's last
-// where !live), and base + u * kRowThreads, the eight's own index.
-template <class F>
-__device__ __forceinline__ void for_eights(const Eights& e, const int32_t* end, F f) {
+// The thread's eights of a run (clamped to the matrix's last where !live): row and
+// first column, the eight's own index, and the first element's in rows of pitch
+// ld.
+struct Run {
+    int64_t row[kUnroll], v[kUnroll], at[kUnroll];
+    uint32_t col[kUnroll];
+    bool live[kUnroll];
+};
+
+// Calls f(run) for every run of the block.  FLAT: rows follow each other without a
+// gap (ld is the width), and f wants neither rows nor columns.
+template <bool FLAT, class F>
+__device__ __forceinline__ void for_eights(const Eights& e, int64_t ld, const int32_t* end, F f) {
     int64_t rows = e.rows;
     if (end) {
         const int64_t n = *end;
@@ -86,25 +95,33 @@ __device__ __forceinline__ void for_eights(const Eights& e, const int32_t* end, 
     }
     const int64_t total = rows * e.per_row;
     for (int64_t base = (int64_t)blockIdx.x * kRowStep; base < total; base += (int64_t)gridDim.x * kRowStep) {
-        const int64_t row0 = e.magic64 ? (int64_t)__umul64hi((uint64_t)base, e.magic64) : base;
-        const uint32_t at0 = (uint32_t)(base - row0 * e.per_row);
         const uint32_t left = (uint32_t)(total - base < kRowStep ? total - base : kRowStep) - 1;
-        int64_t row[kUnroll], v[kUnroll];
-        uint32_t col[kUnroll];
-        bool live[kUnroll];
+        int64_t row0 = 0;
+        uint32_t at0 = 0;
+        if constexpr (!FLAT) {
+            row0 = e.magic64 ? (int64_t)__umul64hi((uint64_t)base, e.magic64) : base;
+            at0 = (uint32_t)(base - row0 * e.per_row);
+        }
+        Run r;
 #pragma unroll
         for (int u = 0; u < kUnroll; u++) {
             const uint32_t i = threadIdx.x + u * kRowThreads;
-            live[u] = i <= left;
-            const uint32_t j = live[u] ? i : left, at = at0 + j;
-            // (at < 2 per_row from 1024 on, at < 2048 below)
-            const uint32_t over = e.per_row >= kRowStep ? (at >= e.per_row ? 1u : 0u)
-                                : e.magic ? __umulhi(at, e.magic) : at;
-            row[u] = row0 + over;
-            col[u] = (at - over * e.per_row) * 8;
-            v[u] = base + j;
+            r.live[u] = i <= left;
+            const uint32_t j = r.live[u] ? i : left;
+            r.v[u] = base + j;
+            if constexpr (FLAT) {
+                r.at[u] = r.v[u] * 8;
+            } else {
+                // (at < 2 per_row from kRowStep on, at < 2 kRowStep below)
+                const uint32_t at = at0 + j;
+                const uint32_t over = e.per_row >= kRowStep ? (at >= e.per_row ? 1u : 0u)
+                                    : e.magic ? __umulhi(at, e.magic) : at;
+                r.row[u] = row0 + over;
+                r.col[u] = (at - over * e.per_row) * 8;
+                r.at[u] = r.row[u] * ld + r.col[u];
+            }
         }
-        f(row, col, v, live);
+        f(r);
     }
 }
 

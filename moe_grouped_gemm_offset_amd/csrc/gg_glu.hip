@@ -18,16 +18,15 @@ __global__ void __launch_bounds__(kRowThreads) glu_kernel(GluArgs p, Eights e) {
     const C* const c = (const C*)p.c;
     Y* const y = (Y*)p.y;
     const int gate = p.act.gate_first ? 0 : 32, input = 32 - gate;
-    for_eights(e, p.end, [&](const int64_t (&row)[kUnroll], const uint32_t (&col)[kUnroll],
-                             const int64_t (&v)[kUnroll], const bool (&live)[kUnroll]) {
+    for_eights<false>(e, p.ldy, p.end, [&](const Run& run) {
         Eight<CDT> u[kUnroll], g[kUnroll];
         float w[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; i++) {
-            const C* const at = c + row[i] * p.ldc + ((col[i] & ~31u) * 2 + (col[i] & 31u));
+            const C* const at = c + run.row[i] * p.ldc + ((run.col[i] & ~31u) * 2 + (run.col[i] & 31u));
             u[i].load(at + input);
             g[i].load(at + gate);
-            w[i] = p.prob ? p.prob[row[i]] : 1.0f;
+            w[i] = p.prob ? p.prob[run.row[i]] : 1.0f;
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; i++) {
@@ -37,8 +36,8 @@ __global__ void __launch_bounds__(kRowThreads) glu_kernel(GluArgs p, Eights e) {
                 f[j] = act_forward<ACT>(g[i].get(j), u[i].get(j), p.act) * w[i];
             Eight<YDT> o;
             o.set(f);
-            if (live[i])
-                o.store(y + row[i] * p.ldy + col[i]);
+            if (run.live[i])
+                o.store(y + run.at[i]);
         }
     });
 }

@@ -17,55 +17,91 @@ namespace {
 typedef uint32_t Word __attribute__((aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+// The largest magnitude of eight elements as fp32 bits (of 16-bit types two at a
+// time: their patterns are ordered alike).
 template <int DT>
+__device__ __forceinline__ uint32_t top_of(const Eight<DT>& x) {
+    if constexpr (DT == GG_F32) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t a = __builtin_bit_cast(uint32_t, x.get(i)) & 0x7FFFFFFFu;
+            top = a > top ? a : top;
+        }
+        return top;
+    } else {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        auto abs2 = [&](int i) { return __builtin_bit_cast(u16x2, (uint32_t)x.v[0].raw[i] & 0x7FFF7FFFu); };
+        const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(abs2(0), abs2(1)),
+                                                  __builtin_elementwise_max(abs2(2), abs2(3)));
+        const uint16_t top = m[0] > m[1] ? m[0] : m[1];
+        return __builtin_bit_cast(uint32_t, to_f32<DT>(top));
+    }
+}
+
+// Eight elements over 2^e, scale = 2^e, as codes: rounded to nearest even.
+template <int DT>
+__device__ __forceinline__ uint32_t codes_of(const Eight<DT>& x, float scale) {
+    uint32_t c = 0;
+    if constexpr (DT == GG_F32) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x.get(0), x.get(1), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x.get(2), x.get(3), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x.get(4), x.get(5), scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x.get(6), x.get(7), scale, 3);
+    } else if constexpr (DT == GG_BF16) {
+        typedef __bf16 Two __attribute__((ext_vector_type(2)));
+        auto two = [&](int i) { return __builtin_bit_cast(Two, (uint32_t)x.v[0].raw[i]); };
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(0), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(1), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(2), scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(3), scale, 3);
+    } else {
+        typedef _Float16 Two __attribute__((ext_vector_type(2)));
+        auto two = [&](int i) { return __builtin_bit_cast(Two, (uint32_t)x.v[0].raw[i]); };
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, two(0), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, two(1), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, two(2), scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, two(3), scale, 3);
+    }
+    return c;
+}
+
+template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kRowThreads) quant_kernel(QuantArgs p, Eights e) {
     typedef typename Elem<DT>::T T;
     const T* const x = (const T*)p.x;
-    for_eights(e, p.end, [&](const int64_t (&row)[kUnroll], const uint32_t (&col)[kUnroll],
-                             const int64_t (&v)[kUnroll], const bool (&live)[kUnroll]) {
+    for_eights<FLAT>(e, p.ld, p.end, [&](const Run& run) {
         Eight<DT> in[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; u++)
-            in[u].load(x + row[u] * p.ld + col[u]);
+            in[u].load(x + run.at[u]);
 #pragma unroll
         for (int u = 0; u < kUnroll; u++) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint32_t a = __builtin_bit_cast(uint32_t, in[u].get(i)) & 0x7FFFFFFFu;
-                top = a > top ? a : top;
-            }
-            top = group_all<4>(top, OpMaxU());
+            const uint32_t top = group_all<4>(top_of<DT>(in[u]), OpMaxU());
             const bool odd = top >= 0x7F800000u;         // an infinity or a NaN
             // the exponent field, one more where f > 1/2, less 2
             const uint32_t up = (top + 0x3FFFFFu) >> 23;
             const uint32_t s = odd ? 255u : (up > 2u ? up - 2u : 0u);
-            const float scale = __builtin_bit_cast(float, s << 23);
-            uint32_t c = 0;
-            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(0), in[u].get(1), scale, 0);
-            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(2), in[u].get(3), scale, 1);
-            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(4), in[u].get(5), scale, 2);
-            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, in[u].get(6), in[u].get(7), scale, 3);
-            if (live[u]) {
-                *(Word*)(p.codes + v[u] * 4) = odd ? 0u : c;
+            const uint32_t c = codes_of<DT>(in[u], __builtin_bit_cast(float, s << 23));
+            if (run.live[u]) {
+                *(Word*)(p.codes + run.v[u] * 4) = odd ? 0u : c;
                 if ((threadIdx.x & 3) == 0)
-                    p.scales[v[u] >> 2] = (uint8_t)s;
+                    p.scales[run.v[u] >> 2] = (uint8_t)s;
             }
         }
     });
 }
 
-template <int DT>
+template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kRowThreads) dequant_kernel(QuantArgs p, Eights e) {
     typedef typename Elem<DT>::T T;
     T* const out = (T*)p.x;
-    for_eights(e, p.end, [&](const int64_t (&row)[kUnroll], const uint32_t (&col)[kUnroll],
-                             const int64_t (&v)[kUnroll], const bool (&live)[kUnroll]) {
+    for_eights<FLAT>(e, p.ld, p.end, [&](const Run& run) {
         uint32_t c[kUnroll], s[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; u++) {
-            c[u] = *(const Word*)(p.codes + v[u] * 4);
-            s[u] = p.scales[v[u] >> 2];
+            c[u] = *(const Word*)(p.codes + run.v[u] * 4);
+            s[u] = p.scales[run.v[u] >> 2];
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; u++) {
@@ -77,8 +113,8 @@ __global__ void __launch_bounds__(kRowThreads) dequant_kernel(QuantArgs p, Eight
             const float f[8] = {a[0], a[1], b[0], b[1], d[0], d[1], g[0], g[1]};
             Eight<DT> o;
             o.set(f);
-            if (live[u])
-                o.store(out + row[u] * p.ld + col[u]);
+            if (run.live[u])
+                o.store(out + run.at[u]);
         }
     });
 }
@@ -96,26 +132,34 @@ hipError_t by_dtype(const char* name, const QuantArgs& p, int dtype, LaunchInfo*
         info->waves = kRowThreads / 64;
         info->grid = grid;
     }
+    auto by_pitch = [&](auto DT) {
+        if (p.ld == p.width)
+            launch(DT, std::true_type(), e, grid);
+        else
+            launch(DT, std::false_type(), e, grid);
+    };
     if (dtype == GG_BF16)
-        launch(std::integral_constant<int, GG_BF16>(), e, grid);
+        by_pitch(std::integral_constant<int, GG_BF16>());
     else if (dtype == GG_F16)
-        launch(std::integral_constant<int, GG_F16>(), e, grid);
+        by_pitch(std::integral_constant<int, GG_F16>());
     else
-        launch(std::integral_constant<int, GG_F32>(), e, grid);
+        by_pitch(std::integral_constant<int, GG_F32>());
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_quant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
-    return by_dtype("quant_kernel", p, dtype, info, [&](auto DT, const Eights& e, unsigned grid) {
-        hipLaunchKernelGGL((quant_kernel<decltype(DT)::value>), dim3(grid), dim3(kRowThreads), 0, s, p, e);
+    return by_dtype("quant_kernel", p, dtype, info, [&](auto DT, auto FLAT, const Eights& e, unsigned grid) {
+        hipLaunchKernelGGL((quant_kernel<decltype(DT)::value, decltype(FLAT)::value>), dim3(grid), dim3(kRowThreads), 0, s,
+                           p, e);
     });
 }
 
 hipError_t launch_dequant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo* info) {
-    return by_dtype("dequant_kernel", p, dtype, info, [&](auto DT, const Eights& e, unsigned grid) {
-        hipLaunchKernelGGL((dequant_kernel<decltype(DT)::value>), dim3(grid), dim3(kRowThreads), 0, s, p, e);
+    return by_dtype("dequant_kernel", p, dtype, info, [&](auto DT, auto FLAT, const Eights& e, unsigned grid) {
+        hipLaunchKernelGGL((dequant_kernel<decltype(DT)::value, decltype(FLAT)::value>), dim3(grid), dim3(kRowThreads), 0, s,
+                           p, e);
     });
 }
 
