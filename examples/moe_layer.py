@@ -6,6 +6,7 @@ input times the choice's weight, then W2), the balance loss.  A step runs
   forward   gg_route   logits -> experts, weights, counts, balance loss
             gg_plan, gg_permute   tokens -> rows sorted by expert, padded to 256
             (the two forward products: torch, expert by expert)
+            gg_glu       the activation between them
             gg_combine   rows -> tokens
   backward  gg_permute   the output's gradient -> rows
             gg_dglu      through W2 and the activation; the weights' gradient
@@ -15,7 +16,15 @@ input times the choice's weight, then W2), the balance loss.  A step runs
             gg_route_bwd the logits' gradient, from the weights' and the loss's
   update    gg_grad_norm, gg_grad_clip over the three weights' gradients
 
-Run it (on an MI355X) for a few steps of gradient descent on random data:
+Mx4Experts is the trained layer for inference, its weights in 4 bits:
+
+  a batch   gg_plan, gg_permute   tokens -> rows sorted by expert
+            gg_mx4_quant, gg_gemm_mx4, gg_glu, gg_mx4_quant, gg_gemm_mx4
+            gg_combine   rows -> tokens, weighted
+  a few     gg_moe_few   up to 64 tokens, in one call
+
+Run it (on an MI355X) for a few steps of gradient descent on random data, and
+the trained layer in 4 bits:
     python examples/moe_layer.py
 """
 import os
@@ -60,7 +69,8 @@ class MoELayer:
                 torch.mm(rows[begin:end], weights[e], out=out[begin:end])
             begin = end
 
-    def forward(self, x):
+    def route(self, x):
+        """The choices of x's tokens (self.ids), their weights and the balance loss."""
         T, E, k = x.shape[0], self.E, self.k
         self.x = x
         self.logits = (x @ self.router.t()).float()
@@ -68,6 +78,11 @@ class MoELayer:
         prob, balance = torch.empty(T, k, device=self.dev), torch.empty(1, device=self.dev)
         gg.gg_route(self.logits, self.ids, prob, self.counts, self.routed, balance,
                     flags=gg.GG_FLAG_NORMALIZE)
+        return prob, balance
+
+    def forward(self, x):
+        T, E, k = x.shape[0], self.E, self.k
+        prob, balance = self.route(x)
 
         m = gg.gg_plan_max_rows(T, k, E)
         self.kept, self.ends, self.row_of = self._int(E), self._int(E), self._int(T, k)
@@ -82,9 +97,8 @@ class MoELayer:
         self.x_rows, self.prob_rows = x_rows[:n], prob_rows[:n]
         self.c = torch.empty(n, 2 * self.I, dtype=x.dtype, device=self.dev)
         self._products(self.x_rows, self.w1, self.c)
-        pair = self.c.float().view(n, self.I // 32, 2, 32)
-        act = pair[:, :, 0] * torch.nn.functional.silu(pair[:, :, 1]) * self.prob_rows[:, None, None]
-        self.act = act.reshape(n, self.I).to(x.dtype)
+        self.act = torch.empty(n, self.I, dtype=x.dtype, device=self.dev)
+        gg.gg_glu(self.c, self.act, prob=self.prob_rows)
         y_rows = torch.empty(n, self.H, dtype=x.dtype, device=self.dev)
         self._products(self.act, self.w2, y_rows)
         out = torch.empty_like(x)
@@ -125,6 +139,59 @@ class MoELayer:
         return norm
 
 
+class Mx4Experts:
+    """A layer's experts for inference, weights in MXFP4 with the reduction axis
+    along the rows: w1 (E, 2I, H), w2 (E, H, I)."""
+
+    def __init__(self, layer):
+        self.H, self.I, self.E, self.dev = layer.H, layer.I, layer.E, layer.dev
+        self.w1, self.sf1 = self._rows(layer.w1.transpose(1, 2).reshape(-1, self.H), (self.E, 2 * self.I, self.H))
+        self.w2, self.sf2 = self._rows(layer.w2.transpose(1, 2).reshape(-1, self.I), (self.E, self.H, self.I))
+
+    def _rows(self, x, shape=None, end=None):
+        """The MXFP4 codes and scales of x's rows up to `end`."""
+        n, width = x.shape
+        codes = torch.empty(n, width // 2, dtype=torch.uint8, device=self.dev)
+        scales = torch.empty(n, width // 32, dtype=torch.uint8, device=self.dev)
+        gg.gg_mx4_quant(x, codes, scales, end=end)
+        if shape is None:
+            return codes, scales
+        return codes.view(*shape[:2], shape[2] // 2), scales.view(*shape[:2], shape[2] // 32)
+
+    def __call__(self, x, ids, prob):
+        """The experts' weighted sum for x's tokens with these choices."""
+        if x.shape[0] > 64:
+            return self.batch(x, ids, prob)
+        y = torch.empty_like(x)
+        gg.gg_moe_few(x, ids, prob, self.w1, self.w2, y, sf1=self.sf1, sf2=self.sf2)
+        return y
+
+    def batch(self, x, ids, prob):
+        """The same with activations in MXFP4 too, for any number of tokens, H and I
+        multiples of 128.  The buffers hold all the rows that the choices can need;
+        nothing is read back: the calls take the rows in use from the last end."""
+        (T, k), E = ids.shape, self.E
+        i32 = dict(dtype=torch.int32, device=self.dev)
+        m = gg.gg_plan_max_rows(T, k, E, granule=1)
+        counts, self.ends, self.row_of = torch.empty(E, **i32), torch.empty(E, **i32), torch.empty(T, k, **i32)
+        gg.gg_plan(ids, counts, self.ends, self.row_of, m, granule=1)
+        bf16 = dict(dtype=torch.bfloat16, device=self.dev)
+        self.x_rows = torch.empty(m, self.H, **bf16)
+        gg.gg_permute(x, self.row_of, counts, self.ends, self.x_rows)
+        end = self.ends[-1:]
+        self.a = self._rows(self.x_rows, end=end)
+        self.c = torch.empty(m, 2 * self.I, **bf16)
+        gg.gg_gemm_mx4(*self.a, self.w1, self.sf1, self.ends, self.c)
+        self.act = torch.empty(m, self.I, **bf16)
+        gg.gg_glu(self.c, self.act, end=end)
+        self.h = self._rows(self.act, end=end)
+        self.y_rows = torch.empty(m, self.H, **bf16)
+        gg.gg_gemm_mx4(*self.h, self.w2, self.sf2, self.ends, self.y_rows)
+        y = torch.empty_like(x)
+        gg.gg_combine(self.y_rows, self.row_of, y, weights=prob)
+        return y
+
+
 def main(steps=5, tokens=4096, hidden=1024, inner=512, experts=16, top_k=2):
     layer = MoELayer(hidden, inner, experts, top_k)
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -139,7 +206,19 @@ def main(steps=5, tokens=4096, hidden=1024, inner=512, experts=16, top_k=2):
             w.sub_(20.0 * d)
         print(f"step {step}: loss {float(err.square().mean()):.4f}, balance {float(balance):.4f}, "
               f"gradient norm {float(norm[0]):.5f}, factor {float(norm[1]):.3f}", flush=True)
+    return layer, x
+
+
+def in_4_bits(layer, x, few=16):
+    """How far 4-bit experts take the layer's output, for a few tokens and all."""
+    experts = Mx4Experts(layer)
+    for n in (few, x.shape[0]):
+        out, _ = layer.forward(x[:n])
+        prob, _ = layer.route(x[:n])
+        y = experts(x[:n], layer.ids, prob)
+        off = float((y.float() - out.float()).norm() / out.float().norm())
+        print(f"{n} tokens with the experts in 4 bits: {off:.3f} of the output's norm away", flush=True)
 
 
 if __name__ == "__main__":
-    main()
+    in_4_bits(*main())
