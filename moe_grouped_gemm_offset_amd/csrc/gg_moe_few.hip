@@ -1,28 +1,38 @@
 // gg_moe_few.hip -- a whole mixture-of-experts layer for up to 64 tokens
-// (gg_moe_few): every weight of a chosen expert is read once, so the layer
-// costs what reading them costs.
+// (gg_moe_few): the layer costs what reading the chosen experts' weights costs.
 //
-// Two passes of one kernel, then the sum over a token's choices:
 //   first    c = w1_e x, h = prob act(c + bias1), for every (token, choice)
 //   second   w2_e h + prob bias2, for every (token, choice)
-// (The sum by the last block of some rows, which saves the launch, took longer:
-// every block then awaits its results and counts itself, 5 us of one token's
-// second pass for the 4 of the launch, 60 us of 64 tokens'.)
+//   sum      y = the sum over a token's choices
+//
 // A wave takes 32 rows of one chosen expert's matrix (in the first pass 16 input
 // rows and the 16 gate rows that go with them) and streams them from memory into
 // the registers that the matrix instruction reads, as its 16-row operand
 // (16x16x32, bf16); 4-bit weights are widened to bf16, which holds each exactly.
-// The tokens of the expert are the 16 columns, from LDS, where the block's waves
-// share them.  The waves of a block have different rows, or, where there are too
-// few rows to fill the device, WK of them the same rows and parts of the
-// reduction axis, added up in LDS.
+// The tokens of the expert are the 16 columns.
+//
+// Tokens that share experts (few_kernel, few_sum_kernel): a block stands for an
+// expert, so that its weights are read once; the waves share the columns in LDS.
+// They have different rows, or, where there are too few rows to fill the device,
+// WK of them the same rows and parts of the reduction axis, added up in LDS.
+// (The sum by the last block of some rows, which saves the launch, took longer:
+// every block then awaits its results and counts itself, 5 us of one token's
+// second pass for the 4 of the launch, 60 us of 64 tokens'.)
+//
+// Few tokens, whose choices share little (lone_first_kernel, lone_second_kernel): a
+// wave takes rows of one choice's expert, with its columns in LDS of its own, so
+// none waits for another on the way, and a token's choices meet in one block of
+// the second pass, which leaves no third.  One token over 64 experts of 4096 x
+// 2048, 8 choices, weights from memory: MXFP4 49 us for 54, bf16 127 for 140.
 //
 // What a CU's load path takes is lines: a vector load of 8 rows x 128 bytes
-// costs half of one of 16 rows x 64 bytes.  So 16 rows x 128 bytes come in two
-// loads of 8 whole lines, and lanes r and r + 8 of every 16 then exchange a half
-// (a DPP move a register), which leaves each lane 16-byte pieces of its own row.
-// The scales of 4 lines (32 bytes of a row) come in one load, 8 bytes a lane, and
-// go to the lanes by row swaps.
+// costs half of one of 16 rows x 64 bytes.  So 16 bf16 rows x 128 bytes come in
+// two loads of 8 whole lines, and lanes r and r + 8 of every 16 then exchange a
+// half (a DPP move a register), which leaves each lane 16-byte pieces of its own
+// row.  4-bit rows come as halves of lines, a quarter of the bytes for the same
+// arithmetic: there the moves cost what the lines save (64 experts of 4096 x 2048, one
+// token, both passes: 28.7 us with them, 28.2 without).  Their scales come in one load for
+// 2 lines, 4 bytes a lane, and go to the lanes by row swaps.
 //
 // h is kept as the sum of `parts` bf16 values, 2 for a 16-bit y (16 bits of h),
 // 3 for an fp32 one (24 bits): the second pass takes them as so many columns and
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
     // Blocks start at different pieces: at the same one they would all read the
     // same few of the memory's channels (rows are powers of two apart: 441 us for
     // 355 on the bf16 first pass of 64 tokens over 64 experts of 4096 x 2048).
-    const int start = (blockIdx.x + blockIdx.y) % steps;
+    const int start = (blockIdx.x + e) % steps;
     auto turn = [&](int t) { return t >= steps ? steps : (t + start >= steps ? t + start - steps : t + start); };
 
     constexpr int kLines = C::kLines;
@@ -446,6 +456,264 @@ __global__ void __launch_bounds__(256) few_sum_kernel(FewArgs p) {
     }
 }
 
+// The most choices that a token's block has waves for.
+constexpr int kLoneK = 8;
+
+// Whether the choices go each for itself: up to 4 tokens, or half as many choices
+// as experts, and not more choices than experts (from memory, us, apart / shared;
+// experts of 4096 x 2048: 4 tokens, 8 of 64, MXFP4 129 / 139, bf16 313 / 327; 8 tokens, 4 of
+// 64, 131 / 138 and 314 / 322; 6 tokens, 8 of 64, 167 / 161 and 430 / 396).
+bool lone(const FewArgs& p) {
+    const int pairs = p.T * p.k;
+    return p.k <= kLoneK && pairs <= p.E && (p.T <= 4 || 2 * pairs <= p.E);
+}
+
+// Few tokens with choices of their own: a wave takes 16 RB rows of one choice's
+// expert (the blocks of 16 `apart` rows from one another), or every WK-th piece of
+// them, against COLS columns, at its own pace: no wave waits for another before
+// their sum.  Its columns pass through its own region of LDS.
+template <bool MX4, int RB, int COLS>
+struct Lone {
+    // a piece: 2 lines of every row (4: 50 for 49 us, and 130 for 127, of the calls
+    // at the head), and as many values of the columns
+    static constexpr int LINES = 2;
+    static constexpr int F = MX4 ? 4 : 1, kBytes = 128 * LINES, kValues = MX4 ? 2 * kBytes : kBytes / 2;
+    static constexpr int kCol = 2 * kValues + 16, kX = COLS * kCol, kLds = 2 * kX;
+    static constexpr int kPer = 2 * kValues / 16, kStage = (COLS * kPer + 63) / 64;
+
+    // The wave's sums: register i of a lane is row 4 q + i of its block, column r.
+    // The rows are those of expert e (R each, of K values) from row0 on; column c's
+    // values are at x0 + c x_next (bytes).  `seed` chooses the piece that is first.
+    static __device__ __forceinline__ void run(char* lds, const void* w_all, const uint8_t* sf_all, int E, int R, int K,
+                                               int e, int row0, int apart, __amdgpu_buffer_rsrc_t rx, uint32_t x0,
+                                               uint32_t x_next, int wk, int WK, int seed, f32x4 (&acc)[RB]) {
+        const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+        const int64_t first = (int64_t)e * R + row0;
+        const uint32_t pitch = (uint32_t)(MX4 ? K / 2 : K * 2), KB = K / 32;
+        const __amdgpu_buffer_rsrc_t rw =
+            make_rsrc(uniform_ptr((const char*)w_all + first * pitch), ((RB - 1) * apart + 16) * pitch);
+        const uint8_t* const sf = sf_all + first * KB;
+        const uint32_t piece = 16 * (MX4 ? q : q + 4 * (r >> 3));
+        uint32_t row_at[RB][2];
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                row_at[rb][i] = (MX4 ? (uint32_t)(rb * apart + r) * pitch + 64 * i
+                                     : (uint32_t)(rb * apart + 8 * i + (r & 7)) * pitch) + piece;
+        const int pieces = (int)((pitch + kBytes - 1) / kBytes), steps = (pieces + WK - 1) / WK;
+        const int start = seed % steps;
+        auto turn = [&](int i) { return i >= steps ? steps : (i + start >= steps ? i + start - steps : i + start); };
+        u32x4 w[LINES][RB][2], xr[kStage];
+        uint32_t sc[RB], next_sc[RB];
+        // (past the row's end as in few_kernel, the scales too)
+        auto load_line = [&](int i, int l) {
+            const uint32_t at = (uint32_t)(i * WK + wk) * kBytes + 128 * l;
+            const bool in = MX4 || at + piece < pitch;
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    w[l][rb][h] = buf16(rw, in ? row_at[rb][h] + at : kInvalid);
+        };
+        const int64_t sf_left = ((int64_t)E * R - first) * KB - 4;
+        const uint32_t sf_last = sf_left < INT32_MAX ? (uint32_t)sf_left : INT32_MAX;
+        auto scale_at = [&](int i) { return (uint32_t)(i * WK + wk) * 16 + 4 * q; };
+        auto load_scales = [&](int i, uint32_t (&v)[RB]) {
+            typedef uint32_t Four __attribute__((aligned(1)));
+            if constexpr (MX4)
+#pragma unroll
+                for (int rb = 0; rb < RB; rb++)
+                    v[rb] = *(const Four*)(sf + min((rb * apart + r) * KB + scale_at(i), sf_last));
+        };
+        auto row_scales = [&](int i, int rb, uint32_t v, uint32_t (&out)[4]) {
+            const uint32_t in_row = scale_at(i), at = (rb * apart + r) * KB + in_row;
+            const uint32_t past = at > sf_last ? at - sf_last : 0;
+            uint32_t x = v >> (8 * (past & 3));
+            if (in_row + 4 > KB)
+                x = in_row < KB ? x & ((1u << (8 * (KB - in_row))) - 1) : 0;
+            spread4(x, out);
+        };
+        uint32_t x_at[kStage], x_lds[kStage];
+        int x_k[kStage];
+#pragma unroll
+        for (int i = 0; i < kStage; i++) {
+            const int c = lane + 64 * i, col = c / kPer, k = c % kPer * 8;
+            x_k[i] = col < COLS ? k : INT32_MAX / 2;
+            x_at[i] = x0 + col * x_next + k * 2;
+            x_lds[i] = min(col, COLS - 1) * kCol + k * 2;
+        }
+        auto load_x = [&](int i) {
+            const int k0 = (i * WK + wk) * kValues;
+#pragma unroll
+            for (int c = 0; c < kStage; c++)
+                xr[c] = buf16(rx, k0 + x_k[c] < K ? x_at[c] + k0 * 2 : kInvalid);
+        };
+        auto store_x = [&](int i) {
+#pragma unroll
+            for (int c = 0; c < kStage; c++)
+                if (COLS * kPer % 64 == 0 || lane + 64 * c < COLS * kPer)
+                    *(u32x4*)(lds + (i & 1) * kX + x_lds[c]) = xr[c];
+            wave_sync();
+        };
+        const uint32_t col_at = (r < COLS ? r : 0) * kCol + q * (MX4 ? 64 : 16);
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++)
+            acc[rb] = f32x4{0};
+        load_x(turn(0));
+        load_scales(turn(0), sc);
+#pragma unroll
+        for (int l = 0; l < LINES; l++)
+            load_line(turn(0), l);
+        for (int i = 0; i < steps; i++) {
+            const int next = turn(i + 1);
+            store_x(i);
+            load_x(next);
+            load_scales(next, next_sc);
+            const char* const xb = lds + (i & 1) * kX + col_at;
+            uint32_t scale[RB][4];
+            if constexpr (MX4)
+#pragma unroll
+                for (int rb = 0; rb < RB; rb++)
+                    row_scales(turn(i), rb, sc[rb], scale[rb]);
+#pragma unroll
+            for (int l = 0; l < LINES; l++) {
+                u32x4 wv[RB][2];
+#pragma unroll
+                for (int rb = 0; rb < RB; rb++) {
+                    if constexpr (MX4)
+                        wv[rb][0] = w[l][rb][0], wv[rb][1] = w[l][rb][1];
+                    else
+                        own_rows(r < 8, w[l][rb][0], w[l][rb][1], wv[rb]);
+                }
+                if constexpr (!MX4)
+                    load_line(next, l);
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+#pragma unroll
+                    for (int f = 0; f < F; f++) {
+                        const bf16x8 xf = __builtin_bit_cast(
+                            bf16x8, *(const u32x4*)(xb + (2 * l + h) * (MX4 ? 256 : 64) + f * 16));
+#pragma unroll
+                        for (int rb = 0; rb < RB; rb++) {
+                            bf16x8 wf;
+                            if constexpr (MX4)
+                                wf = widen(wv[rb][h][f], __builtin_bit_cast(float, __builtin_amdgcn_ubfe(
+                                                             scale[rb][2 * l + h], 8 * q, 8) << 23));
+                            else
+                                wf = __builtin_bit_cast(bf16x8, wv[rb][h]);
+                            acc[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf, acc[rb], 0, 0, 0);
+                        }
+                    }
+                if constexpr (MX4)
+                    load_line(next, l);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++)
+                sc[rb] = next_sc[rb];
+        }
+    }
+};
+
+// h of choice blockIdx.y: a block takes 4 / WK times 16 inputs and their gates.
+template <bool MX4, int WK, int ACT>
+__global__ void __launch_bounds__(256) lone_first_kernel(FewArgs p) {
+    using S = Lone<MX4, 2, 1>;
+    constexpr int NW = 4, WR = NW / WK;
+    __shared__ __attribute__((aligned(16))) char smem[NW][S::kLds];
+    __shared__ f32x4 sum[NW][2][4];
+    const int pair = blockIdx.y;
+    if (blockIdx.x == 0 && pair == 0 && threadIdx.x == 0)
+        *(int32_t*)p.ws = 0;                           // the error word
+    const int e = scalar_read(p.ids + pair);
+    if ((uint32_t)e >= (uint32_t)p.E)
+        return;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int units = p.I / 16;
+    const int unit = min((int)blockIdx.x * WR + wave / WK, units - 1);
+    const uint32_t token = (uint32_t)pair * p.k_magic >> 16;
+    // a finishing thread's row of its unit, and what it needs there
+    const int mu = blockIdx.x * WR + threadIdx.x / 16, mr = threadIdx.x % 16;
+    const bool finishes = threadIdx.x < 16 * WR && mu < units;
+    float v[2] = {0, 0}, prob = 0;
+    if (finishes) {
+        prob = p.prob[pair];
+        if (p.bias1)
+#pragma unroll
+            for (int rb = 0; rb < 2; rb++)
+                v[rb] = p.bias1[(int64_t)e * 2 * p.I + mu / 2 * 64 + mu % 2 * 16 + 32 * rb + mr];
+    }
+    f32x4 acc[2];
+    S::run(smem[wave], p.w1, p.sf1, p.E, 2 * p.I, p.H, e, unit / 2 * 64 + unit % 2 * 16, 32, make_rsrc(p.x),
+           token * (uint32_t)p.ldx * 2, 0, wave % WK, WK, blockIdx.x + e, acc);
+    if (r == 0)
+#pragma unroll
+        for (int rb = 0; rb < 2; rb++)
+            sum[wave][rb][q] = acc[rb];
+    __syncthreads();
+    if (!finishes)
+        return;
+#pragma unroll
+    for (int rb = 0; rb < 2; rb++)
+#pragma unroll
+        for (int i = 0; i < WK; i++)
+            v[rb] += sum[threadIdx.x / 16 * WK + i][rb][mr >> 2][mr & 3];
+    const float g = p.act.gate_first ? v[0] : v[1];
+    float h = act_forward<ACT>(g, p.act.gate_first ? v[1] : v[0], p.act) * prob;
+    uint16_t* at = (uint16_t*)(p.ws + kWsHeader) + (int64_t)pair * p.I + mu * 16 + mr;
+    for (int part = 0; part < p.parts; part++, at += (int64_t)p.T * p.k * p.I) {
+        *at = (uint16_t)f32_to_bf16(h);                // (nothing is left of an infinity)
+        h = fabsf(h) < INFINITY ? h - bf16_to_f32(f32_to_bf16(h)) : 0.0f;
+    }
+}
+
+// y[t], in place of the second pass and the sum: a block takes 16 rows of the
+// token's experts, its waves a choice each, or one of WK parts of it.
+template <bool MX4, int DT>
+__global__ void __launch_bounds__(64 * kLoneK) lone_second_kernel(FewArgs p, int WK) {
+    constexpr int NW = kLoneK, PARTS = DT == GG_F32 ? 3 : 2;
+    using S = Lone<MX4, 1, PARTS>;
+    __shared__ __attribute__((aligned(16))) char smem[NW][S::kLds];
+    __shared__ f32x4 sum[NW][PARTS][4];
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int t = blockIdx.y, row0 = 16 * blockIdx.x, wk = wave % WK, j = wave / WK;
+    const int pair = t * p.k + min(j, p.k - 1);
+    const int e = scalar_read(p.ids + pair);
+    f32x4 acc[1] = {f32x4{0}};
+    if (j < p.k && (uint32_t)e < (uint32_t)p.E) {
+        f32x4 bias = {0};
+        if (p.bias2 && wk == 0) {
+            const float prob = p.prob[pair];
+            const float* const from = p.bias2 + (int64_t)e * p.H + row0 + 4 * q;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                bias[i] = prob * from[i];
+        }
+        S::run(smem[wave], p.w2, p.sf2, p.E, p.H, p.I, e, row0, 0, make_rsrc(p.ws + kWsHeader),
+               (uint32_t)pair * p.I * 2, (uint32_t)(p.T * p.k) * p.I * 2, wk, WK, blockIdx.x + wave, acc);
+        if (r == 0)
+            acc[0] += bias;
+    }
+    if (r < PARTS)
+        sum[wave][r][q] = acc[0];
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        const int c = threadIdx.x;
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NW; i++)
+#pragma unroll
+            for (int part = 0; part < PARTS; part++)
+                y += sum[i][part][c >> 2][c & 3];
+        const int64_t at = t * p.ldy + row0 + c;
+        if constexpr (DT == GG_F32)
+            ((float*)p.y)[at] = y;
+        else
+            ((uint16_t*)p.y)[at] = (uint16_t)from_f32<DT>(y);
+    }
+}
+
 // Calls f(Few<...>()) with a block's shape for `rows` rows of `active` experts
 // (at most) and about `cols` columns of each: parts of the reduction axis until
 // three quarters of the CUs have a block, as far as the columns then fit (3
@@ -472,6 +740,43 @@ size_t few_workspace(int64_t T, int64_t k, int64_t H, int64_t I) {
     return kWsHeader + few_h_bytes(T * k, I) + (size_t)(T * k * H * 4);
 }
 
+// Both passes for choices that go each for itself.  WK of the first: parts of the
+// reduction axis until half of the CUs have a block (blocks undivided, us with 1, 2
+// and 4 parts, MXFP4: 256, 49.1 48.5 48.7; 132, 22.9 24.3 23.8; 64, 14.9 13.3 13.7; 32, 18.0
+// 15.6 13.8.  bf16: 127 128 142; 50 53 52; 22 18 17; 30 22 19).
+template <bool MX4>
+void launch_lone(const FewArgs& p, hipStream_t s) {
+    using std::integral_constant;
+    const int units = p.I / 16, pairs = p.T * p.k, enough = cu_count() / 2;
+    auto first = [&](auto WKc) {
+        constexpr int WK = decltype(WKc)::value;
+        const dim3 grid((units * WK + 3) / 4, pairs);
+        for_act(p.act.act, [&](auto ACT) {
+            hipLaunchKernelGGL((lone_first_kernel<MX4, WK, decltype(ACT)::value>), grid, dim3(256), 0, s, p);
+        });
+    };
+    const int blocks = units * pairs / 4;
+    if (blocks >= enough)
+        first(integral_constant<int, 1>());
+    else if (blocks * 2 >= enough)
+        first(integral_constant<int, 2>());
+    else
+        first(integral_constant<int, 4>());
+    int wk = 1;                                        // of the second: what k leaves
+    while (2 * wk * p.k <= kLoneK)
+        wk *= 2;
+    auto second = [&](auto DT) {
+        hipLaunchKernelGGL((lone_second_kernel<MX4, decltype(DT)::value>), dim3(p.H / 16, p.T), dim3(64 * kLoneK), 0, s,
+                           p, wk);
+    };
+    if (p.y_dtype == GG_BF16)
+        second(integral_constant<int, GG_BF16>());
+    else if (p.y_dtype == GG_F16)
+        second(integral_constant<int, GG_F16>());
+    else
+        second(integral_constant<int, GG_F32>());
+}
+
 hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
     FewArgs p = args;
     const int pairs = p.T * p.k;
@@ -484,11 +789,16 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
     const int share = pairs / p.E * 2 + 4, cols = share < p.T ? share : p.T;
     const int active = pairs < p.E ? pairs : p.E;
     if (info) {
-        snprintf(info->kernel, sizeof info->kernel, "few_kernel<%s> x 2 + sum", p.mx4 ? "mxfp4" : "bf16");
+        snprintf(info->kernel, sizeof info->kernel, lone(p) ? "lone_kernel<%s> x 2" : "few_kernel<%s> x 2 + sum",
+                 p.mx4 ? "mxfp4" : "bf16");
         info->tm = 128;
         info->tn = cols;
         info->waves = 4;
         info->grid = (int64_t)(p.I / 64) * active;
+    }
+    if (lone(p)) {
+        p.mx4 ? launch_lone<true>(p, s) : launch_lone<false>(p, s);
+        return hipGetLastError();
     }
     auto by_weights = [&](auto MX4) {
         constexpr bool mx4 = decltype(MX4)::value;

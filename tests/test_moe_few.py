@@ -249,3 +249,49 @@ def test_binding_refuses():
         a.update(bad)
         with pytest.raises(B.GGError):
             B.gg_moe_few(**a)
+
+
+# One to 8 tokens whose choices are few for the experts: 1 to 8 choices, widths of
+# less than a piece of 512 (MXFP4) or 128 (bf16) values, of whole ones and of parts;
+# rows of one wave, of several blocks, of blocks that are not full.  (Sums: a
+# choice's I terms, then at most 8 waves times 3 parts, within 2 I + 10 roundings.)
+APART = [(1, 8, 1, 32, 32), (1, 1, 1, 160, 1056), (2, 6, 3, 96, 544), (4, 32, 8, 256, 96), (3, 15, 5, 1056, 32),
+         (1, 64, 7, 544, 288), (4, 9, 2, 64, 1184), (8, 64, 4, 128, 160), (7, 64, 4, 512, 512), (1, 12, 8, 2080, 2080)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("T,E,k,H,I", APART)
+def test_choices_apart(T, E, k, H, I, mx4):
+    i = APART.index((T, E, k, H, I))
+    act, dtype, first = i % 3, DTYPES[(i + 1) // 2 % 3], i % 2 == 0
+    s = case(T, E, k, H, I, mx4, bias=i % 2 == 1, seed=50 + i, masked=(0.0, 0.3)[i % 3 == 1])
+    say("moe_few", T, E, k, H, I, mx4, act, dtype)
+    got = run(s, dtype, act, first, px=8 * (i % 3), py=(0, 3, 5)[i % 3])
+    say(f"  {check(s, got, dtype, act, first):.3f} of the tolerance")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_choices_apart_stay_apart(mx4):
+    """Ids that are no choice, an expert chosen twice, NaN and infinity in a token
+    or an expert, a spoilt workspace, and tokens in another order."""
+    s = case(4, 32, 3, 288, 352, mx4, bias=True, seed=77)
+    s["ids"] = torch.tensor([[-1, 32, 2 ** 31 - 1], [5, 5, -1], [31, 0, 7], [-2 ** 31, 2, 7]], dtype=torch.int32)
+    s["prob"][(s["ids"] < 0) | (s["ids"] > 31)] = float("nan")
+    ws = torch.full((B.gg_moe_few_workspace_size(4, 3, 288, 352),), 255, dtype=torch.uint8, device="cuda")
+    got = run(s, workspace=ws)
+    assert (got[0] == 0).all() and torch.equal(got, run(s))
+    p = torch.tensor([2, 0, 3, 1])
+    assert torch.equal(got[p], run(dict(s, x=s["x"][p], ids=s["ids"][p], prob=s["prob"][p])))
+    check(dict(s, prob=torch.nan_to_num(s["prob"])), got, torch.float32)
+    s["x"][3, 287] = float("inf")
+    s["bias1"][5, 1] = float("nan")
+    if mx4:
+        s["sf2"][31, 3, 0] = 255
+        s["sf1"][6, 0, 0] = 255                              # not chosen: its neighbour 5 ends before it
+    bad = run(s)
+    assert (bad[0] == 0).all() and torch.isnan(bad[1]).any() and not torch.isfinite(bad[3]).all()
+    assert torch.isnan(bad[2, 3]) == mx4
+    rest = torch.arange(288) != 3
+    assert torch.equal(bad[2][rest], got[2][rest])
