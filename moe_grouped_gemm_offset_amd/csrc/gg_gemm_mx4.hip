@@ -1,17 +1,22 @@
 // gg_gemm_mx4.hip -- the grouped product of MXFP4 rows and weights
 // (gg_gemm_mx4): d = alpha_g deq(a) deq(b_g)^T + bias_g over ragged groups.
 //
-// Two kernels, chosen by the rows that a group has on average:
-//  * gemm_kernel, tiles of 256 x 256 on the two-buffer main loop of the 8-bit
-//    kernels.  v_mfma_scale_f32_32x32x64_f8f6f4 takes 4-bit operands at twice
+// Two kernels (shape_of has the rule and what both measured):
+//  * gemm_kernel, tiles of 128 x 128 or 256 x 256 on the two-buffer main loop of the
+//    8-bit kernels.  v_mfma_scale_f32_32x32x64_f8f6f4 takes 4-bit operands at twice
 //    the 8-bit rate: a lane supplies one block of 32 values, 16 bytes, so a
-//    64-byte stage of a row is 128 values in two steps, and a load unit 256.
-//  * thin_kernel, for groups of few rows, where reading the weights is what
-//    costs: blocks of 64 weight rows whose waves split the reduction axis, the
-//    weights going from memory into the operand registers (as in
-//    gg_moe_few.hip).
+//    64-byte stage of a row is 128 values in two steps, and a load unit 256.  A
+//    CU has two of the small tiles at a time, one's start and end under the
+//    other's products, and reads twice the bytes a product; the large tile has
+//    the fewest.  64 groups of 4096 x 4096: 65536 rows 664 us (3310 TFLOP/s; the
+//    matrix instructions take half of a block's clocks: 3.3k clocks a unit for 2.05k of
+//    them, 15k a tile for its start and end), 512 rows 100 us (5.8 TB/s of weights).
+//  * thin_kernel, for so few tiles that most CUs would have none: the reduction
+//    axis in four, the weights going from memory into the operand registers (as
+//    in gg_moe_few.hip).
 // Groups have any number of rows: every block counts the tiles of the groups
 // (a scan over the ends by each of its waves) and finds its own.
+#include <cmath>
 #include <type_traits>
 
 #include "gg_forward.hpp"
@@ -139,7 +144,8 @@ __device__ __forceinline__ const char* scales_at(const GemmMx4Args& p, int g, in
 
 // ---- the tiled kernel --------------------------------------------------------
 
-using GemmCfg = Cfg<256, 256, 2, 2>;
+using BigTile = Cfg<256, 256, 2, 2>;
+using SmallTile = Cfg<128, 128, 2, 2>;
 
 // Scales of 8 stages (32 bytes of every tile row, 4 load units) at a time, in two
 // alternating buffers behind the unit buffers: row r of A in slot r, of B in slot
@@ -152,7 +158,8 @@ template <class C>
 struct Scales4 {
     static constexpr int kBuf = (C::TM + C::TN) * 32, kBase = 2 * C::kUnit;
     static constexpr int kSmem = kBase + 2 * kBuf > C::kLds ? kBase + 2 * kBuf : C::kLds;
-    static_assert(C::TM == 256 && C::TN == 256 && C::kWaves == 4, "a wave's load is 32 rows");
+    static constexpr int kSlices = C::TM / 64;         // units that carry a group
+    static_assert(C::TM == C::TN && kSlices <= 4 && C::kWaves == 4, "a wave's load is 32 rows");
 };
 
 template <class C>
@@ -203,7 +210,7 @@ __device__ __forceinline__ void mx4_mainloop(char* smem, const char* a, const ch
         else if (i < kLA + kLB)
             lb.template issue<ODD>(st + TM * kRowBytes, b + kb, ld - kb, i - kLA);
         else                                           // (unit 0: group 0's again)
-            scale_load(u > 0 ? (u - 1) / 4 + 1 : 0, u > 0 ? (u - 1) & 3 : 0);
+            scale_load(u > 0 ? (u - 1) / 4 + 1 : 0, u > 0 ? (u - 1) % S::kSlices : 0);
     };
     const uint32_t sh = 8 * lq;
     const int sc_a = (am0 + lr) * 32, sc_b = (TM + bn0 + lr) * 32, sc_half = lr << 1 & 16;
@@ -251,16 +258,14 @@ __device__ __forceinline__ void mx4_mainloop(char* smem, const char* a, const ch
         }
     };
     FragMx4<C> frag[2];
-    scale_load(0, 0);
-    scale_load(0, 1);
-    scale_load(0, 2);
-    scale_load(0, 3);
+#pragma unroll
+    for (int i = 0; i < S::kSlices; i++)
+        scale_load(0, i);
     pipeline<C, kLA + kLB + 1, 2 * MB * NB, MB + NB>(smem, nk, frag, issue, read, mma);
 }
 
-template <int DT, bool ODD, bool BIAS>
-__global__ void __launch_bounds__(GemmCfg::kThreads, 1) gemm_kernel(GemmMx4Args p) {
-    using C = GemmCfg;
+template <class C, int DT, bool ODD, bool BIAS>
+__global__ void __launch_bounds__(C::kThreads, C::TM == 256 ? 1 : 2) gemm_kernel(GemmMx4Args p) {
     constexpr int TM = C::TM, TN = C::TN, MB = C::MB, NB = C::NB;
     __shared__ __attribute__((aligned(1024))) char smem[Scales4<C>::kSmem];
     check_ends(p);
@@ -281,14 +286,14 @@ __global__ void __launch_bounds__(GemmCfg::kThreads, 1) gemm_kernel(GemmMx4Args 
     mx4_mainloop<C, ODD>(smem, (const char*)p.a + m0 * (p.K / 2), (const char*)p.sfa + m0 * (p.K / 32),
                          weights_at(p, g, n0), scales_at(p, g, n0), p.K, rows, cols, am0, bn0, acc);
     const float alpha = p.alpha ? p.alpha[g] : 1.0f;
-    // Rounded, then through the wave's own region of LDS, a row of the wave's 128
-    // (for fp32 half of one) behind the other, so that a store has whole lines: 16
-    // lanes the 256 bytes of a row.  Rows and columns off the tile are masked by
+    // Rounded, then through the wave's own region of LDS, so that a store has whole
+    // lines: kLanes lanes the 128 or 256 bytes of a row of the wave's.  Rows and columns off the tile are masked by
     // the descriptor.  (Against staging fp32 and rounding behind it, a third of the
-    // LDS instructions: 4k clocks a tile for 15k.)
-    constexpr int kSize = DT == GG_F32 ? 4 : 2, kPasses = kSize / 2, kJ = NB / kPasses;
-    constexpr int kPitch = 32 * kJ * kSize + 16, kRows = TM / C::WM, kWave = kRows * kPitch;
-    static_assert(kPitch == 272 && C::kWaves * kWave <= Scales4<C>::kSmem, "rows of 256 bytes");
+    // LDS instructions: a tile of 256 x 256 5k clocks, 9k where every CU writes, for 15k.)
+    constexpr int kSize = DT == GG_F32 ? 4 : 2, kJ = NB < 8 / kSize ? NB : 8 / kSize, kPasses = NB / kJ;
+    constexpr int kRow = 32 * kJ * kSize, kPitch = kRow + 16, kRows = TM / C::WM, kWave = kRows * kPitch;
+    constexpr int kLanes = kRow / 16, kAtOnce = 64 / kLanes;   // of a row; rows a store
+    static_assert(C::kWaves * kWave <= Scales4<C>::kSmem, "the waves' regions");
     char* const lds = smem + w * kWave;
     const int lane = threadIdx.x & 63, lr = lane & 31, lq = lane >> 5;
     const uint32_t pitch = (uint32_t)p.N * kSize;
@@ -328,13 +333,13 @@ __global__ void __launch_bounds__(GemmCfg::kThreads, 1) gemm_kernel(GemmMx4Args 
                 }
         }
         wave_sync();
-        const int col = n0 + bn0 + 32 * kJ * pass + 16 / kSize * (lane & 15);
-        const uint32_t at = (lane >> 4) * pitch + (uint32_t)col * kSize;
+        const int col = n0 + bn0 + 32 * kJ * pass + 16 / kSize * (lane % kLanes);
+        const uint32_t at = lane / kLanes * pitch + (uint32_t)col * kSize;
 #pragma unroll
-        for (int t4 = 0; t4 < kRows / 4; t4++) {
+        for (int i = 0; i < kRows; i += kAtOnce) {
             typedef int i32x4 __attribute__((ext_vector_type(4)));
-            const i32x4 v = *(const i32x4*)(lds + (4 * t4 + (lane >> 4)) * kPitch + 16 * (lane & 15));
-            __builtin_amdgcn_raw_buffer_store_b128(v, rd, col < p.N ? at + 4 * t4 * pitch : kInvalid, 0, 2);
+            const i32x4 v = *(const i32x4*)(lds + (i + lane / kLanes) * kPitch + 16 * (lane % kLanes));
+            __builtin_amdgcn_raw_buffer_store_b128(v, rd, col < p.N ? at + i * pitch : kInvalid, 0, 2);
         }
         wave_sync();                                   // the region is free again
     }
@@ -344,20 +349,19 @@ __global__ void __launch_bounds__(GemmCfg::kThreads, 1) gemm_kernel(GemmMx4Args 
 
 constexpr int kThinWaves = 4, kThinThreads = 64 * kThinWaves;
 
-// A wave takes 32 rows of the weights and NB blocks of 16 rows of a, piece after
-// piece of 2 lines (512 values) of each row; the next piece's loads go into the
-// registers that a line leaves.  WK waves share the rows of the weights and have
-// a part of the reduction axis each, added up in LDS: for calls with too few rows
-// of weights to fill the device.
+// 32 rows of the weights and NB blocks of 16 rows of a to a block, a quarter of the
+// reduction axis to a wave, in pieces of 2 lines (512 values) of each row; the next
+// piece's loads go into the registers that a line leaves.  The waves' sums are
+// added up in LDS.
 //
 // What a CU's load path takes is lines, so every load is one of whole lines: codes
 // 8 rows x 128 bytes (own_rows brings each lane its own row's), scales as 8 rows x
 // 128 bytes for 8 pieces, through a region of LDS of the wave's own.
-template <int WK, int NB>
+template <int NB>
 __global__ void __launch_bounds__(kThinThreads, 2) thin_kernel(GemmMx4Args p) {
-    constexpr int WR = kThinWaves / WK, kCols = 32 * WR, kBlocks = 2 + NB;   // (two blocks of b, NB of a)
+    constexpr int WK = kThinWaves, kCols = 32, kBlocks = 2 + NB;             // (two blocks of b, NB of a)
     constexpr int kAhead = 8, kPitch = 16 * kAhead + 16;                     // pieces of scales; a row of them in LDS
-    constexpr int kScales = 16 * kBlocks * kPitch, kSum = WK > 1 ? 2 * NB * 1024 : 0;
+    constexpr int kScales = 16 * kBlocks * kPitch, kSum = 2 * NB * 1024;
     __shared__ __attribute__((aligned(16))) char smem[kThinWaves][kScales > kSum ? kScales : kSum];
     check_ends(p);
     const TileAt t = tile_at<16 * NB>(p.ends, p.L, (int)p.m_rows, (p.N + kCols - 1) / kCols, blockIdx.x);
@@ -366,17 +370,14 @@ __global__ void __launch_bounds__(kThinThreads, 2) thin_kernel(GemmMx4Args p) {
     const int g = uniform(t.g), rows = uniform(t.rows);
     const int64_t m0 = uniform(t.m0);
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int wr = wave / WK, wk = wave % WK;
-    const int n0 = uniform(t.nt) * kCols + 32 * wr;
-    const bool live = n0 < p.N;                        // (of the last block's waves some may have none)
+    const int n0 = uniform(t.nt) * kCols;
     const uint32_t pitch = p.K / 2, KB = p.K / 32;
-    const int nw = live ? n0 : 0;
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(uniform_ptr(weights_at(p, g, nw)), 32 * pitch);
-    const __amdgpu_buffer_rsrc_t rsw = make_rsrc(uniform_ptr(scales_at(p, g, nw)), 32 * KB);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(uniform_ptr(weights_at(p, g, n0)), 32 * pitch);
+    const __amdgpu_buffer_rsrc_t rsw = make_rsrc(uniform_ptr(scales_at(p, g, n0)), 32 * KB);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(uniform_ptr((const char*)p.a + m0 * pitch), rows * pitch);
     const __amdgpu_buffer_rsrc_t rsx = make_rsrc(uniform_ptr((const char*)p.sfa + m0 * KB), rows * KB);
     const int pieces = (p.K + 511) / 512, steps = (pieces + WK - 1) / WK;
-    const int first = wk * steps;                      // the wave's pieces: first .. first + steps - 1
+    const int first = wave * steps;                     // the wave's pieces: first .. first + steps - 1
     // block c: rows 16 c .. of the weights, then of a
     auto rsrc = [&](int c) { return c < 2 ? rw : rx; };
     auto scale_rsrc = [&](int c) { return c < 2 ? rsw : rsx; };
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kThinThreads, 2) thin_kernel(GemmMx4Args p) {
     // register i of a lane: weight row 16 rb + 4 q + i, row 16 b + r of a
     auto store = [&](int rb, int b, f32x4 v) {
         const int row = 16 * b + r, col = n0 + 16 * rb + 4 * q;
-        if (!live || row >= rows)
+        if (row >= rows)
             return;
         const float* const bias = p.bias ? p.bias + (int64_t)g * p.N + col : nullptr;
 #pragma unroll
@@ -479,75 +480,60 @@ __global__ void __launch_bounds__(kThinThreads, 2) thin_kernel(GemmMx4Args p) {
             *(u32x2*)((uint16_t*)p.d + at) = u32x2{two(v[0], v[1]), two(v[2], v[3])};
         }
     };
-    if constexpr (WK == 1) {
+    auto sum = [&](int w, int rb, int b) { return (f32x4*)smem[w] + (rb * NB + b) * 64 + lane; };
 #pragma unroll
-        for (int rb = 0; rb < 2; rb++)
+    for (int rb = 0; rb < 2; rb++)
 #pragma unroll
-            for (int b = 0; b < NB; b++)
-                store(rb, b, acc[rb][b]);
-    } else {
-        auto sum = [&](int w, int rb, int b) { return (f32x4*)smem[w] + (rb * NB + b) * 64 + lane; };
+        for (int b = 0; b < NB; b++)
+            *sum(wave, rb, b) = acc[rb][b];
+    __syncthreads();
+    // block (rb, b) by wave rb NB + b
+    if (wave < 2 * NB) {
+        const int rb = wave / NB, b = wave % NB;
+        f32x4 v = *sum(0, rb, b);
 #pragma unroll
-        for (int rb = 0; rb < 2; rb++)
-#pragma unroll
-            for (int b = 0; b < NB; b++)
-                *sum(wave, rb, b) = acc[rb][b];
-        __syncthreads();
-        // block (rb, b) of a row of waves by the wave rb NB + b of them
-        for (int j = wk; j < 2 * NB; j += WK) {
-            const int rb = j / NB, b = j % NB;
-            f32x4 v = *sum(wr * WK, rb, b);
-#pragma unroll
-            for (int k = 1; k < WK; k++)
-                v += *sum(wr * WK + k, rb, b);
-            store(rb, b, v);
-        }
+        for (int k = 1; k < WK; k++)
+            v += *sum(k, rb, b);
+        store(rb, b, v);
     }
 }
 
-// How a call's rows are cut: blocks of 16 rows a tile and the waves that share
-// rows of the weights; nb 0: the tiled kernel.
+// How a call is cut into tiles.  tn 32: thin_kernel.
 struct Shape {
-    int nb, wk;
-    int tm() const { return nb ? 16 * nb : GemmCfg::TM; }
-    int tn() const { return nb ? 32 * kThinWaves / wk : GemmCfg::TN; }
+    int tm, tn;
+    bool thin() const { return tn == 32; }
 };
 
-// Thin up to 32 rows a group, where the weights are what costs (64 groups of 4096 x
-// 4096, thin and tiled: 8 rows 109 and 159 us, 32 rows 151 and 151, 48 rows 268 and
-// 160), and where there are too few tiles for the device, up to 2^20 elements of d
-// (8 groups of 64 rows, 2048 x 2048: 14 and 21 us; of 128: 24 and 21).  Parts of
-// the reduction axis where blocks would leave half the CUs without one (one group
-// of 16 rows, 4096 x 4096: 8 us for 17; 16 groups of 7168 x 2048, 256 blocks: 30
-// for 26).
+// Thin while its blocks do not outnumber the CUs (one group, thin and in tiles of 128:
+// 16 rows of 8192 x 8192, 256 blocks, 12.5 and 24 us; 64 rows of 4096 x 4096, 256, 11.4 and
+// 13.3; 96 rows, 384, 17 and 13; 4 groups of 16 rows, 4096 x 4096, 512, 18.7 and 15.6).
+// Else the tile for which the blocks take less, by what they take in us with u
+// units of 256 values: of 256 x 256, one on a CU, 8 + 1.8 u; of 128 x 128, of which
+// the next starts as soon as one of two ends, 2.1 + 0.57 u (in tiles of 256 and of 128:
+// 16384 rows, one group, 4096 x 4096, 146 and 164 us; 4096 rows of 2048 x 2048 23 and 16; 8
+// groups, 8192 rows, 4096 x 1024 46 and 34, 2048 x 2048 42 and 31; 64 groups of 4096 x 4096:
+// 65536 rows 660 and 786, 16384 rows 250 and 260, 512 rows 136 and 100; fp32 likewise).
+// The rows of a group are known on the device only: counted as tiles are all the
+// rows together and half a tile more for each group but one, and at least one a group.
 Shape shape_of(const GemmMx4Args& p) {
-    const int64_t each = p.m_rows / p.L;               // rows of a group, on average
-    const int64_t groups = p.m_rows < p.L ? p.m_rows : p.L;
-    if (each > 32 && p.m_rows * p.N > (1 << 20))
-        return Shape{0, 1};
-    Shape s = {each <= 16 ? 1 : 2, 1};
-    const int64_t tiles = p.m_rows / s.tm() > groups ? p.m_rows / s.tm() : groups;
-    if (tiles * ((p.N + s.tn() - 1) / s.tn()) <= cu_count() / 2)
-        s.wk = 4;
-    return s;
-}
-
-template <class F>
-void for_thin(const Shape& s, F f) {
-    using std::integral_constant;
-    if (s.nb == 1)
-        s.wk == 1 ? f(integral_constant<int, 1>(), integral_constant<int, 1>())
-                  : f(integral_constant<int, 4>(), integral_constant<int, 1>());
-    else
-        s.wk == 1 ? f(integral_constant<int, 1>(), integral_constant<int, 2>())
-                  : f(integral_constant<int, 4>(), integral_constant<int, 2>());
+    const double groups = (double)(p.m_rows < p.L ? p.m_rows : p.L), cus = cu_count(), units = p.K / 256.0;
+    auto tiles = [&](int tm, int tn) {
+        const double rows = (double)((p.m_rows + tm - 1) / tm) + (groups - 1) / 2;
+        return (rows > groups ? rows : groups) * ((p.N + tn - 1) / tn);
+    };
+    const int tm = p.m_rows / p.L <= 16 ? 16 : 32;
+    if (tiles(tm, 32) <= cus)
+        return Shape{tm, 32};
+    const double big = ceil(tiles(256, 256) / cus) * (8 + 1.8 * units);
+    const double small = (tiles(128, 128) / cus + 0.5) * (2.1 + 0.57 * units);
+    return small < big ? Shape{128, 128} : Shape{256, 256};
 }
 
 }  // namespace
 
 int64_t gemm_mx4_blocks(const GemmMx4Args& p) {
     const Shape c = shape_of(p);
-    const int64_t tiles = tile_bound(p, c.tm(), c.tn());
+    const int64_t tiles = tile_bound(p, c.tm, c.tn);
     return tiles > 1 ? tiles : 1;                      // (one block writes the error word)
 }
 
@@ -555,30 +541,34 @@ hipError_t launch_gemm_mx4(const GemmMx4Args& p, hipStream_t s, LaunchInfo* info
     const Shape c = shape_of(p);
     const dim3 grid((unsigned)gemm_mx4_blocks(p));
     if (info) {
-        snprintf(info->kernel, sizeof info->kernel, "%s<D %s>", c.nb ? "thin_kernel" : "gemm_kernel",
+        snprintf(info->kernel, sizeof info->kernel, "%s<D %s>", c.thin() ? "thin_kernel" : "gemm_kernel",
                  dtype_name(p.d_dtype));
-        info->tm = c.tm();
-        info->tn = c.tn();
-        info->waves = c.nb ? kThinWaves : GemmCfg::kWaves;
+        info->tm = c.tm;
+        info->tn = c.tn;
+        info->waves = c.thin() ? kThinWaves : BigTile::kWaves;
         info->grid = grid.x;
     }
-    if (c.nb)
-        for_thin(c, [&](auto WK, auto NB) {
-            hipLaunchKernelGGL((thin_kernel<decltype(WK)::value, decltype(NB)::value>), grid, dim3(kThinThreads), 0, s,
-                               p);
-        });
-    else {
-        const dim3 block(GemmCfg::kThreads);
+    if (c.thin()) {
+        if (c.tm == 16)
+            hipLaunchKernelGGL((thin_kernel<1>), grid, dim3(kThinThreads), 0, s, p);
+        else
+            hipLaunchKernelGGL((thin_kernel<2>), grid, dim3(kThinThreads), 0, s, p);
+    } else {
+        const dim3 block(BigTile::kThreads);
         auto by_shape = [&](auto DTc) {
             constexpr int DT = decltype(DTc)::value;
-            auto by_bias = [&](auto ODDc) {
+            auto by_bias = [&](auto tile, auto ODDc) {
+                using C = decltype(tile);
                 constexpr bool ODD = decltype(ODDc)::value;
                 if (p.bias)
-                    hipLaunchKernelGGL((gemm_kernel<DT, ODD, true>), grid, block, 0, s, p);
+                    hipLaunchKernelGGL((gemm_kernel<C, DT, ODD, true>), grid, block, 0, s, p);
                 else
-                    hipLaunchKernelGGL((gemm_kernel<DT, ODD, false>), grid, block, 0, s, p);
+                    hipLaunchKernelGGL((gemm_kernel<C, DT, ODD, false>), grid, block, 0, s, p);
             };
-            p.K % 256 ? by_bias(std::true_type()) : by_bias(std::false_type());
+            auto by_k = [&](auto tile) {
+                p.K % 256 ? by_bias(tile, std::true_type()) : by_bias(tile, std::false_type());
+            };
+            c.tm == 256 ? by_k(BigTile()) : by_k(SmallTile());
         };
         if (p.d_dtype == GG_BF16)
             by_shape(std::integral_constant<int, GG_BF16>());

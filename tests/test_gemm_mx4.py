@@ -91,10 +91,40 @@ def test_exact(sizes, K, N, dtype):
     check_exact(s, d, dtype)
 
 
+# tiles of 128 x 128 and of 256 x 256, on ragged groups, K of an odd number of
+# stages, of one unit, of several groups of scales; N off the tiles
+TILES = [(128, [130, 513, 0, 90] * 3, 384, 1056), (128, [1, 127, 128, 129] * 8, 1152, 544), (128, [700] * 4, 256, 1216),
+         (256, [2500, 1000], 128, 4064), (256, [3300, 0], 512, 4096), (256, [1700, 1999], 1920, 3872)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile,sizes,K,N", TILES, ids=lambda v: str(v)[:24].replace(" ", ""))
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_tiles(tile, sizes, K, N, dtype, monkeypatch, capfd):
+    i = TILES.index((tile, sizes, K, N))
+    s = case(sizes, K, N, seed=20 + i, tail=(7, 0)[i % 2], bias=i % 2 == 1)
+    s["sfb"] = s["sfb"] - 6                                  # (within fp16's range)
+    if s["bias"] is not None:
+        s["bias"] = s["bias"] / 64
+    monkeypatch.setenv("GG_LOG", "1")
+    d, err = run(s, dtype, ptrs=i % 3 == 1)
+    monkeypatch.setenv("GG_LOG", "0")
+    assert err == 0 and f"{tile}x{tile}" in capfd.readouterr().err
+    # (fp64 on the device: the products are exact there too)
+    a, b = mx.values(s["a"], s["sfa"]).cuda(), [mx.values(x, y).cuda() for x, y in zip(s["b"], s["sfb"])]
+    at = 0
+    for e, end in enumerate(s["ends"].tolist()):
+        w = float(s["alpha"][e]) * (a[at:end] @ b[e].T)
+        w += 0 if s["bias"] is None else s["bias"][e].double().cuda()
+        assert torch.equal(d[at:end].double(), w.float().to(dtype).double().cpu())
+        at = end
+    assert (d[at:] == 77.0).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("L,rows", [(65, 3), (700, 5), (1024, 1), (130, 100)])
 def test_many_groups(L, rows):
-    """More groups than lanes, some empty; thin and tiled."""
+    """More groups than lanes, some empty."""
     sizes = [(i * 7 % 5) * rows for i in range(L)]
     s = case(sizes, 128, 32, seed=L, tail=9)
     d, err = run(s)
