@@ -852,11 +852,13 @@ size_t gg_moe_few_workspace_size(int32_t tokens, int32_t top_k, int32_t hidden, 
  * act as for gg_glu, on rows of w1 in 32-wide blocks of inputs and gates.  An
  * id outside 0 .. num_experts-1 is no choice (its prob is not used); a token
  * without any gives 0; an expert may be chosen twice by a token.  Products with
- * fp32 accumulation; h is held as the sum of two bf16 values (16 bits) and the
- * choices are added up in fp32 in the order of j, so equal calls give equal
- * bits.  Only the chosen experts' weights are read.
+ * fp32 accumulation; h is held as the sum of two bf16 values (16 bits), for an
+ * fp32 y of three (24 bits), and the choices are added up in fp32 in a fixed
+ * order, so equal calls give equal bits.  Only the chosen experts' weights are
+ * read.
  *
- * x          (tokens, hidden) bf16, row pitch ldx >= hidden, a multiple of 8.
+ * x          (tokens, hidden) bf16, row pitch ldx >= hidden, a multiple of 8, at
+ *            most 2^23.
  * tokens     0 .. 64.  hidden, inner: multiples of 32, at most 2^16.
  *            num_experts 1..1024, top_k 1..32.
  * ids, prob  (tokens, top_k) int32 / float, as made by gg_route.

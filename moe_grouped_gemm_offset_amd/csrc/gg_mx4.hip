@@ -6,6 +6,9 @@
 // 6 = 1.5 * 2^2, the smallest e with 6 * 2^e >= largest is E - 2, or E - 1
 // where f > 1/2.  The conversion instruction divides by 2^e, rounds to nearest
 // even and packs; the division is exact, so this is the only rounding.
+//
+// Bound by memory: 65536 rows of 4096 bf16 values, 680 MB, to MXFP4 in 113 us (6.0
+// TB/s), back in 97 (7.0, the codes partly from the last-level cache).
 #include <type_traits>
 
 #include "gg_act.hpp"
