@@ -504,17 +504,21 @@ struct Shape {
     bool thin() const { return tn == 32; }
 };
 
-// Thin while its blocks do not outnumber the CUs (one group, thin and in tiles of 128:
-// 16 rows of 8192 x 8192, 256 blocks, 12.5 and 24 us; 64 rows of 4096 x 4096, 256, 11.4 and
-// 13.3; 96 rows, 384, 17 and 13; 4 groups of 16 rows, 4096 x 4096, 512, 18.7 and 15.6).
+// Thin while its blocks do not outnumber the CUs (one group, thin and in tiles of
+// 128: 16 rows of 8192 x 8192, 256 blocks, 12.5 and 24 us; 64 rows of 4096 x 4096,
+// 256, 11.4 and 13.3; 96 rows, 384, 17 and 13; 4 groups of 16 rows, 512, 18.7 and
+// 15.6).
 // Else the tile for which the blocks take less, by what they take in us with u
 // units of 256 values: of 256 x 256, one on a CU, 8 + 1.8 u; of 128 x 128, of which
-// the next starts as soon as one of two ends, 2.1 + 0.57 u (in tiles of 256 and of 128:
-// 16384 rows, one group, 4096 x 4096, 146 and 164 us; 4096 rows of 2048 x 2048 23 and 16; 8
-// groups, 8192 rows, 4096 x 1024 46 and 34, 2048 x 2048 42 and 31; 64 groups of 4096 x 4096:
-// 65536 rows 660 and 786, 16384 rows 250 and 260, 512 rows 136 and 100; fp32 likewise).
+// the next starts as soon as one of two ends, 2.1 + 0.57 u; with an fp32 d 11 and
+// 2.7 in place of 8 and 2.1.  (In tiles of 256 and of 128: one group of 16384 rows,
+// 4096 x 4096, 146 and 164 us, of 4096 rows, 2048 x 2048, 23 and 16; 8 groups, 8192
+// rows, 4096 x 1024 46 and 34, 2048 x 2048 42 and 31; 64 groups of 4096 x 4096, 65536
+// rows 660 and 786, 16384 rows 250 and 260, 512 rows 136 and 100; fp32, 8 groups,
+// 5003 rows, 2080 x 1920, 26.0 and 24.0.)
 // The rows of a group are known on the device only: counted as tiles are all the
-// rows together and half a tile more for each group but one, and at least one a group.
+// rows together and half a tile more for each group but one, and at least one a
+// group.
 Shape shape_of(const GemmMx4Args& p) {
     const double groups = (double)(p.m_rows < p.L ? p.m_rows : p.L), cus = cu_count(), units = p.K / 256.0;
     auto tiles = [&](int tm, int tn) {
@@ -524,8 +528,9 @@ Shape shape_of(const GemmMx4Args& p) {
     const int tm = p.m_rows / p.L <= 16 ? 16 : 32;
     if (tiles(tm, 32) <= cus)
         return Shape{tm, 32};
-    const double big = ceil(tiles(256, 256) / cus) * (8 + 1.8 * units);
-    const double small = (tiles(128, 128) / cus + 0.5) * (2.1 + 0.57 * units);
+    const bool wide = p.d_dtype == GG_F32;
+    const double big = ceil(tiles(256, 256) / cus) * ((wide ? 11 : 8) + 1.8 * units);
+    const double small = (tiles(128, 128) / cus + 0.5) * ((wide ? 2.7 : 2.1) + 0.57 * units);
     return small < big ? Shape{128, 128} : Shape{256, 256};
 }
 
