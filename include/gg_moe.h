@@ -791,7 +791,7 @@ gg_status gg_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t ro
  * prob       float[rows], or NULL for 1.
  * rows       0 .. 2^30.  n: a multiple of 32, at most 2^20.
  * y          output (rows, n), GG_BF16, GG_F16 or GG_F32, row pitch ldy >= n.
- * c and y aligned to their elements.
+ * c and y aligned to their elements; no element of y is one of c.
  * act and its constants  as for gg_dglu_mx.
  * flags      0 or GG_FLAG_GATE_FIRST.
  * end        as for gg_mx4_quant.

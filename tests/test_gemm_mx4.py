@@ -179,6 +179,40 @@ def test_malformed_ends(per):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tile,sizes,K,N", [(128, [300, 127, 129], 384, 1568), (128, [300, 127, 129], 512, 1568),
+                                            (256, [2500, 1000], 384, 4064), (256, [2500, 1000], 512, 4064)],
+                         ids=lambda v: str(v).replace(" ", ""))
+def test_nan_and_ends_in_tiles(tile, sizes, K, N, monkeypatch, capfd):
+    """NaN scales in the rows and columns next to a tile's edges, in the first
+    block of the row behind an odd number of stages, in rows behind the last
+    group; then ends that fall and lie past m_rows."""
+    s = case(sizes, K, N, seed=3, tail=9)
+    edge = torch.tensor([0, 1, 126, 127, 128, 255, 256, 257, s["m"] - 9])
+    s["sfa"][edge, 0] = 255
+    s["sfa"][4::97, -1] = 255
+    s["sfa"][-8:] = 255
+    s["sfb"][1, torch.tensor([0, 31, 127, 128, 255, 256, N - 1]), 0] = 255
+    s["sfb"][0, 5::61, -1] = 255
+    s["alpha"] = None
+    a, b = mx.values(s["a"], s["sfa"]).cuda(), [mx.values(x, y).cuda() for x, y in zip(s["b"], s["sfb"])]
+    m = s["m"]
+    for ends, flag in [(s["ends"].tolist(), 0), ([sizes[0], -5] + sizes[2:], 1), ([sizes[0]] + [m + 1] * (len(sizes) - 1), 4)]:
+        monkeypatch.setenv("GG_LOG", "1")
+        d, err = run(s, ends=torch.tensor(ends, dtype=torch.int32))
+        monkeypatch.setenv("GG_LOG", "0")
+        assert f"{tile}x{tile}" in capfd.readouterr().err and err in (flag, flag | 1)
+        at = 0
+        for e, end in enumerate(ends):
+            end = max(at, min(end, m))
+            w = (a[at:end] @ b[e].T).cpu()
+            assert torch.equal(torch.isnan(d[at:end]), torch.isnan(w))
+            ok = ~torch.isnan(w)
+            assert torch.equal(d[at:end][ok].double(), w[ok])
+            at = end
+        assert (d[at:] == 77.0).all()
+
+
+@pytest.mark.gpu
 def test_no_rows():
     s = case([0, 0, 0], 128, 32)
     ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")

@@ -194,15 +194,16 @@ def test_equal_calls_give_equal_bits(mx4):
 
 
 @pytest.mark.gpu
-def test_past_4_gib():
+@pytest.mark.parametrize("T", [2, 24])
+def test_past_4_gib(T):
     """The last expert's weights lie past 2^32 bytes."""
     E, H, I = 40, 8192, 4096
-    s = case(2, 1, 1, H, I, False)
+    s = case(T, 1, 1, H, I, False)
     w1 = torch.zeros(E, 2 * I, H, dtype=torch.bfloat16, device="cuda")
     w2 = torch.zeros(E, H, I, dtype=torch.bfloat16, device="cuda")
     w1[-1], w2[-1] = s["w1"][0].cuda(), s["w2"][0].cuda()
-    y = torch.zeros(2, H, device="cuda")
-    B.gg_moe_few(s["x"].cuda(), torch.full((2, 1), E - 1, dtype=torch.int32, device="cuda"), s["prob"].cuda(), w1, w2, y)
+    y = torch.zeros(T, H, device="cuda")
+    B.gg_moe_few(s["x"].cuda(), torch.full((T, 1), E - 1, dtype=torch.int32, device="cuda"), s["prob"].cuda(), w1, w2, y)
     check(s, y.cpu(), torch.float32)
 
 

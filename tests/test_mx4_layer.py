@@ -139,7 +139,7 @@ def same(a, b):
     return all(torch.equal(x, y) for x, y in zip(a, b))
 
 
-@pytest.mark.parametrize("T", [7, 50, 2000])
+@pytest.mark.parametrize("T", [2, 7, 50, 2000])
 def test_graph_replays(T):
     """Two graphs of their own buffers, captured once and replayed in turn with
     eager work in between: every replay equals the eager call bit for bit."""
