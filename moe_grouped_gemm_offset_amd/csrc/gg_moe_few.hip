@@ -37,6 +37,7 @@
 // h is kept as the sum of `parts` bf16 values, 2 for a 16-bit y (16 bits of h),
 // 3 for an fp32 one (24 bits): the second pass takes them as so many columns and
 // adds the columns' results up.
+#include <cmath>
 #include <type_traits>
 
 #include "gg_act.hpp"
@@ -714,21 +715,36 @@ __global__ void __launch_bounds__(64 * kLoneK) lone_second_kernel(FewArgs p, int
     }
 }
 
-// Calls f(Few<...>()) with a block's shape for `rows` rows of `active` experts
-// (at most) and about `cols` columns of each: parts of the reduction axis until
-// three quarters of the CUs have a block, as far as the columns then fit (3
-// tokens over 8 experts of 2048 x 1024 in bf16, first and second pass: 18.4 + 10.2
-// us undivided, 12.4 + 6.6 in two, 13.2 + 8.0 in four; one token over 64 of 4096 x
-// 2048 in MXFP4, 256 blocks undivided: 17.5 + 11.1, 18.7 + 11.4, 20.2 + 14.0); room
-// for 32 columns where 16 are too few.
+// Calls f(Few<...>()) with a block's shape for `units` pairs of row blocks, of rows
+// of K, of `active` experts (at most) and about `cols` columns of each.
+//  * Eight waves and room for 32 columns where more than `room` are likely and there
+//    are blocks enough (both passes, us, against four waves: 64 tokens, 8 of 64
+//    experts of 4096 x 2048 in bf16 553 and 622; 26 tokens, 7 of 8 of 4736 x 1184 in
+//    MXFP4 62 and 83; short rows need more blocks: 17 tokens, 4 of 8 of 2528 x 320
+//    in MXFP4, 79 of them in the second pass, 31 and 23).
+//  * Four waves for MXFP4; two for bf16 (two and four: 18 tokens, 7 of 60 of 5120 x
+//    1728, 517 and 537; 15 tokens, 6 of 32 of 4224 x 672, 112 and 123), where an
+//    expert's last block of four would have two or three waves idle (52 tokens, 8 of
+//    128 of 6112 x 416 in MXFP4 172 and 184), and where blocks of four would be fewer
+//    than half the CUs (46 tokens, 5 of 8 of 1888 x 1216 in bf16 52 and 62).
+//  * Fewer blocks and columns: parts of the reduction axis (3 tokens over 8 experts
+//    of 2048 x 1024 in bf16, first and second pass: 18.4 + 10.2 undivided, 12.4 + 6.6
+//    in two, 13.2 + 8.0 in four; 3 tokens, 6 of 16 of 5696 x 256 38 in two and 29 in
+//    four), as far as the columns fit and the parts have a piece each.
 template <bool MX4, class F>
-void for_shape(int rows, int active, int cols, F f) {
-    const int64_t blocks = (int64_t)(rows / 32) * active / 4, enough = cu_count() * 3 / 4;
-    if (cols > 16)
-        f(Few<MX4, 8, 1, 2>());
-    else if (blocks >= enough || cols > 8)
-        f(Few<MX4, 4, 1, 1>());
-    else if (blocks * 2 >= enough || cols > 4)
+void for_shape(int units, int K, int active, int cols, int room, F f) {
+    const int cus = cu_count();
+    const int64_t blocks = (int64_t)((units + 3) / 4) * active, wide = (int64_t)units * active / 8;
+    const int pieces = (K + (MX4 ? 511 : 255)) / (MX4 ? 512 : 256);
+    const int idle = -units & 3;                       // waves of an expert's last block of 4
+    if (cols > room && wide >= (pieces < 4 ? cus / 2 : cus / 4))
+        return f(Few<MX4, 8, 1, 2>());
+    if constexpr (MX4)
+        if (blocks >= cus / 2 && (cols > 8 || pieces < 2 || blocks >= cus * 3 / 4) && (idle < 2 || units >= 32))
+            return f(Few<MX4, 4, 1, 1>());
+    if (blocks >= cus * 3 / 4 || cols > 8 || pieces < 2)
+        f(Few<MX4, 2, 1, 1>());
+    else if (blocks * 2 >= cus * 3 / 4 || cols > 4 || pieces < 4)
         f(Few<MX4, 4, 2, 1>());
     else
         f(Few<MX4, 4, 4, 1>());
@@ -784,9 +800,11 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
         return hipSuccess;
     p.parts = p.y_dtype == GG_F32 ? 3 : 2;
     p.k_magic = 65536u / p.k + 1;
-    // Columns that an expert is likely to have: twice its share and a few more,
-    // at most one a token.  (More take another pass over its weights.)
-    const int share = pairs / p.E * 2 + 4, cols = share < p.T ? share : p.T;
+    // Columns that an expert is likely to have: its share and one and a half times
+    // that one's root, at most one a token.  (More take another pass over its
+    // weights.)
+    const double share = (double)pairs / p.E;
+    const int likely = (int)ceil(share + 1.5 * sqrt(share)), cols = likely < p.T ? likely : p.T;
     const int active = pairs < p.E ? pairs : p.E;
     if (info) {
         snprintf(info->kernel, sizeof info->kernel, lone(p) ? "lone_kernel<%s> x 2" : "few_kernel<%s> x 2 + sum",
@@ -802,14 +820,16 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
     }
     auto by_weights = [&](auto MX4) {
         constexpr bool mx4 = decltype(MX4)::value;
-        for_shape<mx4>(2 * p.I, active, cols, [&](auto shape) {
+        // (bf16: eight waves from 9 columns on for long rows, as above; 63 tokens, 6 of
+        // 64 experts of 768 x 576, 56 us and 49 without)
+        for_shape<mx4>(p.I / 16, p.H, active, cols, mx4 || p.H < 2048 ? 16 : 8, [&](auto shape) {
             using C = decltype(shape);
             const dim3 grid((p.I / 16 + C::WR - 1) / C::WR, active);
             for_act(p.act.act, [&](auto ACT) {
                 hipLaunchKernelGGL((few_kernel<C, decltype(ACT)::value, 1>), grid, dim3(C::kThreads), 0, s, p);
             });
         });
-        for_shape<mx4>(p.H, active, cols * p.parts, [&](auto shape) {
+        for_shape<mx4>(p.H / 32, p.I, active, cols * p.parts, 16, [&](auto shape) {
             using C = decltype(shape);
             const dim3 grid((p.H / 32 + C::WR - 1) / C::WR, active);
             if (p.parts == 2)

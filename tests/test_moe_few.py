@@ -109,7 +109,8 @@ def check(s, got, dtype, act=B.GG_DSWIGLU, gate_first=False):
 # 64; columns of one block of 16 to several passes
 SHAPES = [(1, 1, 1, 32, 32), (1, 64, 8, 256, 128), (2, 8, 2, 2048, 96), (3, 5, 3, 544, 288), (16, 4, 2, 96, 64),
           (17, 3, 2, 320, 160), (33, 2, 1, 64, 544), (64, 1, 1, 288, 96), (64, 40, 6, 512, 64), (64, 2, 2, 160, 320),
-          (9, 1024, 32, 64, 32), (64, 1024, 32, 32, 32), (5, 3, 7, 128, 64)]
+          (9, 1024, 32, 64, 32), (64, 1024, 32, 32, 32), (5, 3, 7, 128, 64), (64, 16, 8, 2112, 1120),
+          (40, 64, 2, 512, 256), (13, 20, 3, 1056, 2080), (6, 4, 9, 2048, 544)]
 DTYPES = [torch.bfloat16, torch.float16, torch.float32]
 
 
