@@ -98,6 +98,18 @@ struct Choices {
     }
 };
 
+// What the next bf16 part of h is rounded from: h, but no more than bf16's largest
+// where h is finite (an fp32 number past it would become an infinity, and h less
+// that one too).
+__device__ __forceinline__ float part_of(float h) {
+    constexpr float top = 0x1.FEp127f;
+    return fabsf(h) < INFINITY ? __builtin_amdgcn_fmed3f(h, -top, top) : h;
+}
+// What a part leaves of h (nothing of an infinity).
+__device__ __forceinline__ float less_part(float h) {
+    return fabsf(h) < INFINITY ? h - bf16_to_f32(f32_to_bf16(part_of(h))) : 0.0f;
+}
+
 // Eight 4-bit codes times 2^(s - 127), scale = s << 23.
 __device__ __forceinline__ bf16x8 widen(uint32_t codes, float scale) {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
@@ -395,10 +407,11 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
                 }
                 char* at = hbuf + ((int64_t)m.pair * p.I + m.u * 16 + 4 * m.q) * 2;
                 for (int part = 0; part < p.parts; part++, at += (int64_t)pairs * p.I * 2) {
-                    *(u32x2*)at = u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+                    *(u32x2*)at = u32x2{pack_bf16x2(part_of(h[0]), part_of(h[1])),
+                                        pack_bf16x2(part_of(h[2]), part_of(h[3]))};
 #pragma unroll
-                    for (int i = 0; i < 4; i++)        // (nothing is left of an infinity)
-                        h[i] = fabsf(h[i]) < INFINITY ? h[i] - bf16_to_f32(f32_to_bf16(h[i])) : 0.0f;
+                    for (int i = 0; i < 4; i++)
+                        h[i] = less_part(h[i]);
                 }
             }
         } else {
@@ -664,8 +677,8 @@ __global__ void __launch_bounds__(256) lone_first_kernel(FewArgs p) {
     float h = act_forward<ACT>(g, p.act.gate_first ? v[1] : v[0], p.act) * prob;
     uint16_t* at = (uint16_t*)(p.ws + kWsHeader) + (int64_t)pair * p.I + mu * 16 + mr;
     for (int part = 0; part < p.parts; part++, at += (int64_t)p.T * p.k * p.I) {
-        *at = (uint16_t)f32_to_bf16(h);                // (nothing is left of an infinity)
-        h = fabsf(h) < INFINITY ? h - bf16_to_f32(f32_to_bf16(h)) : 0.0f;
+        *at = f32_to_bf16(part_of(h));
+        h = less_part(h);
     }
 }
 

@@ -297,3 +297,50 @@ def test_choices_apart_stay_apart(mx4):
     assert torch.isnan(bad[2, 3]) == mx4
     rest = torch.arange(288) != 3
     assert torch.equal(bad[2][rest], got[2][rest])
+
+
+# --------------------------------------------------------------------------
+# h at the edges of what its bf16 parts hold
+# --------------------------------------------------------------------------
+
+# choices apart, and two tokens more than the experts allow
+EDGE = [(4, 8), (5, 2)]
+
+
+def edge_case(T, E, mx4, w2, prob, odd=None):
+    """H = I = 32, x = 0 and biases that make act = 32 sigmoid(32) 2^-5 = 1 (in fp32
+    and to 2^-46 in 64 bits) of every h; w2 everywhere; row 3 of w2 instead all 0
+    but its first, `odd`."""
+    s = dict(T=T, E=E, k=1, H=32, I=32, mx4=mx4, x=torch.zeros(T, 32).bfloat16(), bias2=None)
+    s["ids"] = (torch.arange(T, dtype=torch.int32) % E).reshape(T, 1)
+    s["prob"] = torch.tensor(prob[:T]).float().reshape(T, 1)
+    s["bias1"] = torch.cat([torch.full((E, 32), 2.0 ** -5), torch.full((E, 32), 32.0)], 1)
+    w = torch.full((E, 32, 32), w2, dtype=torch.float64)
+    if odd is not None:
+        w[:, 3] = 0.0
+        w[:, 3, 0] = odd
+    if not mx4:
+        s["w1"], s["w2"] = torch.zeros(E, 64, 32).bfloat16(), w.bfloat16()
+        s["sf1"] = s["sf2"] = None
+    else:
+        s["w1"], s["sf1"] = torch.zeros(E, 64, 16, dtype=torch.uint8), torch.full((E, 64, 1), 127, dtype=torch.uint8)
+        c, q = mx.quantise(torch.where(w.isinf(), 0.0, w).reshape(-1, 32))
+        s["w2"], s["sf2"] = c.reshape(E, 32, 16), q.reshape(E, 32, 1)
+        if odd is not None:                                  # 6 * 2^127: past bf16's largest
+            s["w2"][:, 3, 0], s["sf2"][:, 3] = 7 if odd > 0 else 15, 254
+    return s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("T,E", EDGE)
+def test_h_past_the_largest_bf16(T, E, dtype, mx4):
+    """A finite h between bf16's largest number and fp32's stays finite: y is 32
+    2^-120 h.  Errors: the activation 10 u and the product with prob u of h, its
+    parts 2^-16 (fp32 y: 2^-24), 32 terms in two or three parts 96 u; then the
+    rounding of y."""
+    s = edge_case(T, E, mx4, 2.0 ** -120, [3.4e38, -3.4e38, 3.395e38, 3.4028e38, 3.3895e38])
+    y = 32 * 2.0 ** -120 * s["prob"].double().expand(T, 32)
+    tol = ((2.0 ** -24 if dtype == torch.float32 else 2.0 ** -16) + 107 * U + HALF[dtype]) * y.abs()
+    assert ((run(s, dtype).double() - y).abs() <= tol).all()
