@@ -110,6 +110,12 @@ __device__ __forceinline__ float less_part(float h) {
     return fabsf(h) < INFINITY ? h - bf16_to_f32(f32_to_bf16(part_of(h))) : 0.0f;
 }
 
+// A sum over all parts of h, from that over the first parts alone: an infinite
+// weight makes a NaN of a part that is 0, and of parts of different signs, where its
+// product with h is an infinity, as with the first part.  (Finite weights give a NaN
+// in both or in neither.)
+__device__ __forceinline__ float over_parts(float all, float first) { return all == all ? all : first; }
+
 // Eight 4-bit codes times 2^(s - 127), scale = s << 23.
 __device__ __forceinline__ bf16x8 widen(uint32_t codes, float scale) {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
@@ -420,13 +426,14 @@ __global__ void __launch_bounds__(C::kThreads, 2) few_kernel(FewArgs p) {
                 if (m.u >= units)
                     continue;
                 const Extra x = it < C::kThreads ? early : extra(m);
-                f32x4 v = total(m.wrow, m.rb, m.q, m.which);
+                const f32x4 of_first = total(m.wrow, m.rb, m.q, m.which);
+                f32x4 v = of_first;
 #pragma unroll
                 for (int part = 1; part < PARTS; part++)
                     v += total(m.wrow, m.rb, m.q, part * kPass + m.which);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    v[i] = fmaf(x.prob, x.bias[0][i], v[i]);
+                    v[i] = fmaf(x.prob, x.bias[0][i], over_parts(v[i], of_first[i]));
                 *(f32x4*)(out + (int64_t)m.pair * p.H + m.u * 32 + 16 * m.rb + 4 * m.q) = v;
             }
         }
@@ -714,12 +721,15 @@ __global__ void __launch_bounds__(64 * kLoneK) lone_second_kernel(FewArgs p, int
     __syncthreads();
     if (threadIdx.x < 16) {
         const int c = threadIdx.x;
-        float y = 0.0f;
+        float y = 0.0f, of_first = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NW; i++)
+        for (int i = 0; i < NW; i++) {
+            of_first += sum[i][0][c >> 2][c & 3];
 #pragma unroll
             for (int part = 0; part < PARTS; part++)
                 y += sum[i][part][c >> 2][c & 3];
+        }
+        y = over_parts(y, of_first);
         const int64_t at = t * p.ldy + row0 + c;
         if constexpr (DT == GG_F32)
             ((float*)p.y)[at] = y;

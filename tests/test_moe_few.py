@@ -344,3 +344,24 @@ def test_h_past_the_largest_bf16(T, E, dtype, mx4):
     y = 32 * 2.0 ** -120 * s["prob"].double().expand(T, 32)
     tol = ((2.0 ** -24 if dtype == torch.float32 else 2.0 ** -16) + 107 * U + HALF[dtype]) * y.abs()
     assert ((run(s, dtype).double() - y).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("T,E", EDGE)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_weights(T, E, dtype, mx4, sign):
+    """An infinite weight (of MXFP4: a value past bf16's largest) times h is an
+    infinity of the product's sign, whatever is left of h after its first part
+    (nothing of 1 and 2, something of either sign of 0.3 and 0.7); a NaN where h
+    is 0.  The other rows of y are untouched."""
+    s = edge_case(T, E, mx4, 0.5, [1.0, 0.3, -0.7, 0.0, 2.0], odd=sign * float("inf"))
+    got = run(s, dtype)
+    want3 = s["prob"][:, 0].double() * sign * float("inf")
+    assert torch.equal(torch.isnan(got[:, 3]), torch.isnan(want3)) and torch.isnan(want3).sum() == 1
+    ok = ~torch.isnan(want3)
+    assert torch.equal(got[:, 3].double()[ok], want3[ok])
+    rest = torch.arange(32) != 3
+    y = 16 * s["prob"].double().expand(T, 31)
+    assert ((got[:, rest].double() - y).abs() <= (2.0 ** -16 + 107 * U + HALF[dtype]) * y.abs()).all()
