@@ -477,6 +477,12 @@ __global__ void __launch_bounds__(256) few_sum_kernel(FewArgs p) {
     }
 }
 
+// A call without tokens.
+__global__ void __launch_bounds__(64) few_none_kernel(int32_t* ws) {
+    if (threadIdx.x == 0)
+        *ws = 0;                                       // the error word
+}
+
 // The most choices that a token's block has waves for.
 constexpr int kLoneK = 8;
 
@@ -819,8 +825,10 @@ void launch_lone(const FewArgs& p, hipStream_t s) {
 hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
     FewArgs p = args;
     const int pairs = p.T * p.k;
-    if (p.T == 0)
-        return hipSuccess;
+    if (p.T == 0) {
+        hipLaunchKernelGGL(few_none_kernel, dim3(1), dim3(64), 0, s, (int32_t*)p.ws);
+        return hipGetLastError();
+    }
     p.parts = p.y_dtype == GG_F32 ? 3 : 2;
     p.k_magic = 65536u / p.k + 1;
     // Columns that an expert is likely to have: its share and one and a half times

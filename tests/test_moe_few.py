@@ -365,3 +365,14 @@ def test_infinite_weights(T, E, dtype, mx4, sign):
     rest = torch.arange(32) != 3
     y = 16 * s["prob"].double().expand(T, 31)
     assert ((got[:, rest].double() - y).abs() <= (2.0 ** -16 + 107 * U + HALF[dtype]) * y.abs()).all()
+
+
+@pytest.mark.gpu
+def test_no_tokens_clear_the_error_word():
+    """As every call on a workspace does."""
+    s = case(1, 4, 2, 64, 32, False)
+    ws = torch.full((B.gg_moe_few_workspace_size(0, 2, 64, 32),), 255, dtype=torch.uint8, device="cuda")
+    y = torch.zeros(0, 64, device="cuda")
+    used = B.gg_moe_few(s["x"].cuda()[:0], s["ids"].cuda()[:0], s["prob"].cuda()[:0], s["w1"].cuda(), s["w2"].cuda(), y,
+                        workspace=ws)
+    assert B.gg_device_error(used) == 0 and (ws[4:] == 255).all()
