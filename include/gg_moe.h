@@ -825,6 +825,8 @@ size_t gg_gemm_mx4_workspace_size(void);
  *            makes an empty group and sets GG_DEVERR_DECREASING, one past
  *            m_rows is cut off and sets GG_DEVERR_LAST.  L in 1..1024.
  * m_rows     0 .. 2^31-1.  Rows of d at or past the last end are not written.
+ *            (m_rows/256 + min(m_rows, L)) * ceil(n/256), the tiles that there
+ *            may be, are limited to 2^23 (GG_ERR_UNSUPPORTED).
  * alpha      float[L], or NULL for 1.  bias: float (L, n), or NULL.
  * d          output (m_rows, n) contiguous, GG_BF16, GG_F16 or GG_F32.
  * Codes and d 16-byte, scales, alpha and bias 4-byte aligned.

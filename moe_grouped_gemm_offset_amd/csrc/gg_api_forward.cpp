@@ -176,7 +176,7 @@ gg_status gg_gemm_mx4(const uint8_t* a_fp4, const uint8_t* sfa, int64_t m_rows, 
     p.d = d;
     p.d_dtype = d_dtype;
     p.ws = (int32_t*)workspace;
-    if (gemm_mx4_blocks(p) > (1 << 23))
+    if (gemm_mx4_blocks(p) > kMaxGemmBlocks)
         return fail(GG_ERR_UNSUPPORTED, "m_rows x n has more tiles than one launch holds");
     return go("gg_gemm_mx4", m_rows, n,
               [&](LaunchInfo* li) { return launch_gemm_mx4(p, (hipStream_t)stream, li); });

@@ -73,7 +73,9 @@ struct FewArgs {
 
 // Bytes of workspace that a gg_moe_few call uses.
 size_t few_workspace(int64_t T, int64_t k, int64_t H, int64_t I);
-// Blocks that a gg_gemm_mx4 call launches.
+// Blocks that a gg_gemm_mx4 call launches, and the most that one launch may (of 256
+// threads; a launch holds 2^32 threads).
+constexpr int64_t kMaxGemmBlocks = 1 << 23;
 int64_t gemm_mx4_blocks(const GemmMx4Args& p);
 hipError_t launch_quant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo* info);
 hipError_t launch_dequant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo* info);

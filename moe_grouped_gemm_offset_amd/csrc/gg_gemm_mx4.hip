@@ -61,6 +61,8 @@ template <int TM>
 __device__ __forceinline__ TileAt tile_at(const int32_t* ends, int L, int m_rows, int tiles_n, int q) {
     const int lane = threadIdx.x & 63, per = (L + 63) >> 6, g0 = lane * per;
     auto end_of = [&](int g) { return min(max(ends[g], 0), m_rows); };
+    // (unsigned: a group of 2^31 - 1 rows and TM - 1 more)
+    auto tiles_of = [](int rows) { return (int)(((uint32_t)rows + TM - 1) / TM); };
     int top = 0;
     for (int i = 0; i < per; i++)
         if (g0 + i < L)
@@ -70,12 +72,12 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* ends, int L, int m_rows
     start = lane ? start : 0;
     int tiles = 0;
     if (per == 1) {
-        tiles = (top - start + TM - 1) / TM;
+        tiles = tiles_of(top - start);
     } else {
         for (int i = 0, at = start; i < per; i++)
             if (g0 + i < L) {
                 const int end = max(at, end_of(g0 + i));
-                tiles += (end - at + TM - 1) / TM;
+                tiles += tiles_of(end - at);
                 at = end;
             }
     }
@@ -91,11 +93,11 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* ends, int L, int m_rows
     const int owner = __ffsll((unsigned long long)__ballot(upto > mt)) - 1;
     int before = __builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(tiles, owner);
     int begin = __builtin_amdgcn_readlane(start, owner), end = __builtin_amdgcn_readlane(top, owner);
-    int n = (end - begin + TM - 1) / TM, g = owner * per;
+    int n = tiles_of(end - begin), g = owner * per;
     if (per > 1)
         for (end = begin; g < L; g++) {
             end = max(begin, uniform(end_of(g)));
-            n = (end - begin + TM - 1) / TM;
+            n = tiles_of(end - begin);
             if (mt < before + n)
                 break;
             before += n;
@@ -516,6 +518,7 @@ struct Shape {
 // rows, 4096 x 1024 46 and 34, 2048 x 2048 42 and 31; 64 groups of 4096 x 4096, 65536
 // rows 660 and 786, 16384 rows 250 and 260, 512 rows 136 and 100; fp32, 8 groups,
 // 5003 rows, 2080 x 1920, 26.0 and 24.0.)
+// Where a launch does not hold the blocks of 128 x 128, 256 x 256 too.
 // The rows of a group are known on the device only: counted as tiles are all the
 // rows together and half a tile more for each group but one, and at least one a
 // group.
@@ -531,7 +534,8 @@ Shape shape_of(const GemmMx4Args& p) {
     const bool wide = p.d_dtype == GG_F32;
     const double big = ceil(tiles(256, 256) / cus) * ((wide ? 11 : 8) + 1.8 * units);
     const double small = (tiles(128, 128) / cus + 0.5) * ((wide ? 2.7 : 2.1) + 0.57 * units);
-    return small < big ? Shape{128, 128} : Shape{256, 256};
+    const bool holds = tile_bound(p, 128, 128) <= kMaxGemmBlocks;
+    return small < big && holds ? Shape{128, 128} : Shape{256, 256};
 }
 
 }  // namespace

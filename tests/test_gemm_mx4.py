@@ -279,3 +279,30 @@ def test_binding_refuses():
         a.update(bad)
         with pytest.raises(B.GGError):
             B.gg_gemm_mx4(**a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1 << 30, (1 << 31) - 1])
+def test_rows_by_the_billion(rows):
+    """More tiles of 128 x 128 than a launch holds: the larger ones take the call,
+    up to the most rows that there can be (132 and 264 GiB of operands)."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 133 * rows + (6 << 30):
+        pytest.skip("not enough free memory on this device")
+    K, N = 128, 32
+    g = torch.Generator().manual_seed(0)
+    pick = torch.tensor([0, 1, 255, 256, rows // 2, rows // 2 + 1, rows - 257, rows - 256, rows - 255, rows - 2, rows - 1])
+    codes, scales = mx.random_mx4(g, (len(pick), K))
+    b, sfb = mx.random_mx4(g, (1, N, K))
+    a = torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda")
+    sfa = torch.full((rows, K // 32), 127, dtype=torch.uint8, device="cuda")
+    a[pick.cuda()], sfa[pick.cuda()] = codes.cuda(), scales.cuda()
+    d = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ends = torch.tensor([rows], dtype=torch.int32, device="cuda")
+    ws = B.gg_gemm_mx4(a, sfa, b.cuda(), sfb.cuda(), ends, d)
+    assert B.gg_device_error(ws) == 0
+    w = mx.values(codes, scales) @ mx.values(b[0], sfb[0]).T
+    assert torch.equal(d[pick.cuda()].cpu().double(), w.float().bfloat16().double())
+    for at in range(2, rows, 1 << 24):                       # rows of zeros between the picked ones
+        if not bool((pick >= at).logical_and(pick < at + 64).any()):
+            assert not d[at:at + 64].any()
