@@ -606,8 +606,9 @@ def gg_grad_clip(ptrs, ends, dtypes, total, sumsq, max_norm, norm, eps=1e-6, out
 # the experts' forward pass: MXFP4, the gated activation, a few tokens' layer
 # --------------------------------------------------------------------------
 
-_CODES = (torch.uint8, torch.float4_e2m1fn_x2)
-_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+# (those that this torch has)
+_CODES = tuple(getattr(torch, t) for t in ("uint8", "float4_e2m1fn_x2") if hasattr(torch, t))
+_SCALES = tuple(getattr(torch, t) for t in ("uint8", "float8_e8m0fnu") if hasattr(torch, t))
 
 
 def _need_one(t, what, shape, dtypes, dev):

@@ -182,3 +182,23 @@ def test_binding_refuses():
                      lambda: B.gg_mx4_dequant(a["c"], a["s"], a["x"], end=a["end"])):
             with pytest.raises(B.GGError):
                 call()
+
+
+def test_a_torch_without_the_types():
+    """Where torch has no float4_e2m1fn_x2 or float8_e8m0fnu, codes and scales are
+    uint8, and every call is there."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+for name in ("float4_e2m1fn_x2", "float8_e8m0fnu"):
+    if hasattr(torch, name):
+        delattr(torch, name)
+from moe_grouped_gemm_offset_amd import binding as B
+assert B._CODES == B._SCALES == (torch.uint8,)
+assert all(hasattr(B.load_library(), name) for name in B.EXPORTS)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
