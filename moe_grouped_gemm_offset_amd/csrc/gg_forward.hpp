@@ -81,6 +81,7 @@ hipError_t launch_quant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo
 hipError_t launch_dequant(const QuantArgs& p, int dtype, hipStream_t s, LaunchInfo* info);
 hipError_t launch_glu(const GluArgs& p, int c_dtype, int y_dtype, hipStream_t s, LaunchInfo* info);
 hipError_t launch_gemm_mx4(const GemmMx4Args& p, hipStream_t s, LaunchInfo* info);
+// (info: of both passes, two)
 hipError_t launch_few(const FewArgs& p, hipStream_t s, LaunchInfo* info);
 
 }  // namespace gg

@@ -48,19 +48,21 @@ inline void report(const char* op, const LaunchInfo& info, int64_t rows, int64_t
         log_launch(op, info, shape);
 }
 
-// What every entry does last: the device check, the launch, the report.
+// What every entry does last: the device check, the launch, the report (of two
+// kernels, where the launcher names a second).
 template <class Launch>
 gg_status go(const char* op, int64_t rows, int64_t cols, Launch launch) {
     gg_status st = check_device();
     if (st != GG_OK)
         return st;
-    LaunchInfo info{};
-    LaunchInfo* li = log_enabled() ? &info : nullptr;
+    LaunchInfo info[2]{};
+    LaunchInfo* li = log_enabled() ? info : nullptr;
     const hipError_t e = launch(li);
     if (e != hipSuccess)
         return hip_fail(e, op);
     if (li)
-        report(op, info, rows, cols);
+        for (const LaunchInfo& i : info)
+            report(op, i, rows, cols);
     return ok();
 }
 

@@ -785,17 +785,34 @@ size_t few_workspace(int64_t T, int64_t k, int64_t H, int64_t I) {
     return kWsHeader + few_h_bytes(T * k, I) + (size_t)(T * k * H * 4);
 }
 
+// Reports a pass: rows x choices of a block, its waves, and which kernel it is (parts
+// of the reduction axis as "K in", of h as "h in").
+template <class... Args>
+static void few_info(LaunchInfo* info, int pass, int tm, int tn, int waves, dim3 grid, const char* format,
+                     Args... args) {
+    if (!info)
+        return;
+    info += pass;
+    snprintf(info->kernel, sizeof info->kernel, format, args...);
+    info->tm = tm;
+    info->tn = tn;
+    info->waves = waves;
+    info->grid = (int64_t)grid.x * grid.y;
+}
+static const char* few_name(bool mx4) { return dtype_name(mx4 ? GG_MXFP4 : GG_BF16); }
+
 // Both passes for choices that go each for itself.  WK of the first: parts of the
 // reduction axis until half of the CUs have a block (blocks undivided, us with 1, 2
 // and 4 parts, MXFP4: 256, 49.1 48.5 48.7; 132, 22.9 24.3 23.8; 64, 14.9 13.3 13.7; 32, 18.0
 // 15.6 13.8.  bf16: 127 128 142; 50 53 52; 22 18 17; 30 22 19).
 template <bool MX4>
-void launch_lone(const FewArgs& p, hipStream_t s) {
+void launch_lone(const FewArgs& p, hipStream_t s, LaunchInfo* info) {
     using std::integral_constant;
     const int units = p.I / 16, pairs = p.T * p.k, enough = cu_count() / 2;
     auto first = [&](auto WKc) {
         constexpr int WK = decltype(WKc)::value;
         const dim3 grid((units * WK + 3) / 4, pairs);
+        few_info(info, 0, 128 / WK, 1, 4, grid, "lone_first_kernel<%s, K in %d>", few_name(MX4), WK);
         for_act(p.act.act, [&](auto ACT) {
             hipLaunchKernelGGL((lone_first_kernel<MX4, WK, decltype(ACT)::value>), grid, dim3(256), 0, s, p);
         });
@@ -810,9 +827,10 @@ void launch_lone(const FewArgs& p, hipStream_t s) {
     int wk = 1;                                        // of the second: what k leaves
     while (2 * wk * p.k <= kLoneK)
         wk *= 2;
+    const dim3 grid(p.H / 16, p.T);
+    few_info(info, 1, 16, p.k, kLoneK, grid, "lone_second_kernel<%s, K in %d, h in %d>", few_name(MX4), wk, p.parts);
     auto second = [&](auto DT) {
-        hipLaunchKernelGGL((lone_second_kernel<MX4, decltype(DT)::value>), dim3(p.H / 16, p.T), dim3(64 * kLoneK), 0, s,
-                           p, wk);
+        hipLaunchKernelGGL((lone_second_kernel<MX4, decltype(DT)::value>), grid, dim3(64 * kLoneK), 0, s, p, wk);
     };
     if (p.y_dtype == GG_BF16)
         second(integral_constant<int, GG_BF16>());
@@ -837,16 +855,8 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
     const double share = (double)pairs / p.E;
     const int likely = (int)ceil(share + 1.5 * sqrt(share)), cols = likely < p.T ? likely : p.T;
     const int active = pairs < p.E ? pairs : p.E;
-    if (info) {
-        snprintf(info->kernel, sizeof info->kernel, lone(p) ? "lone_kernel<%s> x 2" : "few_kernel<%s> x 2 + sum",
-                 p.mx4 ? "mxfp4" : "bf16");
-        info->tm = 128;
-        info->tn = cols;
-        info->waves = 4;
-        info->grid = (int64_t)(p.I / 64) * active;
-    }
     if (lone(p)) {
-        p.mx4 ? launch_lone<true>(p, s) : launch_lone<false>(p, s);
+        p.mx4 ? launch_lone<true>(p, s, info) : launch_lone<false>(p, s, info);
         return hipGetLastError();
     }
     auto by_weights = [&](auto MX4) {
@@ -856,6 +866,7 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
         for_shape<mx4>(p.I / 16, p.H, active, cols, mx4 || p.H < 2048 ? 16 : 8, [&](auto shape) {
             using C = decltype(shape);
             const dim3 grid((p.I / 16 + C::WR - 1) / C::WR, active);
+            few_info(info, 0, 32 * C::WR, C::XC, C::NW, grid, "few_kernel<%s, first, K in %d>", few_name(mx4), C::WK);
             for_act(p.act.act, [&](auto ACT) {
                 hipLaunchKernelGGL((few_kernel<C, decltype(ACT)::value, 1>), grid, dim3(C::kThreads), 0, s, p);
             });
@@ -863,6 +874,8 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s, LaunchInfo* info) {
         for_shape<mx4>(p.H / 32, p.I, active, cols * p.parts, 16, [&](auto shape) {
             using C = decltype(shape);
             const dim3 grid((p.H / 32 + C::WR - 1) / C::WR, active);
+            few_info(info, 1, 32 * C::WR, C::XC / p.parts, C::NW, grid,
+                     "few_kernel<%s, second, K in %d, h in %d>, few_sum_kernel", few_name(mx4), C::WK, p.parts);
             if (p.parts == 2)
                 hipLaunchKernelGGL((few_kernel<C, -1, 2>), grid, dim3(C::kThreads), 0, s, p);
             else

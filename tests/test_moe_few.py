@@ -376,3 +376,89 @@ def test_no_tokens_clear_the_error_word():
     used = B.gg_moe_few(s["x"].cuda()[:0], s["ids"].cuda()[:0], s["prob"].cuda()[:0], s["w1"].cuda(), s["w2"].cuda(), y,
                         workspace=ws)
     assert B.gg_device_error(used) == 0 and (ws[4:] == 255).all()
+
+
+# --------------------------------------------------------------------------
+# every shape of a block (GG_LOG reports both passes)
+# --------------------------------------------------------------------------
+
+def logged(capfd, monkeypatch, call):
+    """(the call's result, the report's kernels)."""
+    capfd.readouterr()
+    monkeypatch.setenv("GG_LOG", "1")
+    got = call()
+    monkeypatch.setenv("GG_LOG", "0")
+    lines = [line for line in capfd.readouterr().err.splitlines() if line.startswith("[gg] gg_moe_few ")]
+    return got, [line.split(": ", 1)[1] for line in lines]
+
+
+def few_lines(s, dtype, first, second, active):
+    """What the report says of blocks of (waves, parts of K): a wave's rows are 32,
+    16 columns (eight waves: 32) are shared by the parts of K, and by those of h."""
+    name, h = "mxfp4" if s["mx4"] else "bf16", 3 if dtype == torch.float32 else 2
+    lines = []
+    for (waves, wk), units, parts, what in ((first, s["I"] // 16, 1, "first, K in {}>"),
+                                            (second, s["H"] // 32, h, "second, K in {}, h in %d>, few_sum_kernel" % h)):
+        rows = waves // wk
+        cols = (32 if waves == 8 else 16) // wk // parts
+        lines.append(f"few_kernel<{name}, {what.format(wk)}, tile {32 * rows}x{cols}, {waves} waves, "
+                     f"grid {-(-units // rows) * active}")
+    return lines
+
+
+# T, E, k, H, I; (waves, parts of K) of the first pass, of the second for a 16-bit
+# and an fp32 y, with bf16 weights and with MXFP4 ones: all nine shapes in both
+# passes, the second with two and three parts of h, on a device of 256 CUs.  Widths
+# that end within a piece, tokens without a choice, more choices of an expert than
+# a pass takes.
+BLOCKS = [
+    ((1, 1, 9, 1056, 2144), (4, 4), (4, 4), (4, 4), (4, 2), (4, 4), (4, 4)),
+    ((2, 1, 2, 2080, 2176), (4, 4), (4, 4), (4, 2), (4, 4), (4, 4), (4, 2)),
+    ((1, 1, 5, 1952, 672), (4, 4), (4, 2), (4, 2), (4, 4), (4, 2), (4, 2)),
+    ((2, 3, 3, 672, 736), (4, 2), (4, 2), (4, 2), (4, 2), (4, 2), (4, 2)),
+    ((21, 16, 2, 2080, 96), (4, 2), (2, 1), (8, 1), (4, 2), (4, 1), (8, 1)),
+    ((45, 16, 4, 64, 1056), (8, 1), (2, 1), (2, 1), (8, 1), (2, 1), (2, 1)),
+    ((24, 32, 7, 1056, 64), (2, 1), (8, 1), (8, 1), (2, 1), (8, 1), (8, 1)),
+    ((5, 5, 1, 3232, 96), (4, 4), (2, 1), (2, 1), (4, 4), (4, 1), (4, 1)),
+    ((40, 64, 2, 512, 256), (2, 1), (2, 1), (2, 1), (4, 1), (4, 1), (4, 1)),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("case_at", range(len(BLOCKS)))
+def test_block_shapes(case_at, dtype, mx4, capfd, monkeypatch):
+    shape, *ways = BLOCKS[case_at]
+    first, *second = ways[3 * mx4:][:3]
+    T, E, k, _, _ = shape
+    i = case_at
+    s = case(*shape, mx4, bias=i % 2 == 0, seed=100 + i, masked=0.1 if T > 4 else 0.0)
+    say("moe_few blocks", *shape, mx4, dtype)
+    got, lines = logged(capfd, monkeypatch, lambda: run(s, dtype, i % 3, i % 2 == 1, px=8 * (i % 2), py=i % 4))
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert lines == few_lines(s, dtype, first, second[dtype == torch.float32], min(T * k, E))
+    say(f"  {check(s, got, dtype, i % 3, i % 2 == 1):.3f} of the tolerance")
+
+
+# T, E, k, H, I; parts of K of the first pass, of the second (choices apart)
+LONE = [((1, 8, 1, 32, 32), 4, 8), ((2, 6, 3, 96, 544), 4, 2), ((4, 32, 8, 256, 96), 4, 1), ((4, 9, 2, 64, 1184), 1, 4),
+        ((8, 64, 4, 128, 160), 2, 2), ((1, 12, 8, 2080, 2080), 1, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("case_at", range(len(LONE)))
+def test_lone_shapes(case_at, dtype, mx4, capfd, monkeypatch):
+    shape, wk1, wk2 = LONE[case_at]
+    T, _, k, H, I = shape
+    s = case(*shape, mx4, bias=case_at % 2 == 1, seed=120 + case_at)
+    say("moe_few lone", *shape, mx4, dtype)
+    got, lines = logged(capfd, monkeypatch, lambda: run(s, dtype))
+    name, h = "mxfp4" if mx4 else "bf16", 3 if dtype == torch.float32 else 2
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert lines == [f"lone_first_kernel<{name}, K in {wk1}>, tile {128 // wk1}x1, 4 waves, "
+                         f"grid {(I // 16 * wk1 + 3) // 4 * T * k}",
+                         f"lone_second_kernel<{name}, K in {wk2}, h in {h}>, tile 16x{k}, 8 waves, grid {H // 16 * T}"]
+    check(s, got, dtype)
