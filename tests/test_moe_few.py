@@ -462,3 +462,52 @@ def test_lone_shapes(case_at, dtype, mx4, capfd, monkeypatch):
                          f"grid {(I // 16 * wk1 + 3) // 4 * T * k}",
                          f"lone_second_kernel<{name}, K in {wk2}, h in {h}>, tile 16x{k}, 8 waves, grid {H // 16 * T}"]
     check(s, got, dtype)
+
+
+# --------------------------------------------------------------------------
+# the third part of h
+# --------------------------------------------------------------------------
+
+PRECISE = [b[0] for b in BLOCKS] + [l[0] for l in LONE]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("T,E,k,H,I", PRECISE)
+def test_h_of_an_fp32_result(T, E, k, H, I, mx4):
+    """An fp32 y has 24 bits of h.  x has one value a token and w2 one +-1 a row, so
+    both products are exact: h is off by 10 u of SwiGLU and u of prob, its three parts
+    by u (2^-24), their sum by 2 u, the choices' by k u of the magnitudes; then the
+    rounding of y is in these.  (Two parts alone are off by up to 256 u.)"""
+    s = case(T, E, k, H, I, mx4, seed=200 + T + H)
+    g = torch.Generator().manual_seed(9)
+    s["x"].zero_()
+    s["x"][torch.arange(T), torch.randint(0, H, (T,), generator=g)] = (3 * torch.randn(T, generator=g)).bfloat16()
+    if mx4:
+        s["w1"], s["sf1"] = mx.random_mx4(g, (E, 2 * I, H), 125, 127)
+    else:
+        s["w1"] = torch.randn(E, 2 * I, H, generator=g).bfloat16()
+    w2 = torch.zeros(E, H, I)
+    at = (torch.arange(H) * 7 % I).expand(E, H) + 3 * torch.arange(E)[:, None]
+    w2.scatter_(2, (at % I)[:, :, None], torch.where(torch.rand(E, H, 1, generator=g) < 0.5, -1.0, 1.0))
+    if mx4:
+        code = torch.where(w2 == 0, 0, torch.where(w2 > 0, 2, 10)).to(torch.uint8).reshape(E, H, I // 2, 2)
+        s["w2"] = code[..., 0] | code[..., 1] << 4
+        s["sf2"] = torch.full((E, H, I // 32), 127, dtype=torch.uint8)
+    else:
+        s["w2"] = w2.bfloat16()
+    say("moe_few precise", T, E, k, H, I, mx4)
+    got = run(s)
+    y, mag = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            e = int(s["ids"][t, j])
+            c = (weights(s, "w1", "sf1", e) @ s["x"][t].double()).reshape(I // 32, 2, 32)
+            h = float(s["prob"][t, j]) * act64(c[:, 0].reshape(I), c[:, 1].reshape(I), B.GG_DSWIGLU)
+            term = w2[e].double() @ h
+            y[t] += term
+            mag[t] += term.abs()
+    tol = (14 + k) * U * mag + 2.0 ** -120
+    err = (got.double() - y).abs()
+    say(f"  {float((err / tol).max()):.3f} of the tolerance")
+    assert (err <= tol).all(), float((err / tol).max())
