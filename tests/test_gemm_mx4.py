@@ -306,3 +306,96 @@ def test_rows_by_the_billion(rows):
     for at in range(2, rows, 1 << 24):                       # rows of zeros between the picked ones
         if not bool((pick >= at).logical_and(pick < at + 64).any()):
             assert not d[at:at + 64].any()
+
+
+# --------------------------------------------------------------------------
+# long reduction axes: scale buffers that are used again
+# --------------------------------------------------------------------------
+
+def logged(s, tile, capfd, monkeypatch, *args, **kw):
+    """run(), whose report names the tile."""
+    capfd.readouterr()
+    monkeypatch.setenv("GG_LOG", "1")
+    out = run(s, *args, **kw)
+    monkeypatch.setenv("GG_LOG", "0")
+    err = capfd.readouterr().err
+    assert f"tile {tile}," in err and ("thin_kernel" in err) == tile.endswith("x32"), err
+    return out
+
+
+# The tiles' scales come in groups of 1024 values, in two buffers in turn, the thin
+# kernel's 4096 values at a time for each of four waves.  Odd numbers of stages of 128
+# among them, parts of a tile.
+LONG = [("256x256", [2500, 1000], 4096, 4064), ("256x256", [2500, 1000], 3968, 4064),
+        ("256x256", [1700, 1999], 2176, 4064), ("256x256", [1700, 1999], 8320, 3872),
+        ("128x128", [700] * 4, 4096, 1216), ("128x128", [700] * 4, 3968, 1216),
+        ("128x128", [130, 513, 0, 90] * 3, 2176, 1056), ("32x32", [16], 20480, 64), ("16x32", [5, 0, 30], 20608, 96),
+        ("32x32", [40, 9], 20608, 96), ("32x32", [100], 16896, 160)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile,sizes,K,N", LONG, ids=lambda v: str(v)[:24].replace(" ", ""))
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_long_reductions(tile, sizes, K, N, dtype, monkeypatch, capfd):
+    """Exact: products are multiples of 2^-4, and their magnitudes (with the bias,
+    all before alpha) add up to less than 2^20, which is checked."""
+    i = LONG.index((tile, sizes, K, N))
+    say("gemm_mx4 long", tile, sizes[:4], K, N, dtype)
+    s = case(sizes, K, N, seed=40 + i, tail=(0, 7)[i % 2], bias=i % 2 == 0)
+    a = mx.values(s["a"], s["sfa"]).cuda()
+    b = [mx.values(x, y).cuda() for x, y in zip(s["b"], s["sfb"])]
+    down = 1.0
+    if dtype == torch.float16:                               # (within fp16's range)
+        down = 2.0 ** -8
+        s["sfb"] = s["sfb"] - 8
+        if s["bias"] is not None:
+            s["bias"] = s["bias"] * down
+    d, err = logged(s, tile, capfd, monkeypatch, dtype, ptrs=i % 3 == 1)
+    assert err == 0
+    at = 0
+    for e, end in enumerate(s["ends"].tolist()):
+        al, bias = float(s["alpha"][e]) * down, 0.0
+        if s["bias"] is not None:
+            bias = s["bias"][e].double().cuda() / al
+        w = a[at:end] @ b[e].T + bias
+        if end > at:
+            mag = a[at:end].abs() @ b[e].abs().T + (bias.abs() if s["bias"] is not None else 0)
+            assert float(mag.max()) < 2.0 ** 20
+        assert torch.equal(d[at:end].double(), (al * w).float().to(dtype).double().cpu())
+        at = end
+    assert (d[at:] == 77.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile,sizes,N", [("128x128", [300, 127, 129], 1568), ("256x256", [2500, 1000], 4064),
+                                          ("16x32", [3, 0, 20], 96), ("32x32", [40, 9, 30], 96)],
+                         ids=lambda v: str(v).replace(" ", ""))
+def test_flags_of_the_ends_alone(tile, sizes, N, monkeypatch, capfd):
+    """The error word of each tile's kernel has the flag of what is wrong, no other."""
+    s = case(sizes, 384, N, seed=4, tail=9)
+    m, last = s["m"], sum(sizes)
+    for ends, flag in [(s["ends"].tolist(), 0), ([sizes[0], sizes[0] - 1] + [last] * (len(sizes) - 2), 1),
+                       ([-1] + [last] * (len(sizes) - 1), 1), ([sizes[0]] + [m + 1] * (len(sizes) - 1), 4),
+                       ([m + 1, -5] + [m] * (len(sizes) - 2), 5), ([0] * len(sizes), 0), ([m] * len(sizes), 0)]:
+        _, err = logged(s, tile, capfd, monkeypatch, ends=torch.tensor(ends, dtype=torch.int32))
+        assert err == flag, (ends, err)
+
+
+@pytest.mark.gpu
+def test_thin_past_4_gib(monkeypatch, capfd):
+    """The thin kernel on weights past 2^32 bytes, their scales past 2^28.  Exact:
+    products are multiples of 2^-6, their magnitudes add up to less than 2^18."""
+    K, N, L, rows = (1 << 18) + (1 << 13), 32, 1024, 5
+    g = torch.Generator().manual_seed(0)
+    a, sfa = mx.random_mx4(g, (rows, K), 125, 126)
+    bc, bs = mx.random_mx4(g, (N, K), 125, 126)
+    b = torch.zeros(L, N, K // 2, dtype=torch.uint8, device="cuda")
+    sfb = torch.full((L, N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    b[-1], sfb[-1] = bc.cuda(), bs.cuda()
+    ends = torch.zeros(L, dtype=torch.int32)
+    ends[-1] = rows
+    s = dict(m=rows, N=N, ends=ends, a=a, sfa=sfa, b=b, sfb=sfb, alpha=None, bias=None)
+    d, err = logged(s, "16x32", capfd, monkeypatch)
+    w, x = mx.values(a, sfa), mx.values(bc, bs)
+    assert err == 0 and b.numel() > 2 ** 32 and float((w.abs() @ x.abs().T).max()) < 2.0 ** 18
+    assert torch.equal(d.double(), w @ x.T)
