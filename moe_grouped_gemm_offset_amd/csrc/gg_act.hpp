@@ -45,7 +45,7 @@ void for_act(int act, F f) {
 
 // ---- rows as a run of eights -------------------------------------------------
 // Kernels over (rows, width) elements take eight elements of a row a lane (width
-// is a multiple of 8), kUnroll of them at a time (65536 rows of 4096 in bf16, one, two
+// is a multiple of 32), kUnroll of them at a time (65536 rows of 4096 in bf16, one, two
 // and four at a time: to MXFP4 117, 113 and 113 us, back 114, 97 and 100; the
 // activation to 2048 columns 130, 132 and 138), the block's threads side by side: eight v of the
 // matrix is row v / per_row.  The division goes by the block's first eight (a 64-bit
@@ -57,17 +57,17 @@ constexpr int kRowStep = kRowThreads * kUnroll;
 
 struct Eights {
     int64_t rows;
-    uint32_t per_row;         // eights of a row, at most 2^17
+    uint32_t per_row;         // eights of a row, 4 .. 2^17
     uint32_t magic;           // floor(2^32 / per_row) + 1
-    uint64_t magic64;         // floor(2^64 / per_row) + 1 (0: per_row is 1)
+    uint64_t magic64;         // floor(2^64 / per_row) + 1
 };
 
 inline Eights eights_of(int64_t rows, int width) {
     Eights e;
     e.rows = rows;
     e.per_row = (uint32_t)(width / 8);
-    e.magic = e.per_row > 1 ? (uint32_t)((1ull << 32) / e.per_row + 1) : 0;
-    e.magic64 = e.per_row > 1 ? (uint64_t)(((unsigned __int128)1 << 64) / e.per_row + 1) : 0;
+    e.magic = (uint32_t)((1ull << 32) / e.per_row + 1);
+    e.magic64 = (uint64_t)(((unsigned __int128)1 << 64) / e.per_row + 1);
     return e;
 }
 
@@ -102,7 +102,7 @@ __device__ __forceinline__ void for_eights(const Eights& e, int64_t ld, const in
         int64_t row0 = 0;
         uint32_t at0 = 0;
         if constexpr (!FLAT) {
-            row0 = e.magic64 ? (int64_t)__umul64hi((uint64_t)base, e.magic64) : base;
+            row0 = (int64_t)__umul64hi((uint64_t)base, e.magic64);
             at0 = (uint32_t)(base - row0 * e.per_row);
         }
         Run r;
@@ -117,8 +117,7 @@ __device__ __forceinline__ void for_eights(const Eights& e, int64_t ld, const in
             } else {
                 // (at < 2 per_row from kRowStep on, at < 2 kRowStep below)
                 const uint32_t at = at0 + j;
-                const uint32_t over = e.per_row >= kRowStep ? (at >= e.per_row ? 1u : 0u)
-                                    : e.magic ? __umulhi(at, e.magic) : at;
+                const uint32_t over = e.per_row >= kRowStep ? (at >= e.per_row ? 1u : 0u) : __umulhi(at, e.magic);
                 r.row[u] = row0 + over;
                 r.col[u] = (at - over * e.per_row) * 8;
                 r.at[u] = r.row[u] * ld + r.col[u];
