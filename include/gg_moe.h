@@ -785,7 +785,8 @@ gg_status gg_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t ro
  *   GG_DGEGLU    y = prob gc sigmoid(geglu_alpha gc) (uc + linear_offset),
  *                gc = min(g, clamp_max), uc = clamp(u, clamp_min, clamp_max)
  *   GG_DSITUGLU  y = prob b1 tanh(g/b1) sigmoid(g) b2 tanh(u/b2)
- * fp32 arithmetic, rounded once.  A NaN gate or input gives NaN.
+ * fp32 arithmetic, rounded once; a sigmoid below 2^-126 may count as 0.  A NaN
+ * gate or input gives NaN.
  *
  * c          (rows, 2n), GG_BF16, GG_F16 or GG_F32, row pitch ldc >= 2n.
  * prob       float[rows], or NULL for 1.
@@ -855,9 +856,9 @@ size_t gg_moe_few_workspace_size(int32_t tokens, int32_t top_k, int32_t hidden, 
  * id outside 0 .. num_experts-1 is no choice (its prob is not used); a token
  * without any gives 0; an expert may be chosen twice by a token.  Products with
  * fp32 accumulation; h is held as the sum of two bf16 values (16 bits), for an
- * fp32 y of three (24 bits), and the choices are added up in fp32 in a fixed
- * order, so equal calls give equal bits.  Only the chosen experts' weights are
- * read.
+ * fp32 y of three (24 bits; none finer than 2^-133), and the choices are added
+ * up in fp32 in a fixed order, so equal calls give equal bits.  Only the chosen
+ * experts' weights are read.
  *
  * x          (tokens, hidden) bf16, row pitch ldx >= hidden, a multiple of 8, at
  *            most 2^23.

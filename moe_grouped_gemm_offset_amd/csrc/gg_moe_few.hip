@@ -1,5 +1,9 @@
 // gg_moe_few.hip -- a whole mixture-of-experts layer for up to 64 tokens
-// (gg_moe_few): the layer costs what reading the chosen experts' weights costs.
+// (gg_moe_few): the layer costs what reading the chosen experts' weights costs, as
+// long as a block has columns for all choices of its expert.  It has 4 to 32, shared by
+// the parts of h in the second pass; more choices take another pass over the weights
+// (60 tokens, 7 of 8 experts of 5024 x 2304 in bf16, fp32 y, some 52 choices an expert:
+// 2 passes and 6, 408 us for the 85 of reading them once).
 //
 //   first    c = w1_e x, h = prob act(c + bias1), for every (token, choice)
 //   second   w2_e h + prob bias2, for every (token, choice)
@@ -23,7 +27,10 @@
 // wave takes rows of one choice's expert, with its columns in LDS of its own, so
 // none waits for another on the way, and a token's choices meet in one block of
 // the second pass, which leaves no third.  One token over 64 experts of 4096 x
-// 2048, 8 choices, weights from memory: MXFP4 49 us for 54, bf16 127 for 140.
+// 2048, 8 choices, weights from memory: MXFP4 49 us for 54, bf16 127 for 140.  (From
+// memory, here and below: after 256 MB were overwritten, which are written back under
+// the weights' loads.  Without that, other experts at each call, 855 MB in turn: 28 and
+// 72 us.)
 //
 // What a CU's load path takes is lines: a vector load of 8 rows x 128 bytes
 // costs half of one of 16 rows x 64 bytes.  So 16 bf16 rows x 128 bytes come in
